@@ -34,7 +34,8 @@
  *    step zero_offload_step, which waits for its own copies and host updates.
  *    zero_layout_*, zero_commit_rule and zero_host_adam are host-only and
  *    synchronous.
- *  - Device buffers must be 16-byte aligned (dwordx4 access).
+ *  - Device buffers must be 16-byte aligned (dwordx4 access), except those of the
+ *    stage-3 fetch, which need their element's alignment.
  */
 #ifndef ZERO_SHARD_STEP_H
 #define ZERO_SHARD_STEP_H

@@ -6,8 +6,10 @@ the gathered parameter buffer.
 
 The compute lives in ``libzero.so`` (hand-written HIP for gfx950 behind a C ABI,
 ``include/zero.h``); this package is its ctypes binding (same function names)
-plus ``ShardStep``, which owns buffers and applies the commit rule. There is no
-CPU fallback: without the built library every call raises.
+plus ``ShardStep``, which owns buffers and applies the commit rule. ``layer``
+holds the operators of a linear layer between the fetch of its tensors and the
+step: its products, its gradients into the flat gradient buffer, and dropout.
+There is no CPU fallback: without the built library every call raises.
 """
 from ._binding import (  # noqa: F401
     ZERO_BF16, ZERO_BF16_WIRE, ZERO_COMMIT, ZERO_F32, ZERO_MAX_REPLICAS, ZERO_SKIP, ZeroError, lib,
@@ -25,3 +27,9 @@ from ._binding import (  # noqa: F401
     ZeroRecordError, ZERO_RECORD_OK, ZERO_RECORD_E_COLLECT, ZERO_RECORD_E_MARKS,
     zero_adam_step_noalloc, ZERO_NOALLOC_SCRATCH_BYTES)
 from .shard_step import DeviceShardStep, OffloadShardStep, ShardStep  # noqa: F401
+from .layer import (  # noqa: F401
+    ZERO_ACT_GELU, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, ZERO_LINEAR_FORWARD, ZERO_LINEAR_GRAD_INPUT,
+    ZERO_LINEAR_GRAD_WEIGHT, ZERO_W_IN_OUT, ZERO_W_OUT_IN, FlatLinear, zero_dropout, zero_dropout_add,
+    zero_dropout_args, zero_dropout_grad, zero_linear_args, zero_linear_forward, zero_linear_grad_input,
+    zero_linear_grad_input_args, zero_linear_grad_weight, zero_linear_grad_weight_args,
+    zero_linear_workspace_bytes)

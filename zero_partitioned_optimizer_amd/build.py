@@ -4,12 +4,14 @@ from __future__ import annotations
 import os
 import shutil
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libzero.so")
-SOURCES = ["abi.cpp", "layout.cpp", "step_kernels.hip", "gather_kernels.hip"]
+SOURCES = ["abi.cpp", "layout.cpp", "step_kernels.hip", "gather_kernels.hip", "layer_abi.cpp",
+           "linear_kernels.hip", "dropout_kernels.hip"]
 # host-only C++ (no device pass), compiled to an object and linked in
 HOST_SOURCES = ["offload.cpp"]
 HOST_FLAGS = ["-x", "c++", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-c"]
@@ -36,19 +38,27 @@ def _run(cmd):
 
 
 def build(out: str = LIB, extra=()) -> str:
-    """Compile every source into ``out`` (always recompiles)."""
-    srcs = [os.path.join(CSRC, s) for s in SOURCES]
+    """Compile every source into ``out`` (always recompiles, a few sources at a time)."""
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    objs = []
-    for h in HOST_SOURCES:
-        obj = out + "." + os.path.splitext(h)[0] + ".o"
-        rocm = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(hipcc()) or hipcc())))
-        _run([hipcc(), *HOST_FLAGS, "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"),
-              *inc, os.path.join(CSRC, h), "-o", obj])
+    rocm = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(hipcc()) or hipcc())))
+    jobs, objs = [], []
+    for s in SOURCES + HOST_SOURCES:
+        obj = out + "." + os.path.splitext(s)[0] + ".o"
         objs.append(obj)
-    _run([hipcc(), *HIPCC_FLAGS, *extra, *inc, *srcs, "-x", "none", *objs, "-o", out + ".tmp"])
-    for obj in objs:
-        os.remove(obj)
+        if s in HOST_SOURCES:
+            jobs.append([hipcc(), *HOST_FLAGS, "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(rocm, "include"),
+                         *inc, os.path.join(CSRC, s), "-o", obj])
+        else:
+            flags = [f for f in HIPCC_FLAGS if f != "-shared"]
+            jobs.append([hipcc(), *flags, *extra, *inc, "-c", os.path.join(CSRC, s), "-o", obj])
+    try:
+        with ThreadPoolExecutor(max_workers=4) as pool:
+            list(pool.map(_run, jobs))
+        _run([hipcc(), "--offload-arch=gfx950", "-fPIC", "-shared", *objs, "-o", out + ".tmp"])
+    finally:
+        for obj in objs:
+            if os.path.exists(obj):
+                os.remove(obj)
     os.replace(out + ".tmp", out)
     return out
 

@@ -1,0 +1,77 @@
+// layer_internal.h -- internal interface between the C entry points of the layer
+// operators (layer_abi.cpp) and their gfx950 kernels (linear_kernels.hip,
+// dropout_kernels.hip). Not installed, not part of the ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "zero_layer.h"
+
+namespace zk {
+
+// Dropout as the kernels take it: element (i, j) is dropped when its 16-bit draw
+// is below thr, and kept elements are multiplied by scale; thr = 0 is no dropout.
+struct Drop {
+    uint32_t thr;
+    float scale;                    // 65536 / (65536 - thr), rounded once
+    uint32_t k0, k1;                // the seed's two halves: the generator's key
+    uint64_t offset;
+    const int64_t* counter;         // device, added to offset; may be nullptr
+};
+
+// One product C[p, q] = sum_r A(p, r) B(q, r) with an epilogue. An operand either
+// holds its outer index in rows (element (o, r) at o * ld + r) or, "reduced rows",
+// the reduction index in rows (element (o, r) at r * ld + o).
+enum Epilogue { kEpiForward = 0, kEpiGradInput = 1, kEpiGradWeight = 2 };
+
+struct ProductDesc {
+    const uint16_t* a;
+    const uint16_t* b;
+    int64_t lda, ldb;
+    bool ta, tb;                    // reduced rows
+    int64_t P, Q, R;
+    Epilogue epi;
+    void* out;                      // [P, Q], bf16 or f32
+    int64_t ld_out;
+    bool out_f32;
+    const uint16_t* bias;           // forward: [Q] or nullptr
+    const void* res;                // forward: the residual; weight gradient: the old values
+    int64_t ld_res;                 // (both of out's type), or nullptr
+    const uint16_t* z_in;           // gradient by input: pre-activation [P, Q] or nullptr
+    uint16_t* z_out;                // forward: pre-activation to store, or nullptr
+    int64_t ld_z;
+    int32_t act;
+    Drop drop;
+    float* ws;
+};
+
+// Workspace bytes that launch_product needs for a product of these sizes.
+size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R);
+hipError_t launch_product(const ProductDesc& d, hipStream_t st);
+
+// out[n] = (old ? old[n] : 0) + sum over the M rows of dz[m, n]; ws holds
+// colsum_ws_bytes(M, N) bytes.
+size_t colsum_ws_bytes(int64_t M, int64_t N);
+hipError_t launch_colsum(const uint16_t* dz, int64_t ld, int64_t M, int64_t N, void* out, bool out_f32,
+                         bool accumulate, float* ws, hipStream_t st);
+
+// Elementwise over [M, N]: y = res + D(x), or (grad) y = D'(x) * act'(z).
+struct DropoutDesc {
+    int64_t M, N;
+    const void* x;
+    int64_t ld_x;
+    bool x_f32;
+    const void* res;                // of y's type, or nullptr
+    int64_t ld_res;
+    const uint16_t* z;              // or nullptr
+    int64_t ld_z;
+    int32_t act;
+    void* y;
+    int64_t ld_y;
+    bool y_f32;
+    Drop drop;
+};
+hipError_t launch_dropout(const DropoutDesc& d, bool grad, hipStream_t st);
+
+}  // namespace zk
