@@ -431,3 +431,37 @@ def test_captured_calls_draw_anew(Z):
             assert torch.equal(a, b), (k, name)
         masks.append(y == 0)
     assert not torch.equal(masks[0], masks[1])
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,inner", [(4100, 136), (4096, 64), (4345, 191), (4097, 320)])
+def test_wide_outputs(Z, rows, inner, layout):
+    """Outputs of enough tiles to fill the chip (the largest tiles), with ragged edges
+    and reductions that are and are not whole tiles, in each direction."""
+    rng = np.random.default_rng(hash((14, rows, inner, layout)) % 2 ** 32)
+    cols = 4104
+    say("wide", rows, inner, layout)
+    x, w = inp(rng, rows, inner, pad_ld=-inner % 8), weight(rng, inner, cols, layout, (8, 0))
+    res = inp(rng, rows, cols)
+    y, z = Mat(rows, cols, BF, ld=cols + 8), Mat(rows, cols, BF, ld=cols + 16)
+    Z.zero_linear_forward(x.t, w.t, w_layout=layout, act=2, dropout=Z.zero_dropout(0.2, 1, 2), residual=res.t, y=y.t,
+                          preact=z.t)
+    want, err, wz, ez = R.linear_forward(x.f64(), w64(w, layout), act_name="gelu", p=0.2, seed=1, offset=2,
+                                         residual=res.f64())
+    close("y", y.t, want, err)
+    close("z", z.t, wz, ez)
+    assert y.intact_outside() and z.intact_outside()
+    dz, w = inp(rng, rows, inner, pad_ld=-inner % 8), weight(rng, cols, inner, layout, (-inner % 8, 0))
+    dx = Mat(rows, cols, F32, ld=cols + 8)
+    Z.zero_linear_grad_input(dz.t, w.t, w_layout=layout, act=3, preact=res.t, dx=dx.t)
+    want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="silu", z=res.f64(), out="f32")
+    close("dx", dx.t, want, err)
+    assert dx.intact_outside()
+    dz, x = inp(rng, inner, rows, pad_ld=-rows % 8), inp(rng, inner, cols)
+    r, c = (rows, cols) if layout == 0 else (cols, rows)
+    dw = Mat(r, c, F32, ld=c + 8, fill=rand(rng, r, c))
+    old = w64(dw, layout)
+    Z.zero_linear_grad_weight(dz.t, x.t, dw.t, w_layout=layout, accumulate=True)
+    want, err = R.linear_grad_weight(dz.f64(), x.f64(), old=old, out="f32")
+    close("dw", dw.t if layout == 0 else dw.t.t(), want, err)
+    assert dw.intact_outside()

@@ -46,8 +46,41 @@ __device__ __forceinline__ v4u chunk_load(const uint16_t* p, int n) {
     return w;
 }
 
-// One tile of an operand through registers into LDS; what lies outside the
-// operand becomes 0, so lengths, strides and alignment are arbitrary.
+// Chunk `id` of an operand's tile: what lies outside the operand becomes 0, so
+// lengths, strides and alignment are arbitrary.
+template <int ROWS, bool T>
+__device__ __forceinline__ v4u tile_chunk(int id, const uint16_t* src, int64_t ld, int64_t o0, int64_t O,
+                                          int64_t r0, int64_t r1) {
+    int64_t row, col, n;
+    bool in;
+    if constexpr (T) {
+        row = r0 + id / (ROWS / 8);
+        col = o0 + 8 * (id % (ROWS / 8));
+        in = row < r1;
+        n = O - col;
+    } else {
+        row = o0 + id / (kBR / 8);
+        col = r0 + 8 * (id % (kBR / 8));
+        in = row < O;
+        n = r1 - col;
+    }
+    return in && n > 0 ? chunk_load(src + row * ld + col, n < 8 ? (int)n : 8) : v4u{0, 0, 0, 0};
+}
+template <int ROWS, bool T>
+__device__ __forceinline__ void put_chunk(uint16_t* lds, int id, v4u w) {
+    int at;
+    if constexpr (T) {
+        const int r = id / (ROWS / 8), c = id % (ROWS / 8);
+        at = r * ROWS + 8 * (c ^ perm_reduced<ROWS>(r));
+    } else {
+        const int o = id / (kBR / 8), c = id % (kBR / 8);
+        at = o * kBR + 8 * (c ^ (o & 7));
+    }
+    *reinterpret_cast<v4u*>(lds + at) = w;
+}
+
+// A tile through registers into LDS: all of a thread's chunks loaded, then stored
+// (Stage), or one at a time where registers are short (stage_tail).
 template <int ROWS, bool T, int THREADS>
 struct Stage {
     static constexpr int kChunks = ROWS * kBR / 8 / THREADS;
@@ -55,41 +88,21 @@ struct Stage {
     __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0,
                                          int64_t r1) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int id = threadIdx.x + i * THREADS;
-            int64_t row, col, n;
-            bool in;
-            if constexpr (T) {
-                row = r0 + id / (ROWS / 8);
-                col = o0 + 8 * (id % (ROWS / 8));
-                in = row < r1;
-                n = O - col;
-            } else {
-                row = o0 + id / (kBR / 8);
-                col = r0 + 8 * (id % (kBR / 8));
-                in = row < O;
-                n = r1 - col;
-            }
-            n = in ? (n < 0 ? 0 : n > 8 ? 8 : n) : 0;
-            w[i] = n > 0 ? chunk_load(src + row * ld + col, (int)n) : v4u{0, 0, 0, 0};
-        }
+        for (int i = 0; i < kChunks; ++i)
+            w[i] = tile_chunk<ROWS, T>(threadIdx.x + i * THREADS, src, ld, o0, O, r0, r1);
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int id = threadIdx.x + i * THREADS;
-            int at;
-            if constexpr (T) {
-                const int r = id / (ROWS / 8), c = id % (ROWS / 8);
-                at = r * ROWS + 8 * (c ^ perm_reduced<ROWS>(r));
-            } else {
-                const int o = id / (kBR / 8), c = id % (kBR / 8);
-                at = o * kBR + 8 * (c ^ (o & 7));
-            }
-            *reinterpret_cast<v4u*>(lds + at) = w[i];
-        }
+        for (int i = 0; i < kChunks; ++i) put_chunk<ROWS, T>(lds, threadIdx.x + i * THREADS, w[i]);
     }
 };
+template <int ROWS, bool T, int THREADS>
+__device__ __forceinline__ void stage_tail(uint16_t* lds, const uint16_t* src, int64_t ld, int64_t o0, int64_t O,
+                                           int64_t r0, int64_t r1) {
+#pragma unroll 1
+    for (int id = threadIdx.x; id < ROWS * kBR / 8; id += THREADS)
+        put_chunk<ROWS, T>(lds, id, tile_chunk<ROWS, T>(id, src, ld, o0, O, r0, r1));
+}
 
 // The matrix instruction's operand for 16 outer indices from o0 and reduction
 // elements 32 * s .. 32 * s + 31 of a staged tile: lane l holds outer index
@@ -145,15 +158,80 @@ __device__ __forceinline__ void epilogue8(const ProductDesc& d, uint64_t off, in
     else store8_bf(static_cast<uint16_t*>(d.out) + p * d.ld_out + q, v, n);
 }
 
+typedef int v4i __attribute__((ext_vector_type(4)));
+
+// 16 bytes a lane from the buffer's byte `at` to LDS, lane l of the wave to byte
+// 16 l behind `to` (the same in all lanes). Written in assembly because the
+// compiler, which sees in its own builtin a store to LDS of unknown extent, waits
+// for it before the next LDS read of any tile. It has no output register; what
+// reads the tile waits with loads_landed first.
+__device__ __forceinline__ void lds_load(v4i rsrc, uint32_t at, const uint16_t* to) {
+    const uint32_t m0 = __builtin_amdgcn_readfirstlane(
+        (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)to));
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(m0), "v"(at), "s"(rsrc)
+                 : "memory");
+}
+// Until at most N of this wave's loads are under way.
+template <int N>
+__device__ __forceinline__ void loads_landed() {
+    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+// All waves have come here and their LDS reads and writes are done.
+__device__ __forceinline__ void meet_waves() {
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+}
+
+// One operand's tiles from memory straight into LDS: 16 bytes a lane, lane l of a
+// wave to byte 16 l behind the wave's LDS address, so the chunk permutation is
+// applied to the address that a lane reads. Rows and chunks outside the operand
+// read its last ones instead: they only reach outputs that do not exist. Used
+// where rows start on 16 bytes and a whole tile of the reduction is left.
+template <int ROWS, bool T, int THREADS>
+struct Direct {
+    static constexpr int kLoads = ROWS * kBR / 8 / THREADS;
+    uint32_t at[kLoads];            // byte offsets from `base`
+    const char* base;
+    int64_t step;
+    __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int id = threadIdx.x + i * THREADS;
+            if constexpr (T) {
+                const int r = id / (ROWS / 8);
+                int64_t c = 8 * ((id % (ROWS / 8)) ^ perm_reduced<ROWS>(r));
+                if (o0 + c >= O) c = (O - 1 - o0) & ~int64_t(7);
+                at[i] = (uint32_t)((r * ld + c) * 2);
+            } else {
+                int64_t o = id / (kBR / 8);
+                const int c = 8 * ((id % (kBR / 8)) ^ (int)(o & 7));
+                if (o0 + o >= O) o = O - 1 - o0;
+                at[i] = (uint32_t)((o * ld + c) * 2);
+            }
+        }
+        base = reinterpret_cast<const char*>(src + (T ? r0 * ld + o0 : o0 * ld + r0));
+        step = (T ? kBR * ld : kBR) * 2;
+    }
+    __device__ __forceinline__ void issue(uint16_t* lds) {
+        const v4i rsrc = {(int)(uint32_t)reinterpret_cast<uintptr_t>(base),
+                          (int)(uint32_t)(reinterpret_cast<uintptr_t>(base) >> 32), -1, 0x00020000};
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) lds_load(rsrc, at[i], lds + 8 * (i * THREADS + (threadIdx.x & ~63)));
+        base += step;
+    }
+};
+
 // NWP x NWQ waves, each with FP x FQ blocks of 16 x 16 outputs. The blocks are
 // computed as (q, p), so a lane holds four consecutive columns of one output row;
-// exchanging the odd 16-lane rows of one block with the even ones of the next
-// column block gives every lane eight.
-template <int NWP, int NWQ, int FP, int FQ, bool TA, bool TB, int EPI>
+// and so 16 bytes of the tile that the epilogue takes through LDS.
+template <int NWP, int NWQ, int FP, int FQ, bool TA, bool TB, int EPI, bool DIRECT>
 __global__ void __launch_bounds__(64 * NWP * NWQ) k_product(const ProductArgs g) {
     constexpr int T = 64 * NWP * NWQ, BP = 16 * FP * NWP, BQ = 16 * FQ * NWQ;
-    __shared__ __attribute__((aligned(16))) uint16_t la[BP * kBR];
-    __shared__ __attribute__((aligned(16))) uint16_t lb[BQ * kBR];
+    constexpr int kBufs = DIRECT ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[kBufs * (BP + BQ) * kBR];
+    const auto la = [&](int k) { return lds + k * (BP + BQ) * kBR; };
+    const auto lb = [&](int k) { return lds + k * (BP + BQ) * kBR + BP * kBR; };
     const ProductDesc& d = g.d;
     const int64_t tq = (d.Q + BQ - 1) / BQ;
     const int64_t p0 = (int64_t)(blockIdx.x / tq) * BP, q0 = (int64_t)(blockIdx.x % tq) * BQ;
@@ -168,52 +246,96 @@ __global__ void __launch_bounds__(64 * NWP * NWQ) k_product(const ProductArgs g)
 #pragma unroll
         for (int j = 0; j < FQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
 
-    Stage<BP, TA, T> sa;
-    Stage<BQ, TB, T> sb;
-    if (r0 < r1) {
-        sa.load(d.a, d.lda, p0, d.P, r0, r1);
-        sb.load(d.b, d.ldb, q0, d.Q, r0, r1);
-    }
-    for (int64_t r = r0; r < r1; r += kBR) {
-        __syncthreads();
-        sa.store(la);
-        sb.store(lb);
-        __syncthreads();
-        if (r + kBR < r1) {
-            sa.load(d.a, d.lda, p0, d.P, r + kBR, r1);
-            sb.load(d.b, d.ldb, q0, d.Q, r + kBR, r1);
-        }
+    const auto multiply = [&](const uint16_t* ta, const uint16_t* tb) {
 #pragma unroll
         for (int s = 0; s < kBR / 32; ++s) {
             v8bf fa[FP], fb[FQ];
 #pragma unroll
-            for (int i = 0; i < FP; ++i) fa[i] = fragment<BP, TA>(la, wp + 16 * i, s);
+            for (int i = 0; i < FP; ++i) fa[i] = fragment<BP, TA>(ta, wp + 16 * i, s);
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) fb[j] = fragment<BQ, TB>(lb, wq + 16 * j, s);
+            for (int j = 0; j < FQ; ++j) fb[j] = fragment<BQ, TB>(tb, wq + 16 * j, s);
 #pragma unroll
             for (int i = 0; i < FP; ++i)
 #pragma unroll
                 for (int j = 0; j < FQ; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
         }
+    };
+
+    if constexpr (DIRECT) {
+        const int full = (int)((r1 - r0) / kBR);
+        Direct<BP, TA, T> da;
+        Direct<BQ, TB, T> db;
+        if (full > 0) {
+            da.init(d.a, d.lda, p0, d.P, r0);
+            db.init(d.b, d.ldb, q0, d.Q, r0);
+            da.issue(la(0));
+            db.issue(lb(0));
+        }
+        for (int k = 0; k < full; ++k) {
+            loads_landed<0>();
+            meet_waves();
+            if (k + 1 < full) {
+                da.issue(la((k + 1) & 1));
+                db.issue(lb((k + 1) & 1));
+            }
+            multiply(la(k & 1), lb(k & 1));
+        }
+        if (r0 + (int64_t)full * kBR < r1) {
+            const int64_t r = r0 + (int64_t)full * kBR;
+            stage_tail<BP, TA, T>(la(full & 1), d.a, d.lda, p0, d.P, r, r1);
+            stage_tail<BQ, TB, T>(lb(full & 1), d.b, d.ldb, q0, d.Q, r, r1);
+            __syncthreads();
+            multiply(la(full & 1), lb(full & 1));
+        }
+    } else {
+        Stage<BP, TA, T> sa;
+        Stage<BQ, TB, T> sb;
+        if (r0 < r1) {
+            sa.load(d.a, d.lda, p0, d.P, r0, r1);
+            sb.load(d.b, d.ldb, q0, d.Q, r0, r1);
+        }
+        for (int64_t r = r0; r < r1; r += kBR) {
+            __syncthreads();
+            sa.store(la(0));
+            sb.store(lb(0));
+            __syncthreads();
+            if (r + kBR < r1) {
+                sa.load(d.a, d.lda, p0, d.P, r + kBR, r1);
+                sb.load(d.b, d.ldb, q0, d.Q, r + kBR, r1);
+            }
+            multiply(la(0), lb(0));
+        }
     }
 
-    const int gr = lane >> 4;
+    // Epilogue through LDS, a run of kRows of each wave's rows at a time, so that a
+    // lane gets eight consecutive columns and a wave stores whole 128-byte lines.
+    // Each wave has its own part: 16-byte units, unit u of row o at u ^ (o & 15).
+    constexpr int kCols = 16 * FQ;
+    constexpr int kFit = (int)(sizeof(lds) / sizeof(float)) / (NWP * NWQ * kCols) / 16 * 16;
+    constexpr int kRows = kFit < 16 * FP ? kFit : 16 * FP, kRun = kRows / 16;
+    static_assert(kRun >= 1 && FP % kRun == 0, "the runs cover a wave's rows");
+    static_assert(kCols % 64 == 0, "units are permuted within 64 columns");
     const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
+    float* const mine = reinterpret_cast<float*>(lds) + wave * kRows * kCols;
+    meet_waves();
 #pragma unroll
-    for (int i = 0; i < FP; ++i) {
-        const int64_t p = p0 + wp + 16 * i + (lane & 15);
+    for (int i0 = 0; i0 < FP; i0 += kRun) {
 #pragma unroll
-        for (int j = 0; j < FQ; j += 2) {
-            float v[8];
+        for (int i = 0; i < kRun; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][e]),
-                                                                __float_as_uint(acc[i][j + 1][e]), false, false);
-                v[e] = __uint_as_float(x[0]);
-                v[4 + e] = __uint_as_float(x[1]);
+            for (int j = 0; j < FQ; ++j) {
+                const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
+                *reinterpret_cast<v4f*>(mine + o * kCols + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
             }
-            const int64_t q = q0 + wq + 16 * (j + (gr & 1)) + 8 * (gr >> 1);
+        constexpr int kGroups = kCols / 8;
+#pragma unroll 1
+        for (int at = lane; at < kRows * kGroups; at += 64) {
+            const int o = at / kGroups, c = at % kGroups;
+            const v4f lo = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c) ^ (o & 15)));
+            const v4f hi = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c + 1) ^ (o & 15)));
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            const int64_t p = p0 + wp + 16 * i0 + o, q = q0 + wq + 8 * c;
             if (p >= d.P || q >= d.Q) continue;
             const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
             if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
@@ -260,15 +382,30 @@ size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R) {
     return s.splits > 1 ? (size_t)s.splits * (size_t)P * (size_t)((Q + 7) / 8 * 8) * sizeof(float) : 0;
 }
 
+// Rows on 16 bytes, and a tile's rows within the 2 GiB that its offsets reach.
+static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
+    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld < (int64_t(1) << 21)));
+}
+
+template <int NWP, int NWQ, int FP, int FQ, bool TA, bool TB, int EPI, bool DIRECT>
+static hipError_t tiles_launch(const ProductArgs& g, hipStream_t st) {
+    constexpr int BP = 16 * FP * NWP, BQ = 16 * FQ * NWQ;
+    const int64_t tiles = ((g.d.P + BP - 1) / BP) * ((g.d.Q + BQ - 1) / BQ);
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    hipLaunchKernelGGL((k_product<NWP, NWQ, FP, FQ, TA, TB, EPI, DIRECT>), dim3((unsigned)tiles, (unsigned)g.splits),
+                       dim3(64 * NWP * NWQ), 0, st, g);
+    return hipGetLastError();
+}
+
 template <bool TA, bool TB, int EPI>
 static hipError_t product(ProductArgs& g, hipStream_t st) {
     const ProductDesc& d = g.d;
-    const int64_t tiles = ((d.P + 127) / 128) * ((d.Q + 127) / 128);
-    if (tiles <= 0) return hipSuccess;
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_product<2, 2, 4, 4, TA, TB, EPI>), dim3((unsigned)tiles, (unsigned)(g.splits < 1 ? 1 : g.splits)),
-                       dim3(256), 0, st, g);
-    hipError_t e = hipGetLastError();
+    if (d.P <= 0 || d.Q <= 0) return hipSuccess;
+    const bool direct = direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
+    const int64_t big = ((d.P + 255) / 256) * ((d.Q + 255) / 256);
+    hipError_t e = !direct ? tiles_launch<2, 2, 4, 4, TA, TB, EPI, false>(g, st)
+                   : big >= 256 ? tiles_launch<2, 4, 8, 4, TA, TB, EPI, true>(g, st)
+                                : tiles_launch<2, 2, 4, 4, TA, TB, EPI, true>(g, st);
     if (e != hipSuccess || !g.part) return e;
     const int64_t blocks = (d.P * (g.ld_part / 8) + 255) / 256;
     hipLaunchKernelGGL((k_join<EPI>), dim3((unsigned)blocks), dim3(256), 0, st, g);
