@@ -222,6 +222,22 @@ struct Direct {
     }
 };
 
+// The output tile of a workgroup. Workgroups go to the 8 XCDs in turn, each with an
+// L2 of its own, so each XCD gets a run of consecutive tiles; runs walk down blocks
+// of kTileRows rows of tiles, column by column, so that the 32 workgroups that an
+// XCD runs at a time share few operand rows.
+// (Llama-7B shaped products: 8 rows 5% faster than tiles in order, 4 or 16 rows 2%
+// behind 8 on the deepest reductions.)
+constexpr int kTileRows = 8;
+__device__ __forceinline__ void tile_of(int id, int tiles, int np, int nq, int* tp, int* tq) {
+    const int xcd = id & 7, slot = id >> 3, each = tiles >> 3, more = tiles & 7;
+    const int t = xcd * each + (xcd < more ? xcd : more) + slot;
+    const int block = t / (kTileRows * nq), in = t - block * kTileRows * nq;
+    const int rows = np - block * kTileRows < kTileRows ? np - block * kTileRows : kTileRows;
+    *tq = in / rows;
+    *tp = block * kTileRows + in - *tq * rows;
+}
+
 // NWP x NWQ waves, each with FP x FQ blocks of 16 x 16 outputs. The blocks are
 // computed as (q, p), so a lane holds four consecutive columns of one output row;
 // and so 16 bytes of the tile that the epilogue takes through LDS.
@@ -233,8 +249,9 @@ __global__ void __launch_bounds__(64 * NWP * NWQ) k_product(const ProductArgs g)
     const auto la = [&](int k) { return lds + k * (BP + BQ) * kBR; };
     const auto lb = [&](int k) { return lds + k * (BP + BQ) * kBR + BP * kBR; };
     const ProductDesc& d = g.d;
-    const int64_t tq = (d.Q + BQ - 1) / BQ;
-    const int64_t p0 = (int64_t)(blockIdx.x / tq) * BP, q0 = (int64_t)(blockIdx.x % tq) * BQ;
+    int tp, tq;
+    tile_of(blockIdx.x, gridDim.x, (int)((d.P + BP - 1) / BP), (int)((d.Q + BQ - 1) / BQ), &tp, &tq);
+    const int64_t p0 = (int64_t)tp * BP, q0 = (int64_t)tq * BQ;
     const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
