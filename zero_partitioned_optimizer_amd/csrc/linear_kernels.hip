@@ -23,8 +23,6 @@ struct ProductArgs {
     float* part;                    // [splits, P, ld_part], or nullptr: epilogue in place
 };
 
-typedef __attribute__((address_space(3))) uint16_t lds_u16;
-
 // Staged tiles hold eight-element chunks (16 bytes), permuted within a row so that
 // the lanes that read together meet different banks.
 //   outer rows:   [rows][kBR], chunk c of row o at c ^ (o & 7): the 8 lanes of a
@@ -104,24 +102,43 @@ __device__ __forceinline__ void stage_tail(uint16_t* lds, const uint16_t* src, i
         put_chunk<ROWS, T>(lds, id, tile_chunk<ROWS, T>(id, src, ld, o0, O, r0, r1));
 }
 
-// The matrix instruction's operand for 16 outer indices from o0 and reduction
-// elements 32 * s .. 32 * s + 31 of a staged tile: lane l holds outer index
-// o0 + (l & 15) and elements 8 * (l >> 4) .. + 7.
-template <int ROWS, bool T>
-__device__ __forceinline__ v8bf fragment(const uint16_t* lds, int o0, int s) {
-    const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-    if constexpr (T) {
-        const int r = 32 * s + 8 * g + (i >> 2), col = o0 + 4 * (i & 3);
-        const int at = r * ROWS + 8 * ((col >> 3) ^ perm_reduced<ROWS>(r)) + (col & 7);
-        typedef __attribute__((address_space(3))) v4bf lds_v4bf;
-        const v4bf lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)(lds + at));
-        const v4bf hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)(lds + at + 4 * ROWS));
-        return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-    } else {
-        const int o = o0 + i, c = 4 * s + g;
-        return *reinterpret_cast<const v8bf*>(lds + o * kBR + 8 * (c ^ (o & 7)));
-    }
+typedef __attribute__((address_space(3))) const uint16_t lds_u16;
+typedef __attribute__((address_space(3))) const v8bf lds_v8bf;
+typedef __attribute__((address_space(3))) v4bf lds_v4bf;
+__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
+    return (uint32_t)reinterpret_cast<uintptr_t>((lds_u16*)p);
 }
+
+// The matrix instruction's operands from a staged tile: for block i, lane l holds
+// outer index o0 + 16 i + (l & 15) and reduction elements 32 s + 8 (l >> 4) .. + 7.
+// o0 is a multiple of the outer indices that the wave's blocks cover, a power of
+// two, so one byte offset per lane serves all blocks: a constant is added to it,
+// or, where a block's chunks lie under the permutation, exchanged into it.
+template <int ROWS, bool T>
+struct Fragments {
+    uint32_t at;
+    __device__ __forceinline__ explicit Fragments(int o0) {
+        const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
+        if constexpr (T) {
+            const int r = 8 * g + (i >> 2), chunk = (o0 >> 3) + ((i & 3) >> 1);
+            at = 2 * (r * ROWS + 8 * (chunk ^ perm_reduced<ROWS>(r)) + 4 * (i & 1));
+        } else {
+            const int o = o0 + i;
+            at = 2 * (o * kBR + 8 * (g ^ (o & 7)));
+        }
+    }
+    __device__ __forceinline__ v8bf get(uint32_t tile, int i, int s) const {
+        if constexpr (T) {
+            // rows 32 further on have the same permutation
+            const uint32_t p = tile + (at ^ (32u * i)) + 2 * 32 * ROWS * s;
+            const v4bf lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)p);
+            const v4bf hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)(p + 2 * 4 * ROWS));
+            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
+        } else {
+            return *(lds_v8bf*)(tile + (at ^ (64u * s)) + 2 * 16 * kBR * i);
+        }
+    }
+};
 
 // The epilogue of eight consecutive columns q .. of row p; n of them exist.
 template <int EPI>
@@ -165,12 +182,10 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // compiler, which sees in its own builtin a store to LDS of unknown extent, waits
 // for it before the next LDS read of any tile. It has no output register; what
 // reads the tile waits with loads_landed first.
-__device__ __forceinline__ void lds_load(v4i rsrc, uint32_t at, const uint16_t* to) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(
-        (uint32_t)reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const void*)to));
+__device__ __forceinline__ void lds_load(v4i rsrc, uint32_t at, uint32_t to) {
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
-                 : "s"(m0), "v"(at), "s"(rsrc)
+                 : "s"(to), "v"(at), "s"(rsrc)
                  : "memory");
 }
 // Until at most N of this wave's loads are under way.
@@ -180,7 +195,9 @@ __device__ __forceinline__ void loads_landed() {
 }
 // All waves have come here and their LDS reads and writes are done.
 __device__ __forceinline__ void meet_waves() {
-    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
+    asm volatile("" : : : "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0), where the compiler counts it too
+    asm volatile("s_barrier" : : : "memory");
 }
 
 // One operand's tiles from memory straight into LDS: 16 bytes a lane, lane l of a
@@ -195,6 +212,7 @@ struct Direct {
     const char* base;
     int64_t step;
     __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0) {
+        if (o0 >= O) o0 = (O - 1) & ~int64_t(7);        // a half tile with nothing in it
 #pragma unroll
         for (int i = 0; i < kLoads; ++i) {
             const int id = threadIdx.x + i * THREADS;
@@ -213,11 +231,13 @@ struct Direct {
         base = reinterpret_cast<const char*>(src + (T ? r0 * ld + o0 : o0 * ld + r0));
         step = (T ? kBR * ld : kBR) * 2;
     }
-    __device__ __forceinline__ void issue(uint16_t* lds) {
+    // The tile's loads to LDS byte address `tile`; `wave` is the same in all lanes.
+    // With `records` 0 the buffer's range check stops them (they still count as loads).
+    __device__ __forceinline__ void issue(uint32_t tile, int wave, int records) {
         const v4i rsrc = {(int)(uint32_t)reinterpret_cast<uintptr_t>(base),
-                          (int)(uint32_t)(reinterpret_cast<uintptr_t>(base) >> 32), -1, 0x00020000};
+                          (int)(uint32_t)(reinterpret_cast<uintptr_t>(base) >> 32), records, 0x00020000};
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) lds_load(rsrc, at[i], lds + 8 * (i * THREADS + (threadIdx.x & ~63)));
+        for (int i = 0; i < kLoads; ++i) lds_load(rsrc, at[i], tile + 16 * (i * THREADS + 64 * wave));
         base += step;
     }
 };
@@ -238,39 +258,81 @@ __device__ __forceinline__ void tile_of(int id, int tiles, int np, int nq, int* 
     *tp = block * kTileRows + in - *tq * rows;
 }
 
-// NWP x NWQ waves, each with FP x FQ blocks of 16 x 16 outputs. The blocks are
-// computed as (q, p), so a lane holds four consecutive columns of one output row;
-// and so 16 bytes of the tile that the epilogue takes through LDS.
-template <int NWP, int NWQ, int FP, int FQ, bool TA, bool TB, int EPI, bool DIRECT>
-__global__ void __launch_bounds__(64 * NWP * NWQ) k_product(const ProductArgs g) {
-    constexpr int T = 64 * NWP * NWQ, BP = 16 * FP * NWP, BQ = 16 * FQ * NWQ;
+// The epilogue of a workgroup's tile, through LDS: kRun rows of a wave's blocks at a
+// time, so that a lane gets eight consecutive columns and stores 16 bytes or more.
+// Blocks are computed as (q, p), so a lane holds four consecutive columns of one
+// output row, one 16-byte unit. Each wave has its own part of LDS; unit u of row o
+// lies at u ^ (o & 15). row_of(i) and col_of(j): first row and column of the wave's
+// blocks (i, j) in the output; the rows of a run are consecutive.
+template <int EPI, int LDS_BYTES, int WAVES, int FP, int FQ, typename Row, typename Col>
+__device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP][FQ], uint16_t* lds, int wave,
+                                       Row row_of, Col col_of) {
+    static_assert(FQ == 4, "16 units a row");
+    constexpr int kFit = LDS_BYTES / (WAVES * 16 * 64 * 4), kRun = kFit >= 4 ? 4 : kFit;
+    static_assert(kRun >= 1 && FP % kRun == 0, "the runs cover a wave's rows");
+    const ProductDesc& d = g.d;
+    const int lane = threadIdx.x & 63;
+    const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
+    float* const mine = reinterpret_cast<float*>(lds) + wave * kRun * 16 * 64;
+#pragma unroll
+    for (int i0 = 0; i0 < FP; i0 += kRun) {
+#pragma unroll
+        for (int i = 0; i < kRun; ++i)
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) {
+                const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
+                *reinterpret_cast<v4f*>(mine + o * 64 + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
+            }
+        const int c = lane & 7;
+        const int64_t q = col_of(c >> 1) + 8 * (c & 1);
+#pragma unroll 1
+        for (int o = lane >> 3; o < 16 * kRun; o += 8) {
+            const v4f lo = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c) ^ (o & 15)));
+            const v4f hi = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c + 1) ^ (o & 15)));
+            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            const int64_t p = row_of(i0) + o;
+            if (p >= d.P || q >= d.Q) continue;
+            const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
+            if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
+            else epilogue8<EPI>(d, off, p, q, v, n);
+        }
+    }
+}
+
+// 128 x 128 outputs by four waves, 64 x 64 each (4 x 4 blocks), for outputs of few
+// tiles and, without DIRECT, for operands at any address: tiles of 64 reduction
+// elements, two in LDS, the next one loading while one is multiplied. Two
+// workgroups of 64 KB fit a compute unit and fill each other's waits.
+template <bool TA, bool TB, int EPI, bool DIRECT>
+__global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
+    constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
     constexpr int kBufs = DIRECT ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) uint16_t lds[kBufs * (BP + BQ) * kBR];
-    const auto la = [&](int k) { return lds + k * (BP + BQ) * kBR; };
-    const auto lb = [&](int k) { return lds + k * (BP + BQ) * kBR + BP * kBR; };
+    __shared__ __attribute__((aligned(16))) uint16_t lds[kBufs * 2 * kTile];
     const ProductDesc& d = g.d;
     int tp, tq;
-    tile_of(blockIdx.x, gridDim.x, (int)((d.P + BP - 1) / BP), (int)((d.Q + BQ - 1) / BQ), &tp, &tq);
-    const int64_t p0 = (int64_t)tp * BP, q0 = (int64_t)tq * BQ;
+    tile_of(blockIdx.x, gridDim.x, (int)((d.P + B - 1) / B), (int)((d.Q + B - 1) / B), &tp, &tq);
+    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
     const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int wp = (wave / NWQ) * 16 * FP, wq = (wave % NWQ) * 16 * FQ;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = (wave >> 1) * 64, wq = (wave & 1) * 64;
 
     v4f acc[FP][FQ];
 #pragma unroll
     for (int i = 0; i < FP; ++i)
 #pragma unroll
         for (int j = 0; j < FQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const auto multiply = [&](const uint16_t* ta, const uint16_t* tb) {
+    const Fragments<B, TA> ga(wp);
+    const Fragments<B, TB> gb(wq);
+    const uint32_t base = lds_address(lds);
+    const auto multiply = [&](uint32_t tile) {
 #pragma unroll
         for (int s = 0; s < kBR / 32; ++s) {
             v8bf fa[FP], fb[FQ];
 #pragma unroll
-            for (int i = 0; i < FP; ++i) fa[i] = fragment<BP, TA>(ta, wp + 16 * i, s);
+            for (int i = 0; i < FP; ++i) fa[i] = ga.get(tile, i, s);
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) fb[j] = fragment<BQ, TB>(tb, wq + 16 * j, s);
+            for (int j = 0; j < FQ; ++j) fb[j] = gb.get(tile + 2 * kTile, j, s);
 #pragma unroll
             for (int i = 0; i < FP; ++i)
 #pragma unroll
@@ -281,84 +343,202 @@ __global__ void __launch_bounds__(64 * NWP * NWQ) k_product(const ProductArgs g)
 
     if constexpr (DIRECT) {
         const int full = (int)((r1 - r0) / kBR);
-        Direct<BP, TA, T> da;
-        Direct<BQ, TB, T> db;
+        Direct<B, TA, T> da;
+        Direct<B, TB, T> db;
         if (full > 0) {
             da.init(d.a, d.lda, p0, d.P, r0);
             db.init(d.b, d.ldb, q0, d.Q, r0);
-            da.issue(la(0));
-            db.issue(lb(0));
+            da.issue(base, wave, -1);
+            db.issue(base + 2 * kTile, wave, -1);
         }
         for (int k = 0; k < full; ++k) {
             loads_landed<0>();
             meet_waves();
+            const uint32_t tile = base + 4 * kTile * (k & 1), next = base + 4 * kTile * ((k + 1) & 1);
             if (k + 1 < full) {
-                da.issue(la((k + 1) & 1));
-                db.issue(lb((k + 1) & 1));
+                da.issue(next, wave, -1);
+                db.issue(next + 2 * kTile, wave, -1);
             }
-            multiply(la(k & 1), lb(k & 1));
+            multiply(tile);
         }
         if (r0 + (int64_t)full * kBR < r1) {
+            // what is left of the reduction, with its end masked
             const int64_t r = r0 + (int64_t)full * kBR;
-            stage_tail<BP, TA, T>(la(full & 1), d.a, d.lda, p0, d.P, r, r1);
-            stage_tail<BQ, TB, T>(lb(full & 1), d.b, d.ldb, q0, d.Q, r, r1);
-            __syncthreads();
-            multiply(la(full & 1), lb(full & 1));
+            uint16_t* const to = lds + 2 * kTile * (full & 1);
+            stage_tail<B, TA, T>(to, d.a, d.lda, p0, d.P, r, r1);
+            stage_tail<B, TB, T>(to + kTile, d.b, d.ldb, q0, d.Q, r, r1);
+            meet_waves();
+            multiply(base + 4 * kTile * (full & 1));
         }
     } else {
-        Stage<BP, TA, T> sa;
-        Stage<BQ, TB, T> sb;
+        Stage<B, TA, T> sa;
+        Stage<B, TB, T> sb;
         if (r0 < r1) {
             sa.load(d.a, d.lda, p0, d.P, r0, r1);
             sb.load(d.b, d.ldb, q0, d.Q, r0, r1);
         }
         for (int64_t r = r0; r < r1; r += kBR) {
             __syncthreads();
-            sa.store(la(0));
-            sb.store(lb(0));
+            sa.store(lds);
+            sb.store(lds + kTile);
             __syncthreads();
             if (r + kBR < r1) {
                 sa.load(d.a, d.lda, p0, d.P, r + kBR, r1);
                 sb.load(d.b, d.ldb, q0, d.Q, r + kBR, r1);
             }
-            multiply(la(0), lb(0));
+            multiply(base);
         }
     }
-
-    // Epilogue through LDS, a run of kRows of each wave's rows at a time, so that a
-    // lane gets eight consecutive columns and a wave stores whole 128-byte lines.
-    // Each wave has its own part: 16-byte units, unit u of row o at u ^ (o & 15).
-    constexpr int kCols = 16 * FQ;
-    constexpr int kFit = (int)(sizeof(lds) / sizeof(float)) / (NWP * NWQ * kCols) / 16 * 16;
-    constexpr int kRows = kFit < 16 * FP ? kFit : 16 * FP, kRun = kRows / 16;
-    static_assert(kRun >= 1 && FP % kRun == 0, "the runs cover a wave's rows");
-    static_assert(kCols % 64 == 0, "units are permuted within 64 columns");
-    const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
-    float* const mine = reinterpret_cast<float*>(lds) + wave * kRows * kCols;
     meet_waves();
+    finish<EPI, sizeof(lds), 4>(g, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
+                                [&](int j) { return q0 + wq + 16 * j; });
+}
+
+// 256 x 256 outputs by eight waves, one workgroup to a compute unit. Operand tiles of
+// 64 reduction elements lie in LDS as halves of 128 outer indices, two tiles of four
+// halves. A wave's outputs are 64 x 32 of each quarter (half of A, half of B), so a
+// tile is four turns of 16 matrix instructions, and a turn has two parts that
+// barriers divide: the wave reads what its quarter needs and no turn before it read,
+// and asks for one half tile of the tiles to come; then it multiplies. Waves 4-7 are
+// one barrier behind waves 0-3, which share their SIMDs, so that one wave of each
+// pair multiplies while the other reads.
+//
+//   turn      reads            asks for           multiplies
+//   4k        A0(k), B0(k)     A1(k + 1)          A0 B0
+//   4k + 1    B1(k)            A0(k + 2)          A0 B1
+//   4k + 2    A1(k)            B0(k + 2)          A1 B1
+//   4k + 3    -                B1(k + 2)          A1 B0
+//
+// A half is read in one turn only, by all waves within the two barrier intervals that
+// begin with that turn of waves 0-3, and asked for again one turn later or more: after
+// them. What turn f reads was asked for in turn f - 6 or before, or in the prologue;
+// turn f - 1 waits until at most the five latest turns' loads are under way, and its
+// barrier comes before anyone's turn f. So a load has five turns to land.
+template <bool TA, bool TB, int EPI>
+__global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
+    constexpr int T = 512, B = 256, H = 128, kHalf = H * kBR;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 4 * kHalf];
+    const ProductDesc& d = g.d;
+    int tp, tq;
+    tile_of(blockIdx.x, gridDim.x, (int)((d.P + B - 1) / B), (int)((d.Q + B - 1) / B), &tp, &tq);
+    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
+    const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = (wave >> 2) * 64, wq = (wave & 3) * 32;
+
+    // blocks (4 a + i, 2 b + j): block (i, j) of the quarter of halves a and b
+    v4f acc[8][4];
 #pragma unroll
-    for (int i0 = 0; i0 < FP; i0 += kRun) {
+    for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int i = 0; i < kRun; ++i)
+        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const Fragments<H, TA> ga(wp);
+    const Fragments<H, TB> gb(wq);
+    v8bf fa[2][4], fb[2][2][2];     // [step][block], [half][step][block]
+    // byte addresses of tile k's halves: A0, A1, B0, B1
+    const uint32_t base = lds_address(lds);
+    const auto half = [&](int k, int h) { return base + 2 * kHalf * (4 * (k & 1) + h); };
+    const auto read_a = [&](uint32_t from) {
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) {
-                const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
-                *reinterpret_cast<v4f*>(mine + o * kCols + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
-            }
-        constexpr int kGroups = kCols / 8;
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[s][i] = ga.get(from, i, s);
+    };
+    const auto read_b = [&](int h, uint32_t from) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[h][s][j] = gb.get(from, j, s);
+    };
+    const auto multiply = [&](int a, int b) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[4 * a + i][2 * b + j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                        fb[b][s][j], fa[s][i], acc[4 * a + i][2 * b + j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+
+    const int n = (int)((r1 - r0) / kBR);
+    if (n > 0) {
+        Direct<H, TA, T> a0, a1;
+        Direct<H, TB, T> b0, b1;
+        constexpr int kLoads = Direct<H, TA, T>::kLoads;
+        a0.init(d.a, d.lda, p0, d.P, r0);
+        a1.init(d.a, d.lda, p0 + H, d.P, r0);
+        b0.init(d.b, d.ldb, q0, d.Q, r0);
+        b1.init(d.b, d.ldb, q0 + H, d.Q, r0);
+        // loads of tiles behind the last are stopped by their buffer's range
+        const auto there = [&](int k) { return __builtin_amdgcn_readfirstlane(k < n ? -1 : 0); };
+        a0.issue(half(0, 0), wave, -1);
+        b0.issue(half(0, 2), wave, -1);
+        b1.issue(half(0, 3), wave, -1);
+        a1.issue(half(0, 1), wave, -1);
+        a0.issue(half(1, 0), wave, there(1));
+        b0.issue(half(1, 2), wave, there(1));
+        b1.issue(half(1, 3), wave, there(1));
+        loads_landed<5 * kLoads>();
+        meet_waves();
+        if (wave >= 4) meet_waves();
 #pragma unroll 1
-        for (int at = lane; at < kRows * kGroups; at += 64) {
-            const int o = at / kGroups, c = at % kGroups;
-            const v4f lo = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c) ^ (o & 15)));
-            const v4f hi = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c + 1) ^ (o & 15)));
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            const int64_t p = p0 + wp + 16 * i0 + o, q = q0 + wq + 8 * c;
-            if (p >= d.P || q >= d.Q) continue;
-            const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
-            if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
-            else epilogue8<EPI>(d, off, p, q, v, n);
+        for (int k = 0; k < n; ++k) {
+            const int one = there(k + 1), two = there(k + 2);
+            read_b(0, half(k, 2));
+            read_a(half(k, 0));
+            a1.issue(half(k + 1, 1), wave, one);
+            loads_landed<5 * kLoads>();
+            meet_waves();
+            multiply(0, 0);
+            meet_waves();
+            read_b(1, half(k, 3));
+            a0.issue(half(k, 0), wave, two);
+            loads_landed<5 * kLoads>();
+            meet_waves();
+            multiply(0, 1);
+            meet_waves();
+            read_a(half(k, 1));
+            b0.issue(half(k, 2), wave, two);
+            loads_landed<5 * kLoads>();
+            meet_waves();
+            multiply(1, 1);
+            meet_waves();
+            b1.issue(half(k, 3), wave, two);
+            loads_landed<5 * kLoads>();
+            meet_waves();
+            multiply(1, 0);
+            meet_waves();
         }
+        if (wave < 4) meet_waves();
+        loads_landed<0>();
+        meet_waves();
     }
+    if (r0 + (int64_t)n * kBR < r1) {
+        // what is left of the reduction, with its end masked
+        const int64_t r = r0 + (int64_t)n * kBR;
+        stage_tail<H, TA, T>(lds, d.a, d.lda, p0, d.P, r, r1);
+        stage_tail<H, TA, T>(lds + kHalf, d.a, d.lda, p0 + H, d.P, r, r1);
+        stage_tail<H, TB, T>(lds + 2 * kHalf, d.b, d.ldb, q0, d.Q, r, r1);
+        stage_tail<H, TB, T>(lds + 3 * kHalf, d.b, d.ldb, q0 + H, d.Q, r, r1);
+        meet_waves();
+        read_b(0, half(0, 2));
+        read_b(1, half(0, 3));
+        read_a(half(0, 0));
+        multiply(0, 0);
+        multiply(0, 1);
+        read_a(half(0, 1));
+        multiply(1, 1);
+        multiply(1, 0);
+        meet_waves();
+    }
+    finish<EPI, sizeof(lds), 8>(g, acc, lds, wave, [&](int i) { return p0 + H * (i >> 2) + wp + 16 * (i & 3); },
+                                [&](int j) { return q0 + H * (j >> 1) + wq + 16 * (j & 1); });
 }
 
 // Joins the splits of a long reduction in their order, then the epilogue: eight
@@ -404,25 +584,21 @@ static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld < (int64_t(1) << 21)));
 }
 
-template <int NWP, int NWQ, int FP, int FQ, bool TA, bool TB, int EPI, bool DIRECT>
-static hipError_t tiles_launch(const ProductArgs& g, hipStream_t st) {
-    constexpr int BP = 16 * FP * NWP, BQ = 16 * FQ * NWQ;
-    const int64_t tiles = ((g.d.P + BP - 1) / BP) * ((g.d.Q + BQ - 1) / BQ);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_product<NWP, NWQ, FP, FQ, TA, TB, EPI, DIRECT>), dim3((unsigned)tiles, (unsigned)g.splits),
-                       dim3(64 * NWP * NWQ), 0, st, g);
-    return hipGetLastError();
-}
-
 template <bool TA, bool TB, int EPI>
 static hipError_t product(ProductArgs& g, hipStream_t st) {
     const ProductDesc& d = g.d;
     if (d.P <= 0 || d.Q <= 0) return hipSuccess;
     const bool direct = direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
-    const int64_t big = ((d.P + 255) / 256) * ((d.Q + 255) / 256);
-    hipError_t e = !direct ? tiles_launch<2, 2, 4, 4, TA, TB, EPI, false>(g, st)
-                   : big >= 256 ? tiles_launch<2, 4, 8, 4, TA, TB, EPI, true>(g, st)
-                                : tiles_launch<2, 2, 4, 4, TA, TB, EPI, true>(g, st);
+    const int64_t wide = ((d.P + 255) / 256) * ((d.Q + 255) / 256), tiles = ((d.P + 127) / 128) * ((d.Q + 127) / 128);
+    if (tiles > INT32_MAX) return hipErrorInvalidValue;
+    const unsigned splits = (unsigned)g.splits;
+    if (direct && wide >= 256)
+        hipLaunchKernelGGL((k_product_wide<TA, TB, EPI>), dim3((unsigned)wide, splits), dim3(512), 0, st, g);
+    else if (direct)
+        hipLaunchKernelGGL((k_product<TA, TB, EPI, true>), dim3((unsigned)tiles, splits), dim3(256), 0, st, g);
+    else
+        hipLaunchKernelGGL((k_product<TA, TB, EPI, false>), dim3((unsigned)tiles, splits), dim3(256), 0, st, g);
+    const hipError_t e = hipGetLastError();
     if (e != hipSuccess || !g.part) return e;
     const int64_t blocks = (d.P * (g.ld_part / 8) + 255) / 256;
     hipLaunchKernelGGL((k_join<EPI>), dim3((unsigned)blocks), dim3(256), 0, st, g);
