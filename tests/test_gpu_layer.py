@@ -465,3 +465,46 @@ def test_wide_outputs(Z, rows, inner, layout):
     want, err = R.linear_grad_weight(dz.f64(), x.f64(), old=old, out="f32")
     close("dw", dw.t if layout == 0 else dw.t.t(), want, err)
     assert dw.intact_outside()
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("M,K,N", [(70, 4104, 4100), (512, 16, 4200), (333, 4200, 8), (9000, 264, 260), (64, 2048, 2304),
+                                   (100, 0, 300)])
+def test_bias_gradient_of_wide_weights(Z, M, K, N, layout):
+    """The bias gradient beside weight gradients of many tiles, of one row or column of
+    tiles, of split sums, and of a weight with no elements."""
+    rng = np.random.default_rng(hash((15, M, K, N, layout)) % 2 ** 32)
+    say("bias", M, K, N, layout)
+    dz, x = inp(rng, M, N, pad_ld=-N % 8), inp(rng, M, K, pad_ld=-K % 8)
+    r, c = (N, K) if layout == 0 else (K, N)
+    dw = torch.zeros((r, c), dtype=F32, device=dev())
+    db = Mat(1, N, F32, fill=rand(rng, 1, N))
+    old = db.f64()[0]
+    Z.zero_linear_grad_weight(dz.t, x.t, dw, db.t[0], w_layout=layout, accumulate=True)
+    want, err = R.column_sums(dz.f64(), old=old, out="f32")
+    close("db", db.t[0], want, err)
+    assert db.intact_outside()
+    want, err = R.linear_grad_weight(dz.f64(), x.f64(), out="f32")
+    close("dw", dw if layout == 0 else dw.t(), want, err)
+
+
+@pytest.mark.parametrize("M,K,N", [(4352, 72, 4096), (4096, 192, 4608), (2048, 64, 16640), (8192, 128, 2304)])
+def test_rounds_and_quarters(Z, M, K, N):
+    """Tile counts a little over whole rounds of the chip, whose rest goes to smaller
+    tiles, in a second launch."""
+    rng = np.random.default_rng(16 + M)
+    x, w = inp(rng, M, K), inp(rng, N, K, scale=0.1)
+    y = Mat(M, N, BF, ld=N + 8)
+    Z.zero_linear_forward(x.t, w.t, y=y.t)
+    want, err, _, _ = R.linear_forward(x.f64(), w.f64())
+    close("y", y.t, want, err)
+    assert y.intact_outside()
+    dz = inp(rng, K, M)
+    dw = torch.empty((M, N), dtype=BF, device=dev())
+    db = torch.empty(M, dtype=BF, device=dev())
+    x = inp(rng, K, N)
+    Z.zero_linear_grad_weight(dz.t, x.t, dw, db)
+    want, err = R.linear_grad_weight(dz.f64(), x.f64())
+    close("dw", dw, want, err)
+    want, err = R.column_sums(dz.f64())
+    close("db", db, want, err)

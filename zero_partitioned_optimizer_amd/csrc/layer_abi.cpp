@@ -150,12 +150,13 @@ Mat ws_mat(void* ws, size_t need) {
     return Mat{"workspace_dev", need ? ws : nullptr, 1, (int64_t)need, (int64_t)need, 1, true, false, true};
 }
 
-// Bytes of the weight gradient's product and, behind it, of the bias gradient.
+// Bytes of the weight gradient's product ([N, K] or [K, N], the larger of the two)
+// and, behind it, of the bias gradient.
 size_t weight_ws(int64_t M, int64_t K, int64_t N, size_t* product) {
-    // a product of [N, K] or of [K, N]: the larger of the two
     const size_t a = zk::product_ws_bytes(N, K, M), b = zk::product_ws_bytes(K, N, M);
+    const size_t c = zk::sums_ws_bytes(N, K, M, true), d = zk::sums_ws_bytes(K, N, M, false);
     *product = ((a > b ? a : b) + 15) & ~(size_t)15;
-    return *product + zk::colsum_ws_bytes(M, N);
+    return *product + (c > d ? c : d);
 }
 
 }  // namespace
@@ -306,11 +307,11 @@ int zero_linear_grad_weight(const zero_linear_grad_weight_args* args, void* stre
     d.res = a.accumulate ? a.dw : nullptr;
     d.ld_res = a.ld_dw;
     d.ws = static_cast<float*>(a.workspace_dev);
-    const hipStream_t st = static_cast<hipStream_t>(stream);
-    if ((rc = zl::hip_error(zk::launch_product(d, st), fn)) || !a.dbias) return rc;
-    float* sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace_dev) + product);
-    return zl::hip_error(zk::launch_colsum(a.dz, a.ld_dz, a.M, a.N, a.dbias, d.out_f32, a.accumulate != 0, sums,
-                                           st), fn);
+    d.bias_out = a.dbias;
+    d.bias_of_a = oi;
+    d.bias_add = a.accumulate != 0;
+    d.ws_sums = reinterpret_cast<float*>(static_cast<char*>(a.workspace_dev) + product);
+    return zl::hip_error(zk::launch_product(d, static_cast<hipStream_t>(stream)), fn);
 }
 
 static int dropout(const char* fn, const zero_dropout_args* args, bool grad, void* stream) {

@@ -43,18 +43,18 @@ struct ProductDesc {
     int64_t ld_z;
     int32_t act;
     Drop drop;
-    float* ws;
+    void* bias_out;                 // weight gradient: the bias's, of out's type, or nullptr
+    bool bias_of_a;                 // ... the sums over r of a, or of b
+    bool bias_add;                  // ... added to what it holds
+    float* ws;                      // product_ws_bytes
+    float* ws_sums;                 // sums_ws_bytes
 };
 
-// Workspace bytes that launch_product needs for a product of these sizes.
+// Workspace bytes that launch_product needs for a product of these sizes, and
+// for the bias gradient beside it.
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R);
+size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a);
 hipError_t launch_product(const ProductDesc& d, hipStream_t st);
-
-// out[n] = (old ? old[n] : 0) + sum over the M rows of dz[m, n]; ws holds
-// colsum_ws_bytes(M, N) bytes.
-size_t colsum_ws_bytes(int64_t M, int64_t N);
-hipError_t launch_colsum(const uint16_t* dz, int64_t ld, int64_t M, int64_t N, void* out, bool out_f32,
-                         bool accumulate, float* ws, hipStream_t st);
 
 // Elementwise over [M, N]: y = res + D(x), or (grad) y = D'(x) * act'(z).
 struct DropoutDesc {

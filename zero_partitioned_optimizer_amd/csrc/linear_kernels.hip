@@ -19,8 +19,16 @@ struct ProductArgs {
     ProductDesc d;
     int64_t r_per_split;            // multiple of kBR
     int32_t splits;
+    int32_t tiles;                  // output tiles of the launch's kind
+    int32_t first_wide;             // k_product: -1, or its workgroups are the quarters of the wide
+                                    // tiles from this one on
     int64_t ld_part;                // row length of a split's partial products
     float* part;                    // [splits, P, ld_part], or nullptr: epilogue in place
+    int32_t sum_of;                 // weight gradient with a bias: 1, 2: sums of operand a, b
+    int32_t sum_rows;               // rows of partial sums
+    int64_t sum_n, ld_sums;         // the bias's length, and a row of partial sums'
+    float* sums;                    // [sum_rows, ld_sums]
+    int64_t join_blocks;            // k_join: workgroups on the product, before those on the sums
 };
 
 // Staged tiles hold eight-element chunks (16 bytes), permuted within a row so that
@@ -205,40 +213,43 @@ __device__ __forceinline__ void meet_waves() {
 // applied to the address that a lane reads. Rows and chunks outside the operand
 // read its last ones instead: they only reach outputs that do not exist. Used
 // where rows start on 16 bytes and a whole tile of the reduction is left.
-template <int ROWS, bool T, int THREADS>
+constexpr int kAllRecords = 0x7FFFFFFF;     // more than a tile's rows reach
+template <int ROWS, bool T, int THREADS, int PARTS>
 struct Direct {
     static constexpr int kLoads = ROWS * kBR / 8 / THREADS;
-    uint32_t at[kLoads];            // byte offsets from `base`
+    uint32_t at[PARTS][kLoads];     // byte offsets from `base`, of PARTS runs of ROWS outer indices
     const char* base;
     int64_t step;
     __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0) {
-        if (o0 >= O) o0 = (O - 1) & ~int64_t(7);        // a half tile with nothing in it
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int id = threadIdx.x + i * THREADS;
-            if constexpr (T) {
-                const int r = id / (ROWS / 8);
-                int64_t c = 8 * ((id % (ROWS / 8)) ^ perm_reduced<ROWS>(r));
-                if (o0 + c >= O) c = (O - 1 - o0) & ~int64_t(7);
-                at[i] = (uint32_t)((r * ld + c) * 2);
-            } else {
-                int64_t o = id / (kBR / 8);
-                const int c = 8 * ((id % (kBR / 8)) ^ (int)(o & 7));
-                if (o0 + o >= O) o = O - 1 - o0;
-                at[i] = (uint32_t)((o * ld + c) * 2);
+        for (int h = 0; h < PARTS; ++h)
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) {
+                const int id = threadIdx.x + i * THREADS;
+                if constexpr (T) {
+                    const int r = id / (ROWS / 8);
+                    int64_t c = ROWS * h + 8 * ((id % (ROWS / 8)) ^ perm_reduced<ROWS>(r));
+                    if (o0 + c >= O) c = (O - 1 - o0) & ~int64_t(7);
+                    at[h][i] = (uint32_t)((r * ld + c) * 2);
+                } else {
+                    const int in = id / (kBR / 8), c = 8 * ((id % (kBR / 8)) ^ (in & 7));
+                    int64_t o = ROWS * h + in;
+                    if (o0 + o >= O) o = O - 1 - o0;
+                    at[h][i] = (uint32_t)((o * ld + c) * 2);
+                }
             }
-        }
         base = reinterpret_cast<const char*>(src + (T ? r0 * ld + o0 : o0 * ld + r0));
         step = (T ? kBR * ld : kBR) * 2;
     }
-    // The tile's loads to LDS byte address `tile`; `wave` is the same in all lanes.
-    // With `records` 0 the buffer's range check stops them (they still count as loads).
-    __device__ __forceinline__ void issue(uint32_t tile, int wave, int records) {
-        const v4i rsrc = {(int)(uint32_t)reinterpret_cast<uintptr_t>(base),
-                          (int)(uint32_t)(reinterpret_cast<uintptr_t>(base) >> 32), records, 0x00020000};
+    // Part h of the tile at `from` (base, or steps away from it) to LDS byte address
+    // `tile`; `wave` is the same in all lanes. With `records` 0 the buffer's range check
+    // stops the loads (which still count as loads).
+    __device__ __forceinline__ void issue(int h, const char* from, uint32_t tile, int wave, int records) const {
+        const uintptr_t b = reinterpret_cast<uintptr_t>(from);
+        const v4i rsrc = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                          __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), records, 0x00020000};
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) lds_load(rsrc, at[i], tile + 16 * (i * THREADS + 64 * wave));
-        base += step;
+        for (int i = 0; i < kLoads; ++i) lds_load(rsrc, at[h][i], tile + 16 * (i * THREADS + 64 * wave));
     }
 };
 
@@ -249,13 +260,52 @@ struct Direct {
 // (Llama-7B shaped products: 8 rows 5% faster than tiles in order, 4 or 16 rows 2%
 // behind 8 on the deepest reductions.)
 constexpr int kTileRows = 8;
-__device__ __forceinline__ void tile_of(int id, int tiles, int np, int nq, int* tp, int* tq) {
+__device__ __forceinline__ int tile_in_turn(int id, int tiles) {
     const int xcd = id & 7, slot = id >> 3, each = tiles >> 3, more = tiles & 7;
-    const int t = xcd * each + (xcd < more ? xcd : more) + slot;
+    return xcd * each + (xcd < more ? xcd : more) + slot;
+}
+__device__ __forceinline__ void tile_place(int t, int np, int nq, int* tp, int* tq) {
     const int block = t / (kTileRows * nq), in = t - block * kTileRows * nq;
     const int rows = np - block * kTileRows < kTileRows ? np - block * kTileRows : kTileRows;
-    *tq = in / rows;
-    *tp = block * kTileRows + in - *tq * rows;
+    const int col = in / rows;
+    // the same in all lanes, which the divisions hide from the compiler
+    *tq = __builtin_amdgcn_readfirstlane(col);
+    *tp = __builtin_amdgcn_readfirstlane(block * kTileRows + in - col * rows);
+}
+
+// Whole tiles of kBR in this split, in 32 bits: a 64-bit comparison would put what
+// depends on it into vector registers, the loads' descriptors among them.
+__device__ __forceinline__ int whole_steps(const ProductArgs& g) {
+    const int per = (int)(g.r_per_split / kBR), left = (int)(g.d.R / kBR) - (int)blockIdx.y * per;
+    const int n = left < per ? left : per;
+    return n > 0 ? n : 0;
+}
+
+// The bias gradient rides on the weight's: each output tile has dz in one of its
+// operands, so the tiles that share a run of dz's columns take turns at its
+// reduction tiles and multiply the operand's blocks by ones as well, which sums
+// their columns: 4 more matrix instructions for 64, once in as many tiles as share.
+struct SumTurn {
+    int32_t turn, others;           // this workgroup's reduction tiles: k % others == turn
+    bool on;
+    int32_t left;                   // tiles until its next one
+    __device__ __forceinline__ SumTurn(int t, int n, bool o) : turn(t), others(n), on(o), left(t) {}
+    // Whether the next tile, in order, is this workgroup's.
+    __device__ __forceinline__ bool next() {
+        const bool now = left == 0;
+        left = now ? others - 1 : left - 1;
+        return on && now;
+    }
+};
+__device__ __forceinline__ v8bf ones8() {
+    const __bf16 one = (__bf16)1.0f;
+    return v8bf{one, one, one, one, one, one, one, one};
+}
+// Lane l of the product's block holds the sum of column l & 15, in all its rows.
+__device__ __forceinline__ void put_sums(const ProductArgs& g, const SumTurn& t, int64_t col, v4f v) {
+    const int lane = threadIdx.x & 63;
+    if (lane < 16 && col + lane < g.sum_n)
+        g.sums[((int64_t)blockIdx.y * t.others + t.turn) * g.ld_sums + col + lane] = v[0];
 }
 
 // The epilogue of a workgroup's tile, through LDS: kRun rows of a wave's blocks at a
@@ -303,15 +353,28 @@ __device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP
 // tiles and, without DIRECT, for operands at any address: tiles of 64 reduction
 // elements, two in LDS, the next one loading while one is multiplied. Two
 // workgroups of 64 KB fit a compute unit and fill each other's waits.
-template <bool TA, bool TB, int EPI, bool DIRECT>
-__global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
+template <bool TA, bool TB, int EPI, bool DIRECT, bool SUM>
+__global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
     constexpr int kBufs = DIRECT ? 2 : 1;
     __shared__ __attribute__((aligned(16))) uint16_t lds[kBufs * 2 * kTile];
     const ProductDesc& d = g.d;
-    int tp, tq;
-    tile_of(blockIdx.x, gridDim.x, (int)((d.P + B - 1) / B), (int)((d.Q + B - 1) / B), &tp, &tq);
+    int tp, tq, np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
+    if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
+    SumTurn turn{0, 1, false};
+    if (g.first_wide < 0) {
+        tile_place(tile_in_turn(blockIdx.x, g.tiles), np, nq, &tp, &tq);
+        turn = g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
+    } else {
+        np = (np + 1) / 2, nq = (nq + 1) / 2;
+        const int id = tile_in_turn(blockIdx.x, g.tiles);
+        tile_place(g.first_wide + (id >> 2), np, nq, &tp, &tq);
+        turn = g.sum_of == 1 ? SumTurn{tq, nq, (id & 1) == 0} : SumTurn{tp, np, g.sum_of == 2 && (id & 2) == 0};
+        tp = 2 * tp + ((id >> 1) & 1);
+        tq = 2 * tq + (id & 1);
+    }
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
     const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -325,7 +388,9 @@ __global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
     const Fragments<B, TA> ga(wp);
     const Fragments<B, TB> gb(wq);
     const uint32_t base = lds_address(lds);
+    v4f sum[4] = {acc[0][0], acc[0][0], acc[0][0], acc[0][0]};
     const auto multiply = [&](uint32_t tile) {
+        const bool now = SUM && turn.next();
 #pragma unroll
         for (int s = 0; s < kBR / 32; ++s) {
             v8bf fa[FP], fb[FQ];
@@ -338,26 +403,38 @@ __global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
 #pragma unroll
                 for (int j = 0; j < FQ; ++j)
                     acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[j], fa[i], acc[i][j], 0, 0, 0);
+            if constexpr (SUM)
+                if (now) {
+                    if (g.sum_of == 1) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fa[i], sum[i], 0, 0, 0);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            sum[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fb[j], sum[j], 0, 0, 0);
+                    }
+                }
         }
     };
 
     if constexpr (DIRECT) {
-        const int full = (int)((r1 - r0) / kBR);
-        Direct<B, TA, T> da;
-        Direct<B, TB, T> db;
+        const int full = whole_steps(g);
+        Direct<B, TA, T, 1> da;
+        Direct<B, TB, T, 1> db;
         if (full > 0) {
             da.init(d.a, d.lda, p0, d.P, r0);
             db.init(d.b, d.ldb, q0, d.Q, r0);
-            da.issue(base, wave, -1);
-            db.issue(base + 2 * kTile, wave, -1);
+            da.issue(0, da.base, base, wave, kAllRecords);
+            db.issue(0, db.base, base + 2 * kTile, wave, kAllRecords);
         }
         for (int k = 0; k < full; ++k) {
             loads_landed<0>();
             meet_waves();
             const uint32_t tile = base + 4 * kTile * (k & 1), next = base + 4 * kTile * ((k + 1) & 1);
             if (k + 1 < full) {
-                da.issue(next, wave, -1);
-                db.issue(next + 2 * kTile, wave, -1);
+                da.issue(0, da.base += da.step, next, wave, kAllRecords);
+                db.issue(0, db.base += db.step, next + 2 * kTile, wave, kAllRecords);
             }
             multiply(tile);
         }
@@ -390,6 +467,10 @@ __global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
         }
     }
     meet_waves();
+    if constexpr (SUM)
+        if (turn.on && (g.sum_of == 1 ? wq : wp) == 0)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) put_sums(g, turn, (g.sum_of == 1 ? p0 + wp : q0 + wq) + 16 * i, sum[i]);
     finish<EPI, sizeof(lds), 4>(g, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
                                 [&](int j) { return q0 + wq + 16 * j; });
 }
@@ -414,13 +495,15 @@ __global__ void __launch_bounds__(256) k_product(const ProductArgs g) {
 // them. What turn f reads was asked for in turn f - 6 or before, or in the prologue;
 // turn f - 1 waits until at most the five latest turns' loads are under way, and its
 // barrier comes before anyone's turn f. So a load has five turns to land.
-template <bool TA, bool TB, int EPI>
+template <bool TA, bool TB, int EPI, bool SUM>
 __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
     constexpr int T = 512, B = 256, H = 128, kHalf = H * kBR;
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 4 * kHalf];
     const ProductDesc& d = g.d;
     int tp, tq;
-    tile_of(blockIdx.x, gridDim.x, (int)((d.P + B - 1) / B), (int)((d.Q + B - 1) / B), &tp, &tq);
+    const int np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
+    tile_place(tile_in_turn(blockIdx.x, g.tiles), np, nq, &tp, &tq);
+    SumTurn turn = g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
     const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
@@ -466,50 +549,84 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
         __builtin_amdgcn_sched_barrier(0);
     };
 
-    const int n = (int)((r1 - r0) / kBR);
+    // Sums of dz's columns: where dz is operand a, the four waves of a row of waves
+    // have the same blocks of a half, and each sums one; where it is b, the two waves
+    // of a column of waves.
+    v4f sum[2] = {acc[0][0], acc[0][0]};
+    const auto sum_a = [&](int h) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((wave & 3) == i)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    sum[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fa[s][i], sum[h], 0, 0, 0);
+    };
+    const auto sum_b = [&](int h) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+            if ((wave >> 2) == j)
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+                    sum[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fb[h][s][j], sum[h], 0, 0, 0);
+    };
+    const auto sum_turn = [&](bool now, int turn_of_tile) {
+        if constexpr (SUM)
+            if (now) {
+                if (g.sum_of == 1 && turn_of_tile != 1) sum_a(turn_of_tile / 2);
+                if (g.sum_of == 2 && turn_of_tile != 2) sum_b(turn_of_tile);
+            }
+    };
+
+    const int n = whole_steps(g);
     if (n > 0) {
-        Direct<H, TA, T> a0, a1;
-        Direct<H, TB, T> b0, b1;
-        constexpr int kLoads = Direct<H, TA, T>::kLoads;
-        a0.init(d.a, d.lda, p0, d.P, r0);
-        a1.init(d.a, d.lda, p0 + H, d.P, r0);
-        b0.init(d.b, d.ldb, q0, d.Q, r0);
-        b1.init(d.b, d.ldb, q0 + H, d.Q, r0);
+        Direct<H, TA, T, 2> da;
+        Direct<H, TB, T, 2> db;
+        constexpr int kLoads = Direct<H, TA, T, 2>::kLoads;
+        da.init(d.a, d.lda, p0, d.P, r0);
+        db.init(d.b, d.ldb, q0, d.Q, r0);
         // loads of tiles behind the last are stopped by their buffer's range
-        const auto there = [&](int k) { return __builtin_amdgcn_readfirstlane(k < n ? -1 : 0); };
-        a0.issue(half(0, 0), wave, -1);
-        b0.issue(half(0, 2), wave, -1);
-        b1.issue(half(0, 3), wave, -1);
-        a1.issue(half(0, 1), wave, -1);
-        a0.issue(half(1, 0), wave, there(1));
-        b0.issue(half(1, 2), wave, there(1));
-        b1.issue(half(1, 3), wave, there(1));
+        const auto there = [&](int k) { return k < n ? kAllRecords : 0; };
+        da.issue(0, da.base, half(0, 0), wave, kAllRecords);
+        db.issue(0, db.base, half(0, 2), wave, kAllRecords);
+        db.issue(1, db.base, half(0, 3), wave, kAllRecords);
+        da.issue(1, da.base, half(0, 1), wave, kAllRecords);
+        da.issue(0, da.base + da.step, half(1, 0), wave, there(1));
+        db.issue(0, db.base + db.step, half(1, 2), wave, there(1));
+        db.issue(1, db.base + db.step, half(1, 3), wave, there(1));
+        da.base += 2 * da.step;         // of tile k + 2
+        db.base += 2 * db.step;
         loads_landed<5 * kLoads>();
         meet_waves();
         if (wave >= 4) meet_waves();
 #pragma unroll 1
         for (int k = 0; k < n; ++k) {
             const int one = there(k + 1), two = there(k + 2);
+            const bool now = SUM && turn.next();
             read_b(0, half(k, 2));
             read_a(half(k, 0));
-            a1.issue(half(k + 1, 1), wave, one);
+            da.issue(1, da.base - da.step, half(k + 1, 1), wave, one);
             loads_landed<5 * kLoads>();
             meet_waves();
             multiply(0, 0);
+            sum_turn(now, 0);
             meet_waves();
             read_b(1, half(k, 3));
-            a0.issue(half(k, 0), wave, two);
+            da.issue(0, da.base, half(k, 0), wave, two);
             loads_landed<5 * kLoads>();
             meet_waves();
             multiply(0, 1);
+            sum_turn(now, 1);
             meet_waves();
             read_a(half(k, 1));
-            b0.issue(half(k, 2), wave, two);
+            db.issue(0, db.base, half(k, 2), wave, two);
             loads_landed<5 * kLoads>();
             meet_waves();
             multiply(1, 1);
+            sum_turn(now, 2);
             meet_waves();
-            b1.issue(half(k, 3), wave, two);
+            db.issue(1, db.base, half(k, 3), wave, two);
+            da.base += da.step;
+            db.base += db.step;
             loads_landed<5 * kLoads>();
             meet_waves();
             multiply(1, 0);
@@ -527,30 +644,65 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
         stage_tail<H, TB, T>(lds + 2 * kHalf, d.b, d.ldb, q0, d.Q, r, r1);
         stage_tail<H, TB, T>(lds + 3 * kHalf, d.b, d.ldb, q0 + H, d.Q, r, r1);
         meet_waves();
+        const bool now = SUM && turn.next();
         read_b(0, half(0, 2));
         read_b(1, half(0, 3));
         read_a(half(0, 0));
         multiply(0, 0);
+        sum_turn(now, 0);
         multiply(0, 1);
+        sum_turn(now, 1);
         read_a(half(0, 1));
         multiply(1, 1);
+        sum_turn(now, 2);
         multiply(1, 0);
         meet_waves();
     }
+    if constexpr (SUM)
+        if (turn.on)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                put_sums(g, turn, (g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 16 * (wave >> 2)) + H * h,
+                         sum[h]);
     finish<EPI, sizeof(lds), 8>(g, acc, lds, wave, [&](int i) { return p0 + H * (i >> 2) + wp + 16 * (i & 3); },
                                 [&](int j) { return q0 + H * (j >> 1) + wq + 16 * (j & 1); });
 }
 
-// Joins the splits of a long reduction in their order, then the epilogue: eight
-// columns of one row per thread.
+// Joins the splits of a long reduction in their order, then the epilogue, eight
+// columns of one row per thread; and, in the workgroups behind those, the rows of
+// partial sums of the bias gradient, 64 columns to a workgroup, its four waves on
+// every fourth row and then joined in order.
 template <int EPI>
 __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
     const ProductDesc& d = g.d;
+    if (EPI == kEpiGradWeight && blockIdx.x >= g.join_blocks) {
+        __shared__ float s[3][64];
+        const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+        const int64_t j = (blockIdx.x - g.join_blocks) * 64 + lane;
+        float v = 0.0f;
+        if (j < g.sum_n) {
+#pragma unroll 4
+            for (int r = wave; r < g.sum_rows; r += 4) v += g.sums[r * g.ld_sums + j];
+        }
+        if (wave) s[wave - 1][lane] = v;
+        __syncthreads();
+        if (wave || j >= g.sum_n) return;
+        v = ((v + s[0][lane]) + s[1][lane]) + s[2][lane];
+        if (d.out_f32) {
+            float* o = static_cast<float*>(d.bias_out) + j;
+            *o = d.bias_add ? *o + v : v;
+        } else {
+            uint16_t* o = static_cast<uint16_t*>(d.bias_out) + j;
+            *o = bf_one(d.bias_add ? bf_f(*o) + v : v);
+        }
+        return;
+    }
     const int64_t groups = g.ld_part / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t p = id / groups, q = 8 * (id % groups);
     if (p >= d.P) return;
     float v[8], t[8];
     load8_f(v, g.part + p * g.ld_part + q, 8);
+#pragma unroll 4
     for (int s = 1; s < g.splits; ++s) {
         load8_f(t, g.part + ((int64_t)s * d.P + p) * g.ld_part + q, 8);
 #pragma unroll
@@ -560,23 +712,82 @@ __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
     epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, n);
 }
 
-// How the reduction of a product of these sizes is split.
-struct Split {
+// How a product of these sizes runs: the kind of tile, and into how many parts its
+// reduction is split, by an estimate of the time in microseconds. Measured on
+// products of 256 and more tiles: a 64-deep step of a 256 x 256 tile takes 1.5, one
+// of two 128 x 128 tiles that share a compute unit 1.0 (1.5 through registers), of
+// one alone 0.65; a tile's start and epilogue 7 and 3; a join 3 and its bytes at
+// 4.5 TB/s.
+struct Plan {
+    bool wide;
     int32_t splits;
-    int64_t per;
+    int64_t per;                    // reduction elements per split
+    int64_t full;                   // wide tiles of whole rounds of the chip; the rest as quarters
 };
-static Split split_of(int64_t P, int64_t Q, int64_t R) {
-    const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), steps = (R + kBR - 1) / kBR;
-    int64_t s = tiles > 0 && tiles < 256 ? 512 / tiles : 1;
-    if (s > steps / 4) s = steps / 4;
-    if (s < 1) s = 1;
-    const int64_t per = (steps + s - 1) / s * kBR;
-    return Split{(int32_t)(per > 0 ? (R + per - 1) / per : 1), per > 0 ? per : kBR};
+static double small_time(int64_t tiles, int64_t steps, bool direct) {
+    const double two = direct ? 1.0 : 1.5, one = direct ? 0.65 : 1.0;
+    const int64_t full = tiles / 512, rest = tiles % 512;
+    return full * (two * steps + 3) + (rest == 0 ? 0 : rest <= 256 ? one * steps + 3 : two * steps + 3);
+}
+static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
+    // a bias gradient beside a weight of no elements still has its column of tiles
+    if (P < 1) P = 1;
+    if (Q < 1) Q = 1;
+    const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
+    const int64_t steps = (R + kBR - 1) / kBR;
+    Plan best{false, 1, steps > 0 ? steps * kBR : kBR, 0};
+    double least = 1e300;
+    for (int64_t s = 1; s <= 64 && (s == 1 || (steps + s - 1) / s >= 2); ++s) {
+        const int64_t each = steps > 0 ? (steps + s - 1) / s : 1, parts = steps > 0 ? (steps + each - 1) / each : 1;
+        // one round and a bit is as fast without a split's traffic
+        if (s > 1 && tiles * s > 2048) break;
+        const double join = parts > 1 ? 3 + (double)parts * P * Q * 8 / 4.5e6 : 0;
+        const double small = small_time(tiles * parts, each, direct) + join;
+        if (small < least) {
+            least = small;
+            best = Plan{false, (int32_t)parts, each * kBR, 0};
+        }
+        if (!direct) continue;
+        const int64_t rounds = wide * parts / 256, rest = wide * parts % 256;
+        const double round = 1.5 * each + 7;
+        double t = (rounds + (rest > 0)) * round + join;
+        int64_t full = wide;
+        if (parts == 1 && rounds > 0 && rest > 0) {
+            const double quarters = rounds * round + 3 + small_time(4 * rest, each, true);
+            if (quarters < t) t = quarters, full = rounds * 256;
+        }
+        if (t < least) {
+            least = t;
+            best = Plan{true, (int32_t)parts, each * kBR, full};
+        }
+    }
+    return best;
+}
+
+static int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
+static size_t part_bytes(const Plan& pl, int64_t P, int64_t Q) {
+    return pl.splits > 1 ? (size_t)pl.splits * (size_t)P * (size_t)up8(Q) * sizeof(float) : 0;
+}
+static int32_t sum_rows(const Plan& pl, int64_t other) {
+    if (other < 1) other = 1;
+    return pl.splits * (int32_t)((other + (pl.wide ? 255 : 127)) / (pl.wide ? 256 : 128));
 }
 
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R) {
-    const Split s = split_of(P, Q, R);
-    return s.splits > 1 ? (size_t)s.splits * (size_t)P * (size_t)((Q + 7) / 8 * 8) * sizeof(float) : 0;
+    size_t most = 0;
+    for (int direct = 0; direct < 2; ++direct) {
+        const size_t b = part_bytes(plan_of(P, Q, R, direct != 0), P, Q);
+        if (b > most) most = b;
+    }
+    return most;
+}
+size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a) {
+    size_t most = 0;
+    for (int direct = 0; direct < 2; ++direct) {
+        const size_t b = (size_t)sum_rows(plan_of(P, Q, R, direct != 0), of_a ? Q : P) * (size_t)up8(of_a ? P : Q) * sizeof(float);
+        if (b > most) most = b;
+    }
+    return most;
 }
 
 // Rows on 16 bytes, and a tile's rows within the 2 GiB that its offsets reach.
@@ -585,111 +796,58 @@ static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
 }
 
 template <bool TA, bool TB, int EPI>
-static hipError_t product(ProductArgs& g, hipStream_t st) {
-    const ProductDesc& d = g.d;
-    if (d.P <= 0 || d.Q <= 0) return hipSuccess;
-    const bool direct = direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
-    const int64_t wide = ((d.P + 255) / 256) * ((d.Q + 255) / 256), tiles = ((d.P + 127) / 128) * ((d.Q + 127) / 128);
-    if (tiles > INT32_MAX) return hipErrorInvalidValue;
-    const unsigned splits = (unsigned)g.splits;
-    if (direct && wide >= 256)
-        hipLaunchKernelGGL((k_product_wide<TA, TB, EPI>), dim3((unsigned)wide, splits), dim3(512), 0, st, g);
-    else if (direct)
-        hipLaunchKernelGGL((k_product<TA, TB, EPI, true>), dim3((unsigned)tiles, splits), dim3(256), 0, st, g);
-    else
-        hipLaunchKernelGGL((k_product<TA, TB, EPI, false>), dim3((unsigned)tiles, splits), dim3(256), 0, st, g);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !g.part) return e;
-    const int64_t blocks = (d.P * (g.ld_part / 8) + 255) / 256;
+static hipError_t product(const ProductDesc& d, hipStream_t st) {
+    const bool some = d.P > 0 && d.Q > 0;
+    if (!some && !d.bias_out) return hipSuccess;
+    const bool direct = some && direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
+    const Plan pl = plan_of(d.P, d.Q, d.R, direct);
+    const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;
+    const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
+    if (tiles > INT32_MAX / 4) return hipErrorInvalidValue;
+    ProductArgs g{};
+    g.d = d;
+    g.splits = pl.splits;
+    g.r_per_split = pl.per;
+    g.ld_part = up8(d.Q);
+    g.part = pl.splits > 1 ? d.ws : nullptr;
+    if (EPI == kEpiGradWeight && d.bias_out) {
+        g.sum_of = d.bias_of_a ? 1 : 2;
+        g.sum_n = d.bias_of_a ? d.P : d.Q;
+        g.ld_sums = up8(g.sum_n);
+        g.sum_rows = sum_rows(pl, d.bias_of_a ? d.Q : d.P);
+        g.sums = d.ws_sums;
+    }
+    const unsigned splits = (unsigned)pl.splits;
+    constexpr bool kSums = EPI == kEpiGradWeight;
+    hipError_t e = hipSuccess;
+    if (pl.wide) {
+        g.tiles = (int32_t)pl.full;
+        const auto k = kSums && g.sums ? k_product_wide<TA, TB, EPI, kSums> : k_product_wide<TA, TB, EPI, false>;
+        hipLaunchKernelGGL(k, dim3((unsigned)pl.full, splits), dim3(512), 0, st, g);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!pl.wide || pl.full < wide) {
+        g.first_wide = pl.wide ? (int32_t)pl.full : -1;
+        g.tiles = (int32_t)(pl.wide ? 4 * (wide - pl.full) : tiles);
+        const auto k = kSums && g.sums
+                           ? direct ? k_product<TA, TB, EPI, true, kSums> : k_product<TA, TB, EPI, false, kSums>
+                           : direct ? k_product<TA, TB, EPI, true, false> : k_product<TA, TB, EPI, false, false>;
+        hipLaunchKernelGGL(k, dim3((unsigned)g.tiles, splits), dim3(256), 0, st, g);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!g.part && !g.sums) return e;
+    g.join_blocks = g.part ? (d.P * (g.ld_part / 8) + 255) / 256 : 0;
+    const int64_t blocks = g.join_blocks + (g.sums ? (g.sum_n + 63) / 64 : 0);
     hipLaunchKernelGGL((k_join<EPI>), dim3((unsigned)blocks), dim3(256), 0, st, g);
     return hipGetLastError();
 }
 
 hipError_t launch_product(const ProductDesc& d, hipStream_t st) {
-    const Split s = split_of(d.P, d.Q, d.R);
-    ProductArgs g{};
-    g.d = d;
-    g.splits = s.splits;
-    g.r_per_split = s.per;
-    g.ld_part = (d.Q + 7) / 8 * 8;
-    g.part = s.splits > 1 ? d.ws : nullptr;
     if (d.epi == kEpiForward)
-        return d.tb ? product<false, true, kEpiForward>(g, st) : product<false, false, kEpiForward>(g, st);
+        return d.tb ? product<false, true, kEpiForward>(d, st) : product<false, false, kEpiForward>(d, st);
     if (d.epi == kEpiGradInput)
-        return d.tb ? product<false, true, kEpiGradInput>(g, st) : product<false, false, kEpiGradInput>(g, st);
-    return product<true, true, kEpiGradWeight>(g, st);
-}
-
-// Column sums of dz: each workgroup sums a run of rows for 512 columns (eight
-// columns to a thread, four waves on alternate rows, joined in LDS), and a second
-// kernel adds the runs in their order.
-constexpr int kSumCols = 512;
-static int64_t sum_runs(int64_t M, int64_t N) {
-    const int64_t cols = (N + kSumCols - 1) / kSumCols;
-    int64_t runs = cols > 0 ? 512 / cols : 1;
-    const int64_t most = (M + 31) / 32;
-    if (runs > most) runs = most;
-    return runs < 1 ? 1 : runs;
-}
-
-size_t colsum_ws_bytes(int64_t M, int64_t N) {
-    return (size_t)sum_runs(M, N) * (size_t)((N + 7) / 8 * 8) * sizeof(float);
-}
-
-__global__ void __launch_bounds__(256) k_colsum(const uint16_t* dz, int64_t ld, int64_t M, int64_t N,
-                                                int64_t rows, float* part) {
-    __shared__ float s[3][kSumCols];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-    const int64_t j = (int64_t)blockIdx.x * kSumCols + 8 * lane;
-    const int64_t m0 = (int64_t)blockIdx.y * rows, m1 = m0 + rows < M ? m0 + rows : M;
-    const int n = N - j >= 8 ? 8 : N - j > 0 ? (int)(N - j) : 0;
-    float v[8], t[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-    if (n > 0)
-        for (int64_t m = m0 + wave; m < m1; m += 4) {
-            load8_bf(t, dz + m * ld + j, n);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += t[k];
-        }
-    if (wave)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) s[wave - 1][8 * lane + k] = v[k];
-    __syncthreads();
-    if (wave == 0 && n > 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            v[k] = ((v[k] + s[0][8 * lane + k]) + s[1][8 * lane + k]) + s[2][8 * lane + k];
-        store8_f(part + (int64_t)blockIdx.y * ((N + 7) / 8 * 8) + j, v, 8);
-    }
-}
-
-__global__ void __launch_bounds__(256) k_colsum_join(const float* part, int64_t N, int runs, void* out, bool f32,
-                                                     bool accumulate) {
-    const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x, ld = (N + 7) / 8 * 8;
-    if (j >= N) return;
-    float v = 0.0f;
-    for (int s = 0; s < runs; ++s) v += part[s * ld + j];
-    if (f32) {
-        float* o = static_cast<float*>(out) + j;
-        *o = accumulate ? *o + v : v;
-    } else {
-        uint16_t* o = static_cast<uint16_t*>(out) + j;
-        *o = bf_one(accumulate ? bf_f(*o) + v : v);
-    }
-}
-
-hipError_t launch_colsum(const uint16_t* dz, int64_t ld, int64_t M, int64_t N, void* out, bool out_f32,
-                         bool accumulate, float* ws, hipStream_t st) {
-    if (N <= 0) return hipSuccess;
-    const int64_t runs = sum_runs(M, N), rows = (M + runs - 1) / runs;
-    hipLaunchKernelGGL(k_colsum, dim3((unsigned)((N + kSumCols - 1) / kSumCols), (unsigned)runs), dim3(256), 0,
-                       st, dz, ld, M, N, rows, ws);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(k_colsum_join, dim3((unsigned)((N + 255) / 256)), dim3(256), 0, st, ws, N, (int)runs, out,
-                       out_f32, accumulate);
-    return hipGetLastError();
+        return d.tb ? product<false, true, kEpiGradInput>(d, st) : product<false, false, kEpiGradInput>(d, st);
+    return product<true, true, kEpiGradWeight>(d, st);
 }
 
 }  // namespace zk
