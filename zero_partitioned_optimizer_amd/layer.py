@@ -13,6 +13,8 @@ are allocated; a workspace that is not given is allocated for the call.
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional, Sequence
 
 import torch
@@ -38,6 +40,7 @@ class zero_dropout(ctypes.Structure):
     def __init__(self, p: float = 0.0, seed: int = 0, offset: int = 0,
                  counter: Optional[torch.Tensor] = None):
         super().__init__(p, seed, offset, None)
+        self.counter = None
         if counter is not None:
             if counter.dtype != torch.int64 or counter.numel() < 1 or not counter.is_cuda:
                 raise B.ZeroError(B.ZERO_E_INVAL, "zero_dropout: counter is not an int64 device tensor")
@@ -76,8 +79,22 @@ class zero_dropout_args(ctypes.Structure):
 
 assert ctypes.sizeof(zero_dropout) == 32
 
-_NO_DROP = zero_dropout()
+# The argument blocks above as struct formats: the calls below fill theirs in one
+# go, which a ctypes structure would do field by field.
+_DROP = "dQQQ"
+_FORWARD = struct.Struct("@qqqQqQqiiQQqQqiiQq" + _DROP + "QQ")
+_GRAD_INPUT = struct.Struct("@qqqQqQqiiQqQqii" + _DROP + "QQ")
+_GRAD_WEIGHT = struct.Struct("@qqqQqQqQqQiiiiQQ")
+_DROPOUT = struct.Struct("@qqQqQqQqQqiiii" + _DROP)
+assert _FORWARD.size == ctypes.sizeof(zero_linear_args)
+assert _GRAD_INPUT.size == ctypes.sizeof(zero_linear_grad_input_args)
+assert _GRAD_WEIGHT.size == ctypes.sizeof(zero_linear_grad_weight_args)
+assert _DROPOUT.size == ctypes.sizeof(zero_dropout_args)
+
+_NO_DROP = (0.0, 0, 0, 0)
+_BF16, _F32 = torch.bfloat16, torch.float32
 _declared: Optional[ctypes.CDLL] = None
+_call: dict = {}
 
 
 def _lib() -> ctypes.CDLL:
@@ -92,17 +109,50 @@ def _lib() -> ctypes.CDLL:
                            ("zero_dropout_grad", zero_dropout_args)):
             getattr(L, name).argtypes = [P(args), vp]
             getattr(L, name).restype = ctypes.c_int
+            # the same entry point, for an argument block that is packed already
+            _call[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp)((name, L))
         L.zero_linear_workspace_bytes.argtypes = [i32, i64, i64, i64]
         L.zero_linear_workspace_bytes.restype = sz
         _declared = L
     return _declared
 
 
+def _enqueue(name: str, block: bytes, stream) -> None:
+    if _declared is None:
+        _lib()
+    if stream is None:
+        stream = _raw_stream()
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    rc = _call[name](block, stream)
+    if rc:
+        B._check(rc)
+
+
+# The current device and its stream's handle, by torch's own short ways to them.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream() -> int:
+    if _current is not None:
+        return _current(_device())
+    return torch.cuda.current_stream().cuda_stream
+
+
 def _bad(fn: str, what: str):
     raise B.ZeroError(B.ZERO_E_INVAL, f"{fn}: {what}")
 
 
-def _mat(fn: str, name: str, t: torch.Tensor, dtype, rows: int = -1, cols: int = -1):
+def _on_device(fn: str, name: str, t: torch.Tensor) -> int:
+    """The device of a call's first tensor, which is the current one."""
+    d = t.get_device()
+    if d < 0 or d != _device():
+        _bad(fn, f"{name} is on {t.device}, not on the current device")
+    return d
+
+
+def _mat(fn: str, name: str, t: torch.Tensor, dtype, device: int, rows: int = -1, cols: int = -1):
     """(address, ld) of a 2-D tensor after checking its type, shape, strides and device."""
     if t.dtype is not dtype:
         _bad(fn, f"{name} is {t.dtype}, not {dtype}")
@@ -110,11 +160,11 @@ def _mat(fn: str, name: str, t: torch.Tensor, dtype, rows: int = -1, cols: int =
     if len(shape) != 2 or (rows >= 0 and shape[0] != rows) or (cols >= 0 and shape[1] != cols):
         _bad(fn, f"{name} has shape {tuple(shape)}, not ({rows if rows >= 0 else 'M'}, "
                  f"{cols if cols >= 0 else 'N'})")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         _bad(fn, f"{name} is on {t.device}, not on the current device")
     r, c = shape
     s0, s1 = t.stride()
-    if c > 1 and s1 != 1:
+    if s1 != 1 and c > 1:
         _bad(fn, f"{name} has column stride {s1}; its rows must be contiguous")
     if r <= 1 or c == 0:
         return t.data_ptr(), c
@@ -123,10 +173,10 @@ def _mat(fn: str, name: str, t: torch.Tensor, dtype, rows: int = -1, cols: int =
     return t.data_ptr(), s0
 
 
-def _vec(fn: str, name: str, t: torch.Tensor, dtype, n: int) -> int:
+def _vec(fn: str, name: str, t: torch.Tensor, dtype, device: int, n: int) -> int:
     if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
         _bad(fn, f"{name} is {t.dtype} of shape {tuple(t.shape)}, not {n} contiguous {dtype}")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != device:
         _bad(fn, f"{name} is on {t.device}, not on the current device")
     return t.data_ptr()
 
@@ -138,68 +188,61 @@ def _type(fn: str, name: str, dtype) -> int:
     return ty
 
 
-def _drop(fn: str, dropout) -> zero_dropout:
+def _drop(fn: str, dropout, device: int):
     if dropout is None:
         return _NO_DROP
-    if dropout.counter_dev and dropout.counter.get_device() != torch.cuda.current_device():
+    counter = dropout.counter_dev
+    if counter and dropout.counter is not None and dropout.counter.get_device() != device:
         _bad(fn, f"the dropout's counter is on {dropout.counter.device}, not on the current device")
-    return dropout
+    return dropout.p, dropout.seed, dropout.offset, counter or 0
 
 
-def _on(fn: str, stream):
-    """(handle, torch stream) of ``stream`` or of the current one."""
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return stream if isinstance(stream, int) else stream.cuda_stream
+@functools.lru_cache(maxsize=4096)
+def _workspace_need(kind: int, M: int, K: int, N: int) -> int:
+    return int(_lib().zero_linear_workspace_bytes(kind, M, K, N))
 
 
 def zero_linear_workspace_bytes(kind: int, M: int, K: int, N: int) -> int:
-    return int(_lib().zero_linear_workspace_bytes(int(kind), int(M), int(K), int(N)))
+    return _workspace_need(int(kind), int(M), int(K), int(N))
 
 
-def _workspace(fn: str, kind: int, M: int, K: int, N: int, given, stream):
+def _new(shape, dtype, device: int, stream):
+    """A new tensor from torch's allocator for use on ``stream``: memory that a call
+    gives back (its workspace) goes to that stream's pool, whose order keeps later
+    use behind the call's kernels."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=_cuda(device))
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=_cuda(device))
+
+
+@functools.lru_cache(maxsize=64)
+def _cuda(device: int) -> torch.device:
+    return torch.device("cuda", device)
+
+
+def _workspace(fn: str, kind: int, M: int, K: int, N: int, given, device: int, stream):
     """(address, bytes, tensor) of a call's workspace."""
     if given is not None:
-        if not given.is_cuda or given.get_device() != torch.cuda.current_device():
+        if given.get_device() != device:
             _bad(fn, f"workspace is on {given.device}, not on the current device")
         if not given.is_contiguous():
             _bad(fn, "workspace is not contiguous")
         return given.data_ptr(), given.numel() * given.element_size(), given
-    need = _lib().zero_linear_workspace_bytes(kind, M, K, N)
+    need = _workspace_need(kind, M, K, N)
     if need == 0:
         return 0, 0, None
-    return _scratch(need, stream)
-
-
-def _scratch(need: int, stream):
-    """A call's own workspace, from torch's allocator, for use on ``stream``: the
-    memory goes back to that stream's pool when the call returns, and the
-    stream's order keeps later use behind this call's kernels."""
-    if stream is None:
-        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
-    else:
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream)
-        with torch.cuda.stream(stream):
-            ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    ws = _new(need, torch.uint8, device, stream)
     return ws.data_ptr(), need, ws
 
 
-def _output(rows: int, cols: int, dtype, like: torch.Tensor, stream):
-    """A new output, allocated for use on ``stream``."""
-    if stream is None:
-        return torch.empty((rows, cols), dtype=dtype, device=like.device)
-    if isinstance(stream, int):
-        stream = torch.cuda.ExternalStream(stream)
-    with torch.cuda.stream(stream):
-        return torch.empty((rows, cols), dtype=dtype, device=like.device)
-
-
-def _weight(fn: str, w: torch.Tensor, w_layout: int, dtype, K: int, N: int):
+def _weight(fn: str, name: str, w: torch.Tensor, w_layout: int, dtype, device: int, K: int, N: int):
     if w_layout == ZERO_W_OUT_IN:
-        return _mat(fn, "w", w, dtype, N, K)
+        return _mat(fn, name, w, dtype, device, N, K)
     if w_layout == ZERO_W_IN_OUT:
-        return _mat(fn, "w", w, dtype, K, N)
+        return _mat(fn, name, w, dtype, device, K, N)
     _bad(fn, f"unknown w_layout {w_layout}")
 
 
@@ -210,29 +253,32 @@ def zero_linear_forward(x, w, bias=None, *, w_layout: int = ZERO_W_OUT_IN, act: 
     receives x W^T + bias, or True for a new one, and (y, preact) is returned.
     ``dtype`` (bfloat16 or float32) is that of a new y."""
     fn = "zero_linear_forward"
-    bf16 = torch.bfloat16
-    px, ldx = _mat(fn, "x", x, bf16)
+    dev = _on_device(fn, "x", x)
+    px, ldx = _mat(fn, "x", x, _BF16, dev)
     M, K = x.shape
     if w.dim() != 2:
         _bad(fn, f"w has shape {tuple(w.shape)}")
     N = w.shape[0] if w_layout == ZERO_W_OUT_IN else w.shape[1]
-    pw, ldw = _weight(fn, w, w_layout, bf16, K, N)
+    pw, ldw = _weight(fn, "w", w, w_layout, _BF16, dev, K, N)
     if y is None:
-        y = _output(M, N, dtype or (residual.dtype if residual is not None else bf16), x, stream)
+        y = _new((M, N), dtype or (residual.dtype if residual is not None else _BF16), dev, stream)
     elif dtype is not None and y.dtype is not dtype:
         _bad(fn, f"y is {y.dtype}, not {dtype}")
     ty = _type(fn, "y", y.dtype)
-    py, ldy = _mat(fn, "y", y, y.dtype, M, N)
-    pr, ldr = _mat(fn, "residual", residual, y.dtype, M, N) if residual is not None else (None, 0)
+    py, ldy = _mat(fn, "y", y, y.dtype, dev, M, N)
+    pr = ldr = pz = ldz = pb = 0
+    if residual is not None:
+        pr, ldr = _mat(fn, "residual", residual, y.dtype, dev, M, N)
     both = preact is not None and preact is not False
-    if preact is True:
-        preact = _output(M, N, bf16, x, stream)
-    pz, ldz = _mat(fn, "preact", preact, bf16, M, N) if both else (None, 0)
-    pb = _vec(fn, "bias", bias, bf16, N) if bias is not None else None
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_FORWARD, M, K, N, workspace, stream)
-    a = zero_linear_args(M, K, N, px, ldx, pw, ldw, w_layout, act, pb, pr, ldr, py, ldy, ty, 0, pz, ldz,
-                         _drop(fn, dropout), ws, nws)
-    B._check(_lib().zero_linear_forward(a, _on(fn, stream)))
+    if both:
+        if preact is True:
+            preact = _new((M, N), _BF16, dev, stream)
+        pz, ldz = _mat(fn, "preact", preact, _BF16, dev, M, N)
+    if bias is not None:
+        pb = _vec(fn, "bias", bias, _BF16, dev, N)
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_FORWARD, M, K, N, workspace, dev, stream)
+    _enqueue(fn, _FORWARD.pack(M, K, N, px, ldx, pw, ldw, w_layout, act, pb, pr, ldr, py, ldy, ty, 0, pz, ldz,
+                               *_drop(fn, dropout, dev), ws, nws), stream)
     return (y, preact) if both else y
 
 
@@ -242,24 +288,23 @@ def zero_linear_grad_input(dz, w, *, w_layout: int = ZERO_W_OUT_IN, act: int = Z
     """dx = D'(dz W) * act'(preact); ``preact`` and ``dropout`` are those of the
     layer below, whose output this layer's input was."""
     fn = "zero_linear_grad_input"
-    bf16 = torch.bfloat16
-    pd, ldd = _mat(fn, "dz", dz, bf16)
+    dev = _on_device(fn, "dz", dz)
+    pd, ldd = _mat(fn, "dz", dz, _BF16, dev)
     M, N = dz.shape
     if w.dim() != 2:
         _bad(fn, f"w has shape {tuple(w.shape)}")
     K = w.shape[1] if w_layout == ZERO_W_OUT_IN else w.shape[0]
-    pw, ldw = _weight(fn, w, w_layout, bf16, K, N)
+    pw, ldw = _weight(fn, "w", w, w_layout, _BF16, dev, K, N)
     if dx is None:
-        dx = _output(M, K, dtype or bf16, dz, stream)
+        dx = _new((M, K), dtype or _BF16, dev, stream)
     elif dtype is not None and dx.dtype is not dtype:
         _bad(fn, f"dx is {dx.dtype}, not {dtype}")
     ty = _type(fn, "dx", dx.dtype)
-    px, ldx = _mat(fn, "dx", dx, dx.dtype, M, K)
-    pz, ldz = _mat(fn, "preact", preact, bf16, M, K) if preact is not None else (None, 0)
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_INPUT, M, K, N, workspace, stream)
-    a = zero_linear_grad_input_args(M, K, N, pd, ldd, pw, ldw, w_layout, act, pz, ldz, px, ldx, ty, 0,
-                                    _drop(fn, dropout), ws, nws)
-    B._check(_lib().zero_linear_grad_input(a, _on(fn, stream)))
+    px, ldx = _mat(fn, "dx", dx, dx.dtype, dev, M, K)
+    pz, ldz = _mat(fn, "preact", preact, _BF16, dev, M, K) if preact is not None else (0, 0)
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_INPUT, M, K, N, workspace, dev, stream)
+    _enqueue(fn, _GRAD_INPUT.pack(M, K, N, pd, ldd, pw, ldw, w_layout, act, pz, ldz, px, ldx, ty, 0,
+                                  *_drop(fn, dropout, dev), ws, nws), stream)
     return dx
 
 
@@ -268,36 +313,36 @@ def zero_linear_grad_weight(dz, x, dw, dbias=None, *, w_layout: int = ZERO_W_OUT
     """dw [+]= dz^T x in the weight's layout, and dbias [+]= the column sums of dz;
     dw and dbias are bf16 or f32 (views of a flat gradient buffer)."""
     fn = "zero_linear_grad_weight"
-    bf16 = torch.bfloat16
-    pd, ldd = _mat(fn, "dz", dz, bf16)
+    dev = _on_device(fn, "dz", dz)
+    pd, ldd = _mat(fn, "dz", dz, _BF16, dev)
     M, N = dz.shape
-    px, ldx = _mat(fn, "x", x, bf16, M)
+    px, ldx = _mat(fn, "x", x, _BF16, dev, M)
     K = x.shape[1]
     ty = _type(fn, "dw", dw.dtype)
-    pw, ldw = _weight(fn, dw, w_layout, dw.dtype, K, N)
-    pb = _vec(fn, "dbias", dbias, dw.dtype, N) if dbias is not None else None
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_WEIGHT, M, K, N, workspace, stream)
-    a = zero_linear_grad_weight_args(M, K, N, pd, ldd, px, ldx, pw, ldw, pb, w_layout, ty, int(bool(accumulate)),
-                                     0, ws, nws)
-    B._check(_lib().zero_linear_grad_weight(a, _on(fn, stream)))
+    pw, ldw = _weight(fn, "dw", dw, w_layout, dw.dtype, dev, K, N)
+    pb = _vec(fn, "dbias", dbias, dw.dtype, dev, N) if dbias is not None else 0
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_WEIGHT, M, K, N, workspace, dev, stream)
+    _enqueue(fn, _GRAD_WEIGHT.pack(M, K, N, pd, ldd, px, ldx, pw, ldw, pb, w_layout, ty, 1 if accumulate else 0, 0,
+                                   ws, nws), stream)
 
 
 def zero_dropout_add(x, dropout: Optional[zero_dropout], *, residual=None, y=None, dtype=None, stream=None):
     """y = residual + D(x) over a matrix; y (and the residual) may be of another
     type than x."""
     fn = "zero_dropout_add"
+    dev = _on_device(fn, "x", x)
     tx = _type(fn, "x", x.dtype)
-    px, ldx = _mat(fn, "x", x, x.dtype)
+    px, ldx = _mat(fn, "x", x, x.dtype, dev)
     M, N = x.shape
     if y is None:
-        y = _output(M, N, dtype or (residual.dtype if residual is not None else x.dtype), x, stream)
+        y = _new((M, N), dtype or (residual.dtype if residual is not None else x.dtype), dev, stream)
     elif dtype is not None and y.dtype is not dtype:
         _bad(fn, f"y is {y.dtype}, not {dtype}")
     ty = _type(fn, "y", y.dtype)
-    py, ldy = _mat(fn, "y", y, y.dtype, M, N)
-    pr, ldr = _mat(fn, "residual", residual, y.dtype, M, N) if residual is not None else (None, 0)
-    a = zero_dropout_args(M, N, px, ldx, pr, ldr, None, 0, py, ldy, tx, ty, 0, 0, _drop(fn, dropout))
-    B._check(_lib().zero_dropout_add(a, _on(fn, stream)))
+    py, ldy = _mat(fn, "y", y, y.dtype, dev, M, N)
+    pr, ldr = _mat(fn, "residual", residual, y.dtype, dev, M, N) if residual is not None else (0, 0)
+    _enqueue(fn, _DROPOUT.pack(M, N, px, ldx, pr, ldr, 0, 0, py, ldy, tx, ty, 0, 0, *_drop(fn, dropout, dev)),
+             stream)
     return y
 
 
@@ -305,18 +350,19 @@ def zero_dropout_grad(dy, dropout: Optional[zero_dropout], *, act: int = ZERO_AC
                       dtype=None, stream=None):
     """dz = D'(dy) * act'(preact): the gradient of dropout behind an activation."""
     fn = "zero_dropout_grad"
+    dev = _on_device(fn, "dy", dy)
     tx = _type(fn, "dy", dy.dtype)
-    px, ldx = _mat(fn, "dy", dy, dy.dtype)
+    px, ldx = _mat(fn, "dy", dy, dy.dtype, dev)
     M, N = dy.shape
     if dz is None:
-        dz = _output(M, N, dtype or dy.dtype, dy, stream)
+        dz = _new((M, N), dtype or dy.dtype, dev, stream)
     elif dtype is not None and dz.dtype is not dtype:
         _bad(fn, f"dz is {dz.dtype}, not {dtype}")
     ty = _type(fn, "dz", dz.dtype)
-    py, ldy = _mat(fn, "dz", dz, dz.dtype, M, N)
-    pz, ldz = _mat(fn, "preact", preact, torch.bfloat16, M, N) if preact is not None else (None, 0)
-    a = zero_dropout_args(M, N, px, ldx, None, 0, pz, ldz, py, ldy, tx, ty, act, 0, _drop(fn, dropout))
-    B._check(_lib().zero_dropout_grad(a, _on(fn, stream)))
+    py, ldy = _mat(fn, "dz", dz, dz.dtype, dev, M, N)
+    pz, ldz = _mat(fn, "preact", preact, _BF16, dev, M, N) if preact is not None else (0, 0)
+    _enqueue(fn, _DROPOUT.pack(M, N, px, ldx, 0, 0, pz, ldz, py, ldy, tx, ty, act, 0, *_drop(fn, dropout, dev)),
+             stream)
     return dz
 
 
