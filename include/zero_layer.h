@@ -89,7 +89,7 @@ typedef struct {
 /*
  * Which product a workspace is for, and its size. The largest of a program's
  * calls serves all of them on one stream. 0 if none is needed (workspace_dev may
- * then be NULL); sizes out of range give 0.
+ * then be NULL); arguments out of range give 0.
  */
 typedef enum {
     ZERO_LINEAR_FORWARD = 0,
@@ -97,7 +97,7 @@ typedef enum {
     ZERO_LINEAR_GRAD_WEIGHT = 2
 } zero_linear_kind;
 
-size_t zero_linear_workspace_bytes(int32_t kind, int64_t M, int64_t K, int64_t N);
+size_t zero_linear_workspace_bytes(int32_t kind, int32_t w_layout, int64_t M, int64_t K, int64_t N);
 
 /*
  * y = residual + D(act(x W^T + bias)), and, if preact is given, preact = x W^T +

@@ -345,7 +345,7 @@ def test_streams_and_workspaces(Z):
     """Calls on two streams, with workspaces of their own, given or allocated."""
     rng = np.random.default_rng(12)
     M, K, N = 4096, 128, 192
-    need = Z.zero_linear_workspace_bytes(Z.ZERO_LINEAR_GRAD_WEIGHT, M, K, N)
+    need = Z.zero_linear_workspace_bytes(Z.ZERO_LINEAR_GRAD_WEIGHT, 0, M, K, N)
     assert need > 0
     data = [(inp(rng, M, N), inp(rng, M, K)) for _ in range(2)]
     want = []
@@ -400,7 +400,7 @@ def test_captured_calls_draw_anew(Z):
     z, dz, dx = torch.empty_like(y), torch.empty_like(y), torch.empty((M, K), dtype=BF, device=dev())
     dw = torch.zeros((N, K), dtype=F32, device=dev())
     db = torch.zeros(N, dtype=F32, device=dev())
-    ws = torch.empty(max(Z.zero_linear_workspace_bytes(k, M, K, N) for k in range(3)), dtype=torch.uint8,
+    ws = torch.empty(max(Z.zero_linear_workspace_bytes(k, 0, M, K, N) for k in range(3)), dtype=torch.uint8,
                      device=dev())
 
     def calls(drop, y, z, dz, dx, dw, db, ws):
@@ -508,3 +508,32 @@ def test_rounds_and_quarters(Z, M, K, N):
     close("dw", dw, want, err)
     want, err = R.column_sums(dz.f64())
     close("db", db, want, err)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("M,K,N", [(1, 768, 2304), (2, 2304, 768), (4, 4100, 515), (7, 71, 4096), (15, 640, 200),
+                                   (16, 4096, 1100), (16, 63, 17), (17, 768, 768), (1, 2, 3000), (3, 11008, 64)])
+def test_few_rows(Z, M, K, N, layout):
+    """One to seventeen rows: the products that are bound by the weights' bytes, with
+    the whole epilogue, whole and odd reductions, padded and odd rows."""
+    rng = np.random.default_rng(hash((17, M, K, N, layout)) % 2 ** 32)
+    for place in ((0, 0), (8, 0), (3, 1)):
+        x, w = inp(rng, M, K, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place)
+        b = torch.from_numpy(rand(rng, N)).to(dev()).to(BF)
+        res = inp(rng, M, N)
+        y, z = Mat(M, N, BF, ld=N + 5), Mat(M, N, BF, ld=N + 8)
+        say("few rows", M, K, N, layout, place)
+        Z.zero_linear_forward(x.t, w.t, b, w_layout=layout, act=3, dropout=Z.zero_dropout(0.25, 9, 8), residual=res.t,
+                              y=y.t, preact=z.t)
+        want, err, wz, ez = R.linear_forward(x.f64(), w64(w, layout), b.cpu().double().numpy(), act_name="silu", p=0.25,
+                                             seed=9, offset=8, residual=res.f64())
+        close("y", y.t, want, err)
+        close("z", z.t, wz, ez)
+        assert y.intact_outside() and z.intact_outside()
+        dz = inp(rng, M, N, pad_ld=place[0], shift=place[1])
+        zz = inp(rng, M, K)
+        dx = Mat(M, K, F32, ld=K + 3)
+        Z.zero_linear_grad_input(dz.t, w.t, w_layout=layout, act=2, preact=zz.t, dx=dx.t)
+        want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="gelu", z=zz.f64(), out="f32")
+        close("dx", dx.t, want, err)
+        assert dx.intact_outside()

@@ -182,12 +182,14 @@ def test_column_slices_of_one_buffer_do_not_overlap():
 
 
 def test_workspace_bytes():
-    assert Z.zero_linear_workspace_bytes(0, -1, 8, 8) == 0
-    assert Z.zero_linear_workspace_bytes(5, 8, 8, 8) == 0
-    assert Z.zero_linear_workspace_bytes(0, 0, 8, 8) == 0
+    assert Z.zero_linear_workspace_bytes(0, 0, -1, 8, 8) == 0
+    assert Z.zero_linear_workspace_bytes(5, 0, 8, 8, 8) == 0
+    assert Z.zero_linear_workspace_bytes(0, 2, 8, 4096, 8) == 0
+    assert Z.zero_linear_workspace_bytes(0, 0, 0, 8, 8) == 0
     for kind in range(3):
         for M, K, N in ((1, 768, 2304), (8192, 768, 768), (8192, 4096, 11008), (1, 1, 1), (7, 50257, 3)):
-            assert 0 <= Z.zero_linear_workspace_bytes(kind, M, K, N) < 1 << 28
+            for layout in range(2):
+                assert 0 <= Z.zero_linear_workspace_bytes(kind, layout, M, K, N) < 1 << 28
     with pytest.raises(Z.ZeroError):
         Z.zero_linear_forward(torch.zeros(2, 4), torch.zeros(3, 4))             # f32, on the CPU
     with pytest.raises(Z.ZeroError):

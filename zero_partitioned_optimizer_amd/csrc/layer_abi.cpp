@@ -150,25 +150,25 @@ Mat ws_mat(void* ws, size_t need) {
     return Mat{"workspace_dev", need ? ws : nullptr, 1, (int64_t)need, (int64_t)need, 1, true, false, true};
 }
 
-// Bytes of the weight gradient's product ([N, K] or [K, N], the larger of the two)
-// and, behind it, of the bias gradient.
-size_t weight_ws(int64_t M, int64_t K, int64_t N, size_t* product) {
-    const size_t a = zk::product_ws_bytes(N, K, M), b = zk::product_ws_bytes(K, N, M);
-    const size_t c = zk::sums_ws_bytes(N, K, M, true), d = zk::sums_ws_bytes(K, N, M, false);
-    *product = ((a > b ? a : b) + 15) & ~(size_t)15;
-    return *product + (c > d ? c : d);
+// Bytes of the weight gradient's product and, behind it, of the bias gradient.
+size_t weight_ws(bool oi, int64_t M, int64_t K, int64_t N, size_t* product) {
+    const int64_t P = oi ? N : K, Q = oi ? K : N;
+    *product = (zk::product_ws_bytes(P, Q, M, true, true) + 15) & ~(size_t)15;
+    return *product + zk::sums_ws_bytes(P, Q, M, oi);
 }
 
 }  // namespace
 
 extern "C" {
 
-size_t zero_linear_workspace_bytes(int32_t kind, int64_t M, int64_t K, int64_t N) {
+size_t zero_linear_workspace_bytes(int32_t kind, int32_t w_layout, int64_t M, int64_t K, int64_t N) {
     if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxDim) return 0;
+    if (w_layout != ZERO_W_OUT_IN && w_layout != ZERO_W_IN_OUT) return 0;
+    const bool oi = w_layout == ZERO_W_OUT_IN;
     size_t product;
-    if (kind == ZERO_LINEAR_FORWARD) return zk::product_ws_bytes(M, N, K);
-    if (kind == ZERO_LINEAR_GRAD_INPUT) return zk::product_ws_bytes(M, K, N);
-    if (kind == ZERO_LINEAR_GRAD_WEIGHT) return weight_ws(M, K, N, &product);
+    if (kind == ZERO_LINEAR_FORWARD) return zk::product_ws_bytes(M, N, K, false, !oi);
+    if (kind == ZERO_LINEAR_GRAD_INPUT) return zk::product_ws_bytes(M, K, N, false, oi);
+    if (kind == ZERO_LINEAR_GRAD_WEIGHT) return weight_ws(oi, M, K, N, &product);
     return 0;
 }
 
@@ -187,7 +187,7 @@ int zero_linear_forward(const zero_linear_args* args, void* stream) {
         return rc;
     const bool oi = a.w_layout == ZERO_W_OUT_IN;
     const int64_t ob = size_of(a.y_dtype);
-    const size_t need = zk::product_ws_bytes(a.M, a.N, a.K);
+    const size_t need = zk::product_ws_bytes(a.M, a.N, a.K, false, !oi);
     if (a.M == 0 || a.N == 0) return ZERO_OK;
     const Mat m[] = {{"x", a.x, a.M, a.K, a.ld_x, 2, false, false, false},
                      {"w", a.w, oi ? a.N : a.K, oi ? a.K : a.N, a.ld_w, 2, false, false, false},
@@ -237,7 +237,7 @@ int zero_linear_grad_input(const zero_linear_grad_input_args* args, void* stream
         return rc;
     const bool oi = a.w_layout == ZERO_W_OUT_IN;
     const bool act = a.act != ZERO_ACT_NONE;
-    const size_t need = zk::product_ws_bytes(a.M, a.K, a.N);
+    const size_t need = zk::product_ws_bytes(a.M, a.K, a.N, false, oi);
     if (a.M == 0 || a.K == 0) return ZERO_OK;
     const Mat m[] = {{"dz", a.dz, a.M, a.N, a.ld_dz, 2, false, false, false},
                      {"w", a.w, oi ? a.N : a.K, oi ? a.K : a.N, a.ld_w, 2, false, false, false},
@@ -281,7 +281,7 @@ int zero_linear_grad_weight(const zero_linear_grad_weight_args* args, void* stre
     const bool oi = a.w_layout == ZERO_W_OUT_IN;
     const int64_t gb = size_of(a.grad_dtype);
     size_t product;
-    size_t need = weight_ws(a.M, a.K, a.N, &product);
+    size_t need = weight_ws(oi, a.M, a.K, a.N, &product);
     if (!a.dbias) need = product;
     if (a.N == 0) return ZERO_OK;
     const Mat m[] = {{"dz", a.dz, a.M, a.N, a.ld_dz, 2, false, false, false},

@@ -52,7 +52,7 @@ struct ProductDesc {
 
 // Workspace bytes that launch_product needs for a product of these sizes, and
 // for the bias gradient beside it.
-size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R);
+size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb);
 size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a);
 hipError_t launch_product(const ProductDesc& d, hipStream_t st);
 

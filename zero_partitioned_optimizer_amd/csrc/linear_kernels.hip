@@ -106,7 +106,7 @@ template <int ROWS, bool T, int THREADS>
 __device__ __forceinline__ void stage_tail(uint16_t* lds, const uint16_t* src, int64_t ld, int64_t o0, int64_t O,
                                            int64_t r0, int64_t r1) {
 #pragma unroll 1
-    for (int id = threadIdx.x; id < ROWS * kBR / 8; id += THREADS)
+    for (int id = threadIdx.x % THREADS; id < ROWS * kBR / 8; id += THREADS)
         put_chunk<ROWS, T>(lds, id, tile_chunk<ROWS, T>(id, src, ld, o0, O, r0, r1));
 }
 
@@ -225,7 +225,7 @@ struct Direct {
         for (int h = 0; h < PARTS; ++h)
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int id = threadIdx.x + i * THREADS;
+                const int id = threadIdx.x % THREADS + i * THREADS;
                 if constexpr (T) {
                     const int r = id / (ROWS / 8);
                     int64_t c = ROWS * h + 8 * ((id % (ROWS / 8)) ^ perm_reduced<ROWS>(r));
@@ -668,6 +668,131 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
                                 [&](int j) { return q0 + H * (j >> 1) + wq + 16 * (j & 1); });
 }
 
+// Products of at most 16 rows, bound by reading b once: a workgroup takes 16 columns
+// (b's outer index in rows; 32 were slower, 21.9 against 17.4 us on one row of a
+// Llama-7B shaped layer, with half the workgroups in flight) or 64 (reduced rows), its eight waves each an eighth of
+// the reduction, and their sums are joined in LDS, so that one launch streams b with
+// everything in flight and nothing goes through memory again. Waves do not wait for
+// each other before that. Operand a is read straight into the matrix instruction's
+// layout by every wave, and b too, where r is contiguous; reduced rows of b, and a
+// with them, go through the wave's own part of LDS, two tiles of 64 in turn.
+template <bool TB, int EPI>
+__global__ void __launch_bounds__(512) k_product_few(const ProductArgs g) {
+    constexpr int kWaves = 8, FQ = TB ? 4 : 1, kCols = 16 * FQ, kTile = (64 + 16) * kBR;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[TB ? kWaves * 2 * kTile : kWaves * 16 * kCols * 2];
+    const ProductDesc& d = g.d;
+    const int lane = threadIdx.x & 63, i = lane & 15, gr = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t q0 = (int64_t)blockIdx.x * kCols;
+    // this wave's tiles of 64 reduction elements, the last of all perhaps partial
+    const int tiles = (int)((d.R + kBR - 1) / kBR), whole = (int)(d.R / kBR);
+    const int t0 = (int)((int64_t)tiles * wave / kWaves), t1 = (int)((int64_t)tiles * (wave + 1) / kWaves);
+    const int tw = t1 < whole ? t1 : whole;
+    const uint16_t* const arow = d.a + (i < d.P ? i : d.P - 1) * d.lda + 8 * gr;
+    v4f acc[FQ];
+#pragma unroll
+    for (int j = 0; j < FQ; ++j) acc[j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const auto mul = [&](v8bf b, v4u a, v4f c) {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, __builtin_bit_cast(v8bf, a), c, 0, 0, 0);
+    };
+    const auto left = [&](int64_t r) { return (int)(d.R - r < 0 ? 0 : d.R - r < 8 ? d.R - r : 8); };
+
+    if constexpr (!TB) {
+        const int64_t q = q0 + i;
+        const uint16_t* const brow = d.b + (q < d.Q ? q : d.Q - 1) * d.ldb + 8 * gr;
+        int t = t0;
+        for (; t + 3 < tw; t += 4) {
+            v4u a[8], b[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) b[k] = chunk_load(brow + (int64_t)t * kBR + 32 * k, 8);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) a[k] = chunk_load(arow + (int64_t)t * kBR + 32 * k, 8);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) acc[0] = mul(__builtin_bit_cast(v8bf, b[k]), a[k], acc[0]);
+        }
+        for (; t < t1; ++t) {
+            const int64_t r = (int64_t)t * kBR;
+            v4u a[2], b[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int n = left(r + 32 * k + 8 * gr);
+                b[k] = n > 0 ? chunk_load(brow + r + 32 * k, n) : v4u{0, 0, 0, 0};
+                a[k] = n > 0 ? chunk_load(arow + r + 32 * k, n) : v4u{0, 0, 0, 0};
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) acc[0] = mul(__builtin_bit_cast(v8bf, b[k]), a[k], acc[0]);
+        }
+    } else {
+        uint16_t* const mine = lds + wave * 2 * kTile;
+        const uint32_t base = lds_address(mine);
+        const Fragments<64, true> gb(0);
+        const Fragments<16, false> ga(0);
+        Direct<64, true, 64, 1> db;
+        Direct<16, false, 64, 1> da;
+        constexpr int kLoads = Direct<64, true, 64, 1>::kLoads + Direct<16, false, 64, 1>::kLoads;
+        const auto load = [&](uint32_t tile) {
+            db.issue(0, db.base, tile, 0, kAllRecords);
+            da.issue(0, da.base, tile + 2 * 64 * kBR, 0, kAllRecords);
+            db.base += db.step;
+            da.base += da.step;
+        };
+        const auto multiply = [&](uint32_t tile) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const v4u a = __builtin_bit_cast(v4u, ga.get(tile + 2 * 64 * kBR, 0, k));
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) acc[j] = mul(gb.get(tile, j, k), a, acc[j]);
+            }
+            // read, before the next turn's loads write here
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+        };
+        if (t0 < tw) {
+            db.init(d.b, d.ldb, q0, d.Q, (int64_t)t0 * kBR);
+            da.init(d.a, d.lda, 0, d.P, (int64_t)t0 * kBR);
+            load(base);
+        }
+        for (int t = t0; t < tw; ++t) {
+            if (t + 1 < tw) {
+                load(base + 2 * kTile * ((t + 1 - t0) & 1));
+                loads_landed<kLoads>();
+            } else {
+                loads_landed<0>();
+            }
+            multiply(base + 2 * kTile * ((t - t0) & 1));
+        }
+        if (tw < t1) {
+            stage_tail<64, true, 64>(mine, d.b, d.ldb, q0, d.Q, (int64_t)tw * kBR, d.R);
+            stage_tail<16, false, 64>(mine + 64 * kBR, d.a, d.lda, 0, d.P, (int64_t)tw * kBR, d.R);
+            asm volatile("s_waitcnt lgkmcnt(0)" : : : "memory");
+            multiply(base);
+        }
+        meet_waves();
+    }
+
+    // [wave][row p][column]: a lane holds columns 16 j + 4 gr .. + 3 of row i
+    float* const sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < FQ; ++j)
+        *reinterpret_cast<v4f*>(sums + (wave * 16 + i) * kCols + 16 * j + 4 * gr) = acc[j];
+    __syncthreads();
+    const int p = threadIdx.x / (kCols / 8), c = threadIdx.x % (kCols / 8);
+    const int64_t q = q0 + 8 * c;
+    if (p >= 16 || p >= d.P || q >= d.Q) return;
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+    for (int w = 0; w < kWaves; ++w) {
+        const v4f lo = *reinterpret_cast<const v4f*>(sums + (w * 16 + p) * kCols + 8 * c);
+        const v4f hi = *reinterpret_cast<const v4f*>(sums + (w * 16 + p) * kCols + 8 * c + 4);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] += lo[k];
+            v[4 + k] += hi[k];
+        }
+    }
+    epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, d.Q - q < 8 ? (int)(d.Q - q) : 8);
+}
+
 // Joins the splits of a long reduction in their order, then the epilogue, eight
 // columns of one row per thread; and, in the workgroups behind those, the rows of
 // partial sums of the bias gradient, 64 columns to a workgroup, its four waves on
@@ -764,6 +889,19 @@ static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
     return best;
 }
 
+// Whether a product of few rows goes to k_product_few. With b's outer index in rows:
+// up to 4 rows always (one row of GPT-2 qkv 8.2 -> 3.3 us, of a Llama-7B shaped layer
+// 19.9 -> 17.4 us against tiles, splits and a join), up to 16 below 32 MB of b (every
+// workgroup reads all of a: 16 rows of the Llama-7B shaped layer 20.5 -> 23.6 us). With
+// reduced rows, 64 columns to a workgroup: where its workgroups' share of memory
+// (55 KB/us each) beats the join's launch and traffic.
+static bool few(int64_t P, int64_t Q, int64_t R, bool tb) {
+    if (P < 1 || P > 16 || Q < 1) return false;
+    if (!tb) return P <= 4 || 2 * Q * R < (int64_t(32) << 20);
+    const double bytes = 2.0 * Q * R, groups = (double)((Q + 63) / 64);
+    return bytes / ((groups < 256 ? groups : 256) * 55e3) < 5 + bytes / 6e6;
+}
+
 static int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 static size_t part_bytes(const Plan& pl, int64_t P, int64_t Q) {
     return pl.splits > 1 ? (size_t)pl.splits * (size_t)P * (size_t)up8(Q) * sizeof(float) : 0;
@@ -773,7 +911,8 @@ static int32_t sum_rows(const Plan& pl, int64_t other) {
     return pl.splits * (int32_t)((other + (pl.wide ? 255 : 127)) / (pl.wide ? 256 : 128));
 }
 
-size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R) {
+size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb) {
+    if (!ta && !tb && few(P, Q, R, tb)) return 0;       // at any alignment
     size_t most = 0;
     for (int direct = 0; direct < 2; ++direct) {
         const size_t b = part_bytes(plan_of(P, Q, R, direct != 0), P, Q);
@@ -797,6 +936,14 @@ static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
 
 template <bool TA, bool TB, int EPI>
 static hipError_t product(const ProductDesc& d, hipStream_t st) {
+    if constexpr (!TA)
+        if (few(d.P, d.Q, d.R, TB) && (!TB || (direct_ok(d.b, d.ldb, d.R) && direct_ok(d.a, d.lda, d.P)))) {
+            ProductArgs g{};
+            g.d = d;
+            const int cols = TB ? 64 : 16;
+            hipLaunchKernelGGL((k_product_few<TB, EPI>), dim3((unsigned)((d.Q + cols - 1) / cols)), dim3(512), 0, st, g);
+            return hipGetLastError();
+        }
     const bool some = d.P > 0 && d.Q > 0;
     if (!some && !d.bias_out) return hipSuccess;
     const bool direct = some && direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);

@@ -111,7 +111,7 @@ def _lib() -> ctypes.CDLL:
             getattr(L, name).restype = ctypes.c_int
             # the same entry point, for an argument block that is packed already
             _call[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp)((name, L))
-        L.zero_linear_workspace_bytes.argtypes = [i32, i64, i64, i64]
+        L.zero_linear_workspace_bytes.argtypes = [i32, i32, i64, i64, i64]
         L.zero_linear_workspace_bytes.restype = sz
         _declared = L
     return _declared
@@ -198,12 +198,12 @@ def _drop(fn: str, dropout, device: int):
 
 
 @functools.lru_cache(maxsize=4096)
-def _workspace_need(kind: int, M: int, K: int, N: int) -> int:
-    return int(_lib().zero_linear_workspace_bytes(kind, M, K, N))
+def _workspace_need(kind: int, w_layout: int, M: int, K: int, N: int) -> int:
+    return int(_lib().zero_linear_workspace_bytes(kind, w_layout, M, K, N))
 
 
-def zero_linear_workspace_bytes(kind: int, M: int, K: int, N: int) -> int:
-    return _workspace_need(int(kind), int(M), int(K), int(N))
+def zero_linear_workspace_bytes(kind: int, w_layout: int, M: int, K: int, N: int) -> int:
+    return _workspace_need(int(kind), int(w_layout), int(M), int(K), int(N))
 
 
 def _new(shape, dtype, device: int, stream):
@@ -223,7 +223,7 @@ def _cuda(device: int) -> torch.device:
     return torch.device("cuda", device)
 
 
-def _workspace(fn: str, kind: int, M: int, K: int, N: int, given, device: int, stream):
+def _workspace(fn: str, kind: int, w_layout: int, M: int, K: int, N: int, given, device: int, stream):
     """(address, bytes, tensor) of a call's workspace."""
     if given is not None:
         if given.get_device() != device:
@@ -231,7 +231,7 @@ def _workspace(fn: str, kind: int, M: int, K: int, N: int, given, device: int, s
         if not given.is_contiguous():
             _bad(fn, "workspace is not contiguous")
         return given.data_ptr(), given.numel() * given.element_size(), given
-    need = _workspace_need(kind, M, K, N)
+    need = _workspace_need(kind, w_layout, M, K, N)
     if need == 0:
         return 0, 0, None
     ws = _new(need, torch.uint8, device, stream)
@@ -276,7 +276,7 @@ def zero_linear_forward(x, w, bias=None, *, w_layout: int = ZERO_W_OUT_IN, act: 
         pz, ldz = _mat(fn, "preact", preact, _BF16, dev, M, N)
     if bias is not None:
         pb = _vec(fn, "bias", bias, _BF16, dev, N)
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_FORWARD, M, K, N, workspace, dev, stream)
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_FORWARD, w_layout, M, K, N, workspace, dev, stream)
     _enqueue(fn, _FORWARD.pack(M, K, N, px, ldx, pw, ldw, w_layout, act, pb, pr, ldr, py, ldy, ty, 0, pz, ldz,
                                *_drop(fn, dropout, dev), ws, nws), stream)
     return (y, preact) if both else y
@@ -302,7 +302,7 @@ def zero_linear_grad_input(dz, w, *, w_layout: int = ZERO_W_OUT_IN, act: int = Z
     ty = _type(fn, "dx", dx.dtype)
     px, ldx = _mat(fn, "dx", dx, dx.dtype, dev, M, K)
     pz, ldz = _mat(fn, "preact", preact, _BF16, dev, M, K) if preact is not None else (0, 0)
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_INPUT, M, K, N, workspace, dev, stream)
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_INPUT, w_layout, M, K, N, workspace, dev, stream)
     _enqueue(fn, _GRAD_INPUT.pack(M, K, N, pd, ldd, pw, ldw, w_layout, act, pz, ldz, px, ldx, ty, 0,
                                   *_drop(fn, dropout, dev), ws, nws), stream)
     return dx
@@ -321,7 +321,7 @@ def zero_linear_grad_weight(dz, x, dw, dbias=None, *, w_layout: int = ZERO_W_OUT
     ty = _type(fn, "dw", dw.dtype)
     pw, ldw = _weight(fn, "dw", dw, w_layout, dw.dtype, dev, K, N)
     pb = _vec(fn, "dbias", dbias, dw.dtype, dev, N) if dbias is not None else 0
-    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_WEIGHT, M, K, N, workspace, dev, stream)
+    ws, nws, keep = _workspace(fn, ZERO_LINEAR_GRAD_WEIGHT, w_layout, M, K, N, workspace, dev, stream)
     _enqueue(fn, _GRAD_WEIGHT.pack(M, K, N, pd, ldd, px, ldx, pw, ldw, pb, w_layout, ty, 1 if accumulate else 0, 0,
                                    ws, nws), stream)
 
