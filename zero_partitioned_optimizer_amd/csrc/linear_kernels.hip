@@ -86,16 +86,39 @@ __device__ __forceinline__ void put_chunk(uint16_t* lds, int id, v4u w) {
 }
 
 // A tile through registers into LDS: all of a thread's chunks loaded, then stored
-// (Stage), or one at a time where registers are short (stage_tail).
+// (Stage), or one at a time where registers are short (stage_tail). A whole tile's
+// rows outside the operand read its last one instead, as they reach no output; only
+// a chunk of reduced rows that the operand's edge cuts is loaded by elements.
 template <int ROWS, bool T, int THREADS>
 struct Stage {
     static constexpr int kChunks = ROWS * kBR / 8 / THREADS;
     v4u w[kChunks];
-    __device__ __forceinline__ void load(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0,
-                                         int64_t r1) {
+    const uint16_t* from[kChunks];
+    int n[kChunks];
+    int64_t step;
+    __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0) {
+        step = T ? kBR * ld : kBR;
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i)
-            w[i] = tile_chunk<ROWS, T>(threadIdx.x + i * THREADS, src, ld, o0, O, r0, r1);
+        for (int i = 0; i < kChunks; ++i) {
+            const int id = threadIdx.x + i * THREADS;
+            if constexpr (T) {
+                const int64_t row = r0 + id / (ROWS / 8), col = o0 + 8 * (id % (ROWS / 8));
+                n[i] = O - col >= 8 ? 8 : O - col > 0 ? (int)(O - col) : 0;
+                from[i] = src + row * ld + (n[i] > 0 ? col : 0);
+            } else {
+                int64_t row = o0 + id / (kBR / 8);
+                if (row >= O) row = O - 1;
+                from[i] = src + row * ld + r0 + 8 * (id % (kBR / 8));
+                n[i] = 8;
+            }
+        }
+    }
+    __device__ __forceinline__ void load() {
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            w[i] = !T || n[i] > 0 ? chunk_load(from[i], n[i]) : v4u{0, 0, 0, 0};
+            from[i] += step;
+        }
     }
     __device__ __forceinline__ void store(uint16_t* lds) const {
 #pragma unroll
@@ -356,8 +379,7 @@ __device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP
 template <bool TA, bool TB, int EPI, bool DIRECT, bool SUM>
 __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
-    constexpr int kBufs = DIRECT ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) uint16_t lds[kBufs * 2 * kTile];
+    __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 2 * kTile];
     const ProductDesc& d = g.d;
     int tp, tq, np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
     if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
@@ -448,22 +470,42 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
             multiply(base + 4 * kTile * (full & 1));
         }
     } else {
+        // the next tile waits in registers while one is multiplied
+        const int full = whole_steps(g);
         Stage<B, TA, T> sa;
         Stage<B, TB, T> sb;
-        if (r0 < r1) {
-            sa.load(d.a, d.lda, p0, d.P, r0, r1);
-            sb.load(d.b, d.ldb, q0, d.Q, r0, r1);
-        }
-        for (int64_t r = r0; r < r1; r += kBR) {
-            __syncthreads();
+        if (full > 0) {
+            sa.init(d.a, d.lda, p0, d.P, r0);
+            sb.init(d.b, d.ldb, q0, d.Q, r0);
+            sa.load();
+            sb.load();
             sa.store(lds);
             sb.store(lds + kTile);
-            __syncthreads();
-            if (r + kBR < r1) {
-                sa.load(d.a, d.lda, p0, d.P, r + kBR, r1);
-                sb.load(d.b, d.ldb, q0, d.Q, r + kBR, r1);
+            if (full > 1) {
+                sa.load();
+                sb.load();
             }
-            multiply(base);
+        }
+        for (int k = 0; k < full; ++k) {
+            meet_waves();
+            if (k + 1 < full) {
+                uint16_t* const to = lds + 2 * kTile * ((k + 1) & 1);
+                sa.store(to);
+                sb.store(to + kTile);
+                if (k + 2 < full) {
+                    sa.load();
+                    sb.load();
+                }
+            }
+            multiply(base + 4 * kTile * (k & 1));
+        }
+        if (r0 + (int64_t)full * kBR < r1) {
+            const int64_t r = r0 + (int64_t)full * kBR;
+            uint16_t* const to = lds + 2 * kTile * (full & 1);
+            stage_tail<B, TA, T>(to, d.a, d.lda, p0, d.P, r, r1);
+            stage_tail<B, TB, T>(to + kTile, d.b, d.ldb, q0, d.Q, r, r1);
+            meet_waves();
+            multiply(base + 4 * kTile * (full & 1));
         }
     }
     meet_waves();
