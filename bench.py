@@ -367,6 +367,81 @@ def gather_bench(args, Z, W, w, S) -> int:
     return 0
 
 
+def layer_bench(args, Z, W, w) -> int:
+    """The MLP of one of the workload's layers, forward and backward, with libzero's
+    layer operators: fetch its tensors out of the N rank shards, y = residual +
+    D(act(x W1 + b1) W2 + b2) over args.tokens rows, then the gradients of both
+    layers into a flat bf16 gradient buffer at their tensors' offsets and the
+    gradient by x. Six products, 12 * tokens * inner * outer floating-point
+    operations. GPT-2: GELU, biases, dropout 0.1; Llama: SiLU, none of them (the up
+    and down layers, without the gate)."""
+    import torch
+    dev = torch.device("cuda:0")
+    gpt2 = w.name == "gpt2s"
+    first, last = W.first_layer_tensor(w.name), W.first_layer_tensor(w.name) + W.layer_tensor_count(w.name)
+    h = Z.zero_layout_build(list(w.numels[:last]), w.N, 8, w.B)     # the tensors up to the first layer's end
+    try:
+        S, offsets = Z.zero_layout_info_get(h).shard_S, Z.zero_layout_offsets(h)
+    finally:
+        Z.zero_layout_free(h)
+    numels = list(w.numels[:last])
+    d = numels[last - 1] if gpt2 else numels[first]                  # a bias or a norm's weight: the model's width
+    up, down = (last - 4, last - 2) if gpt2 else (last - 2, last - 1)
+    inner = numels[up] // d
+    layout = Z.ZERO_W_IN_OUT if gpt2 else Z.ZERO_W_OUT_IN
+    base = offsets[up]
+    span = offsets[last - 1] + numels[last - 1] - base
+    l1 = Z.FlatLinear(offsets, numels, up, up + 1 if gpt2 else None, d, inner, w_layout=layout,
+                      act=Z.ZERO_ACT_GELU if gpt2 else Z.ZERO_ACT_SILU)
+    l2 = Z.FlatLinear(offsets, numels, down, down + 1 if gpt2 else None, inner, d, w_layout=layout)
+    M = args.tokens
+    gen = torch.Generator(device=dev)
+    gen.manual_seed(w.seed)
+
+    def rand(*shape, scale):
+        return (torch.randn(*shape, generator=gen, device=dev) * scale).to(torch.bfloat16)
+
+    shards = [rand(S, scale=w.param_sigma).view(torch.int16) for _ in range(w.N)]
+    x, dy = rand(M, d, scale=1.0), rand(M, d, scale=w.grad_sigma)
+    grads = torch.zeros(base + span, dtype=torch.bfloat16, device=dev)
+    counter = torch.zeros(1, dtype=torch.int64, device=dev)
+    drop = Z.zero_dropout(0.1, w.seed, 0, counter) if gpt2 else None
+
+    def run():
+        l1.fetch(shards, S)
+        l2.fetch(shards, S)
+        a, z = l1.forward(x)
+        l2.forward(a, dropout=drop, residual=x)
+        d2 = Z.zero_dropout_grad(dy, drop) if gpt2 else dy
+        dz = l2.backward(d2, a, grads, below=(l1.act, z, None))
+        l1.backward(dz, x, grads)
+        counter.add_(1)
+
+    for _ in range(max(1, args.warmup)):
+        run()
+    torch.cuda.synchronize()
+    t0 = time.perf_counter()
+    for _ in range(args.steps):
+        run()
+    torch.cuda.synchronize()
+    s = (time.perf_counter() - t0) / args.steps
+    tf = 12.0 * M * d * inner / s / 1e12
+    log(f"layer: {M} tokens, {d} x {inner}: {s * 1e3:.3f} ms per pass, {tf:.0f} TFLOP/s")
+    out = {
+        "metric": "MLP of one layer, fetch + forward + backward: TFLOP/s of its six products",
+        "value": tf, "unit": "TFLOP/s", "n_gpus": 1, "steps": args.steps, "warmup": args.warmup,
+        "ms_per_step": s * 1e3, "higher_is_better": True, "scaling": "weak", "vs_baseline": None,
+        "dtype": "bf16", "data": "synthetic",
+        "config": {"workload": f"{w.name} layer", "tokens": M, "width": d, "inner": inner,
+                   "n_shards": w.N, "dropout": 0.1 if gpt2 else 0.0},
+        "roofline": {"bound": "mfma", "achieved": tf, "peak": 2500.0, "unit": "TFLOP/s", "frac": tf / 2500.0,
+                     "traffic": None},
+        "cpu_baseline": None,
+    }
+    print(json.dumps(out), flush=True)
+    return 0
+
+
 def graph_bench(args, w, S, step, reps) -> int:
     """G device-commit steps captured in one HIP graph, replayed back to back: the
     step rate with no host work per step. Every step reads the committed-state
@@ -563,6 +638,10 @@ def main() -> int:
     ap.add_argument("--gather", action="store_true",
                     help="instead of the default line: time the stage-3 fetch (whole tensors out "
                          "of the N bf16 rank shards) for one transformer layer and for the model")
+    ap.add_argument("--layer", action="store_true",
+                    help="time the MLP of one layer (gpt2s, llama7b), fetch, forward and backward, with the "
+                         "layer operators instead of the step")
+    ap.add_argument("--tokens", type=int, default=8192, help="rows of the --layer mode's activations")
     ap.add_argument("--flush-mall", action="store_true",
                     help="write a 1 GiB buffer before every timed step so no step finds its data "
                          "in the 256 MB Infinity Cache; `value` then comes from the step kernels' "
@@ -579,6 +658,10 @@ def main() -> int:
     if args.graph and (args.commit != "device" or args.flush_mall or args.overlap or args.offload
                        or args.gather):
         print("--graph times device-commit steps alone", file=sys.stderr)
+        return 2
+
+    if args.layer and (args.config not in ("gpt2s", "llama7b") or args.tokens < 1):
+        print("--layer times a layer of gpt2s or llama7b over at least one token", file=sys.stderr)
         return 2
 
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -602,6 +685,8 @@ def main() -> int:
     if args.seed is not None:
         import dataclasses
         w = dataclasses.replace(w, seed=int(args.seed))
+    if args.layer:
+        return layer_bench(args, Z, W, w)
     gdt = Z.ZERO_BF16 if w.grad_dtype == "bf16" else Z.ZERO_F32
     wire = args.fold == "bf16-wire"
     if wire:
