@@ -171,17 +171,65 @@ struct Fragments {
     }
 };
 
-// The epilogue of eight consecutive columns q .. of row p; n of them exist.
+// The epilogue of eight consecutive columns q .. of row p; n of them exist. What it
+// reads beside the sums is asked for in one part (EpilogueIn::load), used in another,
+// so that a wave has several rows' loads under way.
+struct EpilogueIn {
+    v4u lo, hi;                     // the residual, old value (f32: both) or pre-activation
+
+    __device__ __forceinline__ void load_bf(const uint16_t* p, int n) { lo = chunk_load(p, n); }
+    __device__ __forceinline__ void load_f(const float* p, int n) {
+        if (n >= 8) {
+            lo = *reinterpret_cast<const v4u_any*>(p);
+            hi = *reinterpret_cast<const v4u_any*>(p + 4);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                lo[k] = k < n ? __float_as_uint(p[k]) : 0;
+                hi[k] = 4 + k < n ? __float_as_uint(p[4 + k]) : 0;
+            }
+        }
+    }
+    template <int EPI>
+    __device__ __forceinline__ void load(const ProductDesc& d, int64_t p, int64_t q, int n) {
+        if constexpr (EPI == kEpiGradInput) {
+            if (d.z_in) load_bf(d.z_in + p * d.ld_z + q, n);
+        } else if (d.res) {
+            if (d.out_f32) load_f(static_cast<const float*>(d.res) + p * d.ld_res + q, n);
+            else load_bf(static_cast<const uint16_t*>(d.res) + p * d.ld_res + q, n);
+        }
+    }
+    __device__ __forceinline__ void get_bf(float t[8]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            t[2 * k] = bf_lo(lo[k]);
+            t[2 * k + 1] = bf_hi(lo[k]);
+        }
+    }
+    __device__ __forceinline__ void get_f(float t[8]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            t[k] = __uint_as_float(lo[k]);
+            t[4 + k] = __uint_as_float(hi[k]);
+        }
+    }
+};
+
+// Columns q .. of the bias, the same for every row.
+__device__ __forceinline__ void epilogue_bias(const ProductDesc& d, int64_t q, int n, float b[8]) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) b[k] = 0.0f;
+    if (d.bias && n > 0) load8_bf(b, d.bias + q, n);
+}
+
 template <int EPI>
-__device__ __forceinline__ void epilogue8(const ProductDesc& d, uint64_t off, int64_t p, int64_t q,
-                                          float v[8], int n) {
+__device__ __forceinline__ void epilogue8(const ProductDesc& d, uint64_t off, int64_t p, int64_t q, float v[8],
+                                          const EpilogueIn& in, const float bias[8], int n) {
     float t[8];
     if constexpr (EPI == kEpiForward) {
-        if (d.bias) {
-            load8_bf(t, d.bias + q, n);
+        if (d.bias)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += t[k];
-        }
+            for (int k = 0; k < 8; ++k) v[k] += bias[k];
         if (d.z_out) store8_bf(d.z_out + p * d.ld_z + q, v, n);
         if (d.act != ZERO_ACT_NONE)
 #pragma unroll
@@ -190,15 +238,14 @@ __device__ __forceinline__ void epilogue8(const ProductDesc& d, uint64_t off, in
     }
     if constexpr (EPI == kEpiGradInput) {
         if (d.z_in) {
-            load8_bf(t, d.z_in + p * d.ld_z + q, n);
+            in.get_bf(t);
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] *= act_slope(d.act, t[k]);
         }
         if (d.drop.thr) drop8(v, d.drop, off, (uint32_t)p, (uint32_t)(q >> 3));
-    }
-    if (d.res) {
-        if (d.out_f32) load8_f(t, static_cast<const float*>(d.res) + p * d.ld_res + q, n);
-        else load8_bf(t, static_cast<const uint16_t*>(d.res) + p * d.ld_res + q, n);
+    } else if (d.res) {
+        if (d.out_f32) in.get_f(t);
+        else in.get_bf(t);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += t[k];
     }
@@ -347,6 +394,12 @@ __device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP
     const int lane = threadIdx.x & 63;
     const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
     float* const mine = reinterpret_cast<float*>(lds) + wave * kRun * 16 * 64;
+    const int c = lane & 7;
+    const int64_t q = col_of(c >> 1) + 8 * (c & 1);
+    const int n = d.Q - q >= 8 ? 8 : d.Q - q > 0 ? (int)(d.Q - q) : 0;
+    float bias[8];
+    epilogue_bias(d, q, g.part ? 0 : n, bias);
+    static_assert(kRun % 2 == 0, "whole groups of four rows a lane");
 #pragma unroll
     for (int i0 = 0; i0 < FP; i0 += kRun) {
 #pragma unroll
@@ -356,18 +409,27 @@ __device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP
                 const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
                 *reinterpret_cast<v4f*>(mine + o * 64 + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
             }
-        const int c = lane & 7;
-        const int64_t q = col_of(c >> 1) + 8 * (c & 1);
+        // four rows of each lane at a time
 #pragma unroll 1
-        for (int o = lane >> 3; o < 16 * kRun; o += 8) {
-            const v4f lo = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c) ^ (o & 15)));
-            const v4f hi = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c + 1) ^ (o & 15)));
-            float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-            const int64_t p = row_of(i0) + o;
-            if (p >= d.P || q >= d.Q) continue;
-            const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
-            if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
-            else epilogue8<EPI>(d, off, p, q, v, n);
+        for (int o0 = lane >> 3; o0 < 16 * kRun; o0 += 32) {
+            EpilogueIn in[4];
+            if (!g.part)
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int64_t p = row_of(i0) + o0 + 8 * u;
+                    if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int o = o0 + 8 * u;
+                const int64_t p = row_of(i0) + o;
+                const v4f lo = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c) ^ (o & 15)));
+                const v4f hi = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c + 1) ^ (o & 15)));
+                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+                if (p >= d.P || n <= 0) continue;
+                if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
+                else epilogue8<EPI>(d, off, p, q, v, in[u], bias, n);
+            }
         }
     }
 }
@@ -820,9 +882,11 @@ __global__ void __launch_bounds__(512) k_product_few(const ProductArgs g) {
     const int p = threadIdx.x / (kCols / 8), c = threadIdx.x % (kCols / 8);
     const int64_t q = q0 + 8 * c;
     if (p >= 16 || p >= d.P || q >= d.Q) return;
+    const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
     float v[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) v[k] = 0.0f;
+#pragma unroll 2
     for (int w = 0; w < kWaves; ++w) {
         const v4f lo = *reinterpret_cast<const v4f*>(sums + (w * 16 + p) * kCols + 8 * c);
         const v4f hi = *reinterpret_cast<const v4f*>(sums + (w * 16 + p) * kCols + 8 * c + 4);
@@ -832,7 +896,11 @@ __global__ void __launch_bounds__(512) k_product_few(const ProductArgs g) {
             v[4 + k] += hi[k];
         }
     }
-    epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, d.Q - q < 8 ? (int)(d.Q - q) : 8);
+    EpilogueIn in;
+    in.template load<EPI>(d, p, q, n);
+    float bias[8];
+    epilogue_bias(d, q, n, bias);
+    epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, in, bias, n);
 }
 
 // Joins the splits of a long reduction in their order, then the epilogue, eight
@@ -867,7 +935,11 @@ __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
     const int64_t groups = g.ld_part / 8, id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t p = id / groups, q = 8 * (id % groups);
     if (p >= d.P) return;
-    float v[8], t[8];
+    const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
+    EpilogueIn in;
+    in.template load<EPI>(d, p, q, n);
+    float v[8], t[8], bias[8];
+    epilogue_bias(d, q, n, bias);
     load8_f(v, g.part + p * g.ld_part + q, 8);
 #pragma unroll 4
     for (int s = 1; s < g.splits; ++s) {
@@ -875,8 +947,7 @@ __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] += t[k];
     }
-    const int n = d.Q - q < 8 ? (int)(d.Q - q) : 8;
-    epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, n);
+    epilogue8<EPI>(d, d.drop.thr ? drop_offset(d.drop) : 0, p, q, v, in, bias, n);
 }
 
 // How a product of these sizes runs: the kind of tile, and into how many parts its
