@@ -9,6 +9,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "layer_device.h"
 
 namespace zk {
@@ -85,42 +87,64 @@ __device__ __forceinline__ void put_chunk(uint16_t* lds, int id, v4u w) {
     *reinterpret_cast<v4u*>(lds + at) = w;
 }
 
+// Elements by .. 7 of eight to the front (what comes behind them does not matter).
+__device__ __forceinline__ v4u chunk_shift(v4u w, int by) {
+    if (by & 1) w = v4u{w[0] >> 16 | w[1] << 16, w[1] >> 16 | w[2] << 16, w[2] >> 16 | w[3] << 16, w[3] >> 16};
+    if (by & 2) w = v4u{w[1], w[2], w[3], 0};
+    if (by & 4) w = v4u{w[2], w[3], 0, 0};
+    return w;
+}
+
 // A tile through registers into LDS: all of a thread's chunks loaded, then stored
 // (Stage), or one at a time where registers are short (stage_tail). A whole tile's
-// rows outside the operand read its last one instead, as they reach no output; only
-// a chunk of reduced rows that the operand's edge cuts is loaded by elements.
+// rows outside the operand read its last one instead, as they reach no output. Of
+// reduced rows, the chunk that the operand's edge cuts is loaded from the row's last
+// eight elements and shifted as it is stored: a load by elements on one side of a
+// branch would make every load wait where the sides meet (1531 x 1001 x 2049 weight
+// gradient 63 -> 40 us).
 template <int ROWS, bool T, int THREADS>
 struct Stage {
     static constexpr int kChunks = ROWS * kBR / 8 / THREADS;
     v4u w[kChunks];
     const uint16_t* from[kChunks];
-    int n[kChunks];
+    int by[T ? kChunks : 1];        // elements to shift
     int64_t step;
+    bool edge, tiny;                // some chunk is cut; rows of fewer than eight elements
     __device__ __forceinline__ void init(const uint16_t* src, int64_t ld, int64_t o0, int64_t O, int64_t r0) {
         step = T ? kBR * ld : kBR;
+        tiny = T && O < 8;
+        edge = T && o0 + ROWS > O;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int id = threadIdx.x + i * THREADS;
             if constexpr (T) {
                 const int64_t row = r0 + id / (ROWS / 8), col = o0 + 8 * (id % (ROWS / 8));
-                n[i] = O - col >= 8 ? 8 : O - col > 0 ? (int)(O - col) : 0;
-                from[i] = src + row * ld + (n[i] > 0 ? col : 0);
+                const int64_t over = col + 8 - O;
+                by[i] = over <= 0 || over > 7 || tiny ? 0 : (int)over;
+                from[i] = src + row * ld + (tiny ? 0 : over > 0 ? O - 8 : col);
             } else {
                 int64_t row = o0 + id / (kBR / 8);
                 if (row >= O) row = O - 1;
                 from[i] = src + row * ld + r0 + 8 * (id % (kBR / 8));
-                n[i] = 8;
             }
         }
     }
-    __device__ __forceinline__ void load() {
+    __device__ __forceinline__ void load(int64_t O) {
+        if (T && tiny) {
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            w[i] = !T || n[i] > 0 ? chunk_load(from[i], n[i]) : v4u{0, 0, 0, 0};
-            from[i] += step;
+            for (int i = 0; i < kChunks; ++i) w[i] = chunk_load(from[i], (int)O);
+        } else {
+#pragma unroll
+            for (int i = 0; i < kChunks; ++i) w[i] = chunk_load(from[i], 8);
         }
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) from[i] += step;
     }
-    __device__ __forceinline__ void store(uint16_t* lds) const {
+    __device__ __forceinline__ void store(uint16_t* lds) {
+        if constexpr (T)
+            if (edge)
+#pragma unroll
+                for (int i = 0; i < kChunks; ++i) w[i] = chunk_shift(w[i], by[i]);
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) put_chunk<ROWS, T>(lds, threadIdx.x + i * THREADS, w[i]);
     }
@@ -330,9 +354,20 @@ struct Direct {
 // (Llama-7B shaped products: 8 rows 5% faster than tiles in order, 4 or 16 rows 2%
 // behind 8 on the deepest reductions.)
 constexpr int kTileRows = 8;
-__device__ __forceinline__ int tile_in_turn(int id, int tiles) {
-    const int xcd = id & 7, slot = id >> 3, each = tiles >> 3, more = tiles & 7;
-    return xcd * each + (xcd < more ? xcd : more) + slot;
+// With a split reduction the tiles of one split are consecutive, since they share the
+// split's rows of both operands (GPT-2 projection
+// gradient, 7 splits of 36 tiles: 27.2 -> 24.1 us).
+__device__ __forceinline__ int tile_in_turn(const ProductArgs& g, int* split) {
+    const int all = g.tiles * g.splits, id = blockIdx.x;
+    const int xcd = id & 7, slot = id >> 3, each = all >> 3, more = all & 7;
+    const int t = xcd * each + (xcd < more ? xcd : more) + slot;
+    if (g.splits == 1) {
+        *split = 0;
+        return t;
+    }
+    const int y = t / g.tiles;
+    *split = __builtin_amdgcn_readfirstlane(y);
+    return __builtin_amdgcn_readfirstlane(t - y * g.tiles);
 }
 __device__ __forceinline__ void tile_place(int t, int np, int nq, int* tp, int* tq) {
     const int block = t / (kTileRows * nq), in = t - block * kTileRows * nq;
@@ -345,8 +380,8 @@ __device__ __forceinline__ void tile_place(int t, int np, int nq, int* tp, int* 
 
 // Whole tiles of kBR in this split, in 32 bits: a 64-bit comparison would put what
 // depends on it into vector registers, the loads' descriptors among them.
-__device__ __forceinline__ int whole_steps(const ProductArgs& g) {
-    const int per = (int)(g.r_per_split / kBR), left = (int)(g.d.R / kBR) - (int)blockIdx.y * per;
+__device__ __forceinline__ int whole_steps(const ProductArgs& g, int split) {
+    const int per = (int)(g.r_per_split / kBR), left = (int)(g.d.R / kBR) - split * per;
     const int n = left < per ? left : per;
     return n > 0 ? n : 0;
 }
@@ -372,34 +407,35 @@ __device__ __forceinline__ v8bf ones8() {
     return v8bf{one, one, one, one, one, one, one, one};
 }
 // Lane l of the product's block holds the sum of column l & 15, in all its rows.
-__device__ __forceinline__ void put_sums(const ProductArgs& g, const SumTurn& t, int64_t col, v4f v) {
+__device__ __forceinline__ void put_sums(const ProductArgs& g, int split, const SumTurn& t, int64_t col, v4f v) {
     const int lane = threadIdx.x & 63;
     if (lane < 16 && col + lane < g.sum_n)
-        g.sums[((int64_t)blockIdx.y * t.others + t.turn) * g.ld_sums + col + lane] = v[0];
+        g.sums[((int64_t)split * t.others + t.turn) * g.ld_sums + col + lane] = v[0];
 }
 
 // The epilogue of a workgroup's tile, through LDS: kRun rows of a wave's blocks at a
 // time, so that a lane gets eight consecutive columns and stores 16 bytes or more.
 // Blocks are computed as (q, p), so a lane holds four consecutive columns of one
 // output row, one 16-byte unit. Each wave has its own part of LDS; unit u of row o
-// lies at u ^ (o & 15). row_of(i) and col_of(j): first row and column of the wave's
+// lies at u ^ (o & 15), or u ^ (o & 7) where a row has 8. row_of(i) and col_of(j): first row and column of the wave's
 // blocks (i, j) in the output; the rows of a run are consecutive.
 template <int EPI, int LDS_BYTES, int WAVES, int FP, int FQ, typename Row, typename Col>
-__device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP][FQ], uint16_t* lds, int wave,
+__device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4f (&acc)[FP][FQ], uint16_t* lds, int wave,
                                        Row row_of, Col col_of) {
-    static_assert(FQ == 4, "16 units a row");
-    constexpr int kFit = LDS_BYTES / (WAVES * 16 * 64 * 4), kRun = kFit >= 4 ? 4 : kFit;
+    static_assert(FQ == 2 || FQ == 4, "8 or 16 units a row");
+    constexpr int kCols = 16 * FQ, kMask = 4 * FQ - 1, kLanes = 2 * FQ, kStep = 64 / kLanes;
+    constexpr int kFit = LDS_BYTES / (WAVES * 16 * kCols * 4), kRun = kFit >= 4 ? 4 : kFit;
     static_assert(kRun >= 1 && FP % kRun == 0, "the runs cover a wave's rows");
+    static_assert(16 * kRun % (4 * kStep) == 0, "whole groups of four rows a lane");
     const ProductDesc& d = g.d;
     const int lane = threadIdx.x & 63;
     const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
-    float* const mine = reinterpret_cast<float*>(lds) + wave * kRun * 16 * 64;
-    const int c = lane & 7;
+    float* const mine = reinterpret_cast<float*>(lds) + wave * kRun * 16 * kCols;
+    const int c = lane % kLanes;
     const int64_t q = col_of(c >> 1) + 8 * (c & 1);
     const int n = d.Q - q >= 8 ? 8 : d.Q - q > 0 ? (int)(d.Q - q) : 0;
     float bias[8];
     epilogue_bias(d, q, g.part ? 0 : n, bias);
-    static_assert(kRun % 2 == 0, "whole groups of four rows a lane");
 #pragma unroll
     for (int i0 = 0; i0 < FP; i0 += kRun) {
 #pragma unroll
@@ -407,31 +443,50 @@ __device__ __forceinline__ void finish(const ProductArgs& g, const v4f (&acc)[FP
 #pragma unroll
             for (int j = 0; j < FQ; ++j) {
                 const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
-                *reinterpret_cast<v4f*>(mine + o * 64 + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
+                *reinterpret_cast<v4f*>(mine + o * kCols + 4 * (u ^ (o & kMask))) = acc[i0 + i][j];
             }
         // four rows of each lane at a time
 #pragma unroll 1
-        for (int o0 = lane >> 3; o0 < 16 * kRun; o0 += 32) {
+        for (int o0 = lane / kLanes; o0 < 16 * kRun; o0 += 4 * kStep) {
             EpilogueIn in[4];
             if (!g.part)
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const int64_t p = row_of(i0) + o0 + 8 * u;
+                    const int64_t p = row_of(i0) + o0 + kStep * u;
                     if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
                 }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const int o = o0 + 8 * u;
+                const int o = o0 + kStep * u;
                 const int64_t p = row_of(i0) + o;
-                const v4f lo = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c) ^ (o & 15)));
-                const v4f hi = *reinterpret_cast<const v4f*>(mine + o * 64 + 4 * ((2 * c + 1) ^ (o & 15)));
+                const v4f lo = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c) ^ (o & kMask)));
+                const v4f hi = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c + 1) ^ (o & kMask)));
                 float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 if (p >= d.P || n <= 0) continue;
-                if (g.part) store8_f(g.part + ((int64_t)blockIdx.y * d.P + p) * g.ld_part + q, v, 8);
+                if (g.part) store8_f(g.part + ((int64_t)split * d.P + p) * g.ld_part + q, v, 8);
                 else epilogue8<EPI>(d, off, p, q, v, in[u], bias, n);
             }
         }
     }
+}
+
+// The 128 x 128 tile of a workgroup: of all of them, or of the quarters of wide tiles.
+template <bool SUM>
+__device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split, int* tp, int* tq) {
+    int np = (int)((g.d.P + 127) / 128), nq = (int)((g.d.Q + 127) / 128);
+    if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
+    const int id = tile_in_turn(g, split);
+    if (g.first_wide < 0) {
+        tile_place(id, np, nq, tp, tq);
+        return g.sum_of == 1 ? SumTurn{*tq, nq, true} : SumTurn{*tp, np, g.sum_of == 2};
+    }
+    np = (np + 1) / 2, nq = (nq + 1) / 2;
+    tile_place(g.first_wide + (id >> 2), np, nq, tp, tq);
+    const SumTurn turn =
+        g.sum_of == 1 ? SumTurn{*tq, nq, (id & 1) == 0} : SumTurn{*tp, np, g.sum_of == 2 && (id & 2) == 0};
+    *tp = 2 * *tp + ((id >> 1) & 1);
+    *tq = 2 * *tq + (id & 1);
+    return turn;
 }
 
 // 128 x 128 outputs by four waves, 64 x 64 each (4 x 4 blocks), for outputs of few
@@ -443,23 +498,11 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 2 * kTile];
     const ProductDesc& d = g.d;
-    int tp, tq, np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
-    if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
-    SumTurn turn{0, 1, false};
-    if (g.first_wide < 0) {
-        tile_place(tile_in_turn(blockIdx.x, g.tiles), np, nq, &tp, &tq);
-        turn = g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
-    } else {
-        np = (np + 1) / 2, nq = (nq + 1) / 2;
-        const int id = tile_in_turn(blockIdx.x, g.tiles);
-        tile_place(g.first_wide + (id >> 2), np, nq, &tp, &tq);
-        turn = g.sum_of == 1 ? SumTurn{tq, nq, (id & 1) == 0} : SumTurn{tp, np, g.sum_of == 2 && (id & 2) == 0};
-        tp = 2 * tp + ((id >> 1) & 1);
-        tq = 2 * tq + (id & 1);
-    }
+    int split, tp, tq;
+    SumTurn turn = small_place<SUM>(g, &split, &tp, &tq);
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
     if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
-    const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
+    const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = (wave >> 1) * 64, wq = (wave & 1) * 64;
@@ -503,7 +546,7 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     };
 
     if constexpr (DIRECT) {
-        const int full = whole_steps(g);
+        const int full = whole_steps(g, split);
         Direct<B, TA, T, 1> da;
         Direct<B, TB, T, 1> db;
         if (full > 0) {
@@ -533,19 +576,19 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
         }
     } else {
         // the next tile waits in registers while one is multiplied
-        const int full = whole_steps(g);
+        const int full = whole_steps(g, split);
         Stage<B, TA, T> sa;
         Stage<B, TB, T> sb;
         if (full > 0) {
             sa.init(d.a, d.lda, p0, d.P, r0);
             sb.init(d.b, d.ldb, q0, d.Q, r0);
-            sa.load();
-            sb.load();
+            sa.load(d.P);
+            sb.load(d.Q);
             sa.store(lds);
             sb.store(lds + kTile);
             if (full > 1) {
-                sa.load();
-                sb.load();
+                sa.load(d.P);
+                sb.load(d.Q);
             }
         }
         for (int k = 0; k < full; ++k) {
@@ -555,8 +598,8 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
                 sa.store(to);
                 sb.store(to + kTile);
                 if (k + 2 < full) {
-                    sa.load();
-                    sb.load();
+                    sa.load(d.P);
+                    sb.load(d.Q);
                 }
             }
             multiply(base + 4 * kTile * (k & 1));
@@ -574,8 +617,127 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     if constexpr (SUM)
         if (turn.on && (g.sum_of == 1 ? wq : wp) == 0)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) put_sums(g, turn, (g.sum_of == 1 ? p0 + wp : q0 + wq) + 16 * i, sum[i]);
-    finish<EPI, sizeof(lds), 4>(g, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
+            for (int i = 0; i < 4; ++i) put_sums(g, split, turn, (g.sum_of == 1 ? p0 + wp : q0 + wq) + 16 * i, sum[i]);
+    finish<EPI, sizeof(lds), 4>(g, split, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
+                                [&](int j) { return q0 + wq + 16 * j; });
+}
+
+// 128 x 128 outputs by eight waves, 64 x 32 each, one workgroup to a compute unit: the
+// wide kernel's turns with a whole tile of 64 reduction elements to a turn, in a ring of
+// four. A wave reads the tile's operands and asks for the tile three ahead; then it
+// multiplies; waves 4-7 are one barrier behind waves 0-3. A tile's place is asked for
+// again one turn after it was read, two barriers or more after its last reads began;
+// each turn ends when the next turn's tile is here, one barrier before anyone reads it.
+template <bool TA, bool TB, int EPI, bool SUM>
+__global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
+    constexpr int T = 512, B = 128, FP = 4, FQ = 2, kTile = B * kBR, kSlots = 4;
+    __shared__ __attribute__((aligned(16))) uint16_t lds[kSlots * 2 * kTile];
+    const ProductDesc& d = g.d;
+    int split, tp, tq;
+    SumTurn turn = small_place<SUM>(g, &split, &tp, &tq);
+    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
+    const int64_t r0 = (int64_t)split * g.r_per_split;
+    const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wp = (wave >> 2) * 64, wq = (wave & 3) * 32;
+
+    v4f acc[FP][FQ], sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+    const Fragments<B, TA> ga(wp);
+    const Fragments<B, TB> gb(wq);
+    const uint32_t base = lds_address(lds);
+    v8bf fa[2][FP], fb[2][FQ];
+    const auto read = [&](uint32_t tile) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) fb[s][j] = gb.get(tile + 2 * kTile, j, s);
+#pragma unroll
+            for (int i = 0; i < FP; ++i) fa[s][i] = ga.get(tile, i, s);
+        }
+    };
+    const auto multiply = [&]() {
+        const bool now = SUM && turn.next();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < FP; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[s][j], fa[s][i], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (SUM)
+            if (now) {
+                // waves with the same blocks of dz's operand sum one each
+#pragma unroll
+                for (int s = 0; s < 2; ++s) {
+#pragma unroll
+                    for (int i = 0; i < FP; ++i)
+                        if (g.sum_of == 1 && (wave & 3) == i)
+                            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fa[s][i], sum, 0, 0, 0);
+#pragma unroll
+                    for (int j = 0; j < FQ; ++j)
+                        if (g.sum_of == 2 && (wave >> 2) == j)
+                            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones8(), fb[s][j], sum, 0, 0, 0);
+                }
+            }
+    };
+
+    const int n = whole_steps(g, split);
+    if (n > 0) {
+        Direct<B, TA, T, 1> da;
+        Direct<B, TB, T, 1> db;
+        constexpr int kLoads = Direct<B, TA, T, 1>::kLoads + Direct<B, TB, T, 1>::kLoads;
+        da.init(d.a, d.lda, p0, d.P, r0);
+        db.init(d.b, d.ldb, q0, d.Q, r0);
+        // loads of tiles behind the last are stopped by their buffer's range
+        const auto load = [&](int k) {
+            const int records = k < n ? kAllRecords : 0;
+            const uint32_t to = base + 4 * kTile * (k % kSlots);
+            da.issue(0, da.base, to, wave, records);
+            db.issue(0, db.base, to + 2 * kTile, wave, records);
+            da.base += da.step;
+            db.base += db.step;
+        };
+#pragma unroll
+        for (int k = 0; k < kSlots - 1; ++k) load(k);
+        loads_landed<(kSlots - 2) * kLoads>();
+        meet_waves();
+        if (wave >= 4) meet_waves();
+#pragma unroll 1
+        for (int k = 0; k < n; ++k) {
+            read(base + 4 * kTile * (k % kSlots));
+            load(k + kSlots - 1);
+            loads_landed<(kSlots - 2) * kLoads>();
+            meet_waves();
+            multiply();
+            meet_waves();
+        }
+        if (wave < 4) meet_waves();
+        loads_landed<0>();
+        meet_waves();
+    }
+    if (r0 + (int64_t)n * kBR < r1) {
+        // what is left of the reduction, with its end masked
+        const int64_t r = r0 + (int64_t)n * kBR;
+        stage_tail<B, TA, T>(lds, d.a, d.lda, p0, d.P, r, r1);
+        stage_tail<B, TB, T>(lds + kTile, d.b, d.ldb, q0, d.Q, r, r1);
+        meet_waves();
+        read(base);
+        multiply();
+        meet_waves();
+    }
+    if constexpr (SUM)
+        if (turn.on)
+            put_sums(g, split, turn, g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 16 * (wave >> 2), sum);
+    finish<EPI, sizeof(lds), 8>(g, split, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
                                 [&](int j) { return q0 + wq + 16 * j; });
 }
 
@@ -604,12 +766,12 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
     constexpr int T = 512, B = 256, H = 128, kHalf = H * kBR;
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 4 * kHalf];
     const ProductDesc& d = g.d;
-    int tp, tq;
+    int split, tp, tq;
     const int np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
-    tile_place(tile_in_turn(blockIdx.x, g.tiles), np, nq, &tp, &tq);
+    tile_place(tile_in_turn(g, &split), np, nq, &tp, &tq);
     SumTurn turn = g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
-    const int64_t r0 = (int64_t)blockIdx.y * g.r_per_split;
+    const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wp = (wave >> 2) * 64, wq = (wave & 3) * 32;
@@ -681,7 +843,7 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
             }
     };
 
-    const int n = whole_steps(g);
+    const int n = whole_steps(g, split);
     if (n > 0) {
         Direct<H, TA, T, 2> da;
         Direct<H, TB, T, 2> db;
@@ -766,9 +928,9 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
         if (turn.on)
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                put_sums(g, turn, (g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 16 * (wave >> 2)) + H * h,
+                put_sums(g, split, turn, (g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 16 * (wave >> 2)) + H * h,
                          sum[h]);
-    finish<EPI, sizeof(lds), 8>(g, acc, lds, wave, [&](int i) { return p0 + H * (i >> 2) + wp + 16 * (i & 3); },
+    finish<EPI, sizeof(lds), 8>(g, split, acc, lds, wave, [&](int i) { return p0 + H * (i >> 2) + wp + 16 * (i & 3); },
                                 [&](int j) { return q0 + H * (j >> 1) + wq + 16 * (j & 1); });
 }
 
@@ -1083,16 +1245,20 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
     if (pl.wide) {
         g.tiles = (int32_t)pl.full;
         const auto k = kSums && g.sums ? k_product_wide<TA, TB, EPI, kSums> : k_product_wide<TA, TB, EPI, false>;
-        hipLaunchKernelGGL(k, dim3((unsigned)pl.full, splits), dim3(512), 0, st, g);
+        hipLaunchKernelGGL(k, dim3((unsigned)pl.full * splits), dim3(512), 0, st, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!pl.wide || pl.full < wide) {
         g.first_wide = pl.wide ? (int32_t)pl.full : -1;
         g.tiles = (int32_t)(pl.wide ? 4 * (wide - pl.full) : tiles);
-        const auto k = kSums && g.sums
-                           ? direct ? k_product<TA, TB, EPI, true, kSums> : k_product<TA, TB, EPI, false, kSums>
-                           : direct ? k_product<TA, TB, EPI, true, false> : k_product<TA, TB, EPI, false, false>;
-        hipLaunchKernelGGL(k, dim3((unsigned)g.tiles, splits), dim3(256), 0, st, g);
+        const bool mid = direct && (int64_t)g.tiles * splits <= 256;
+        const auto pick = [&](auto sums) {
+            constexpr bool S = decltype(sums)::value;
+            return mid ? k_product_mid<TA, TB, EPI, S>
+                       : direct ? k_product<TA, TB, EPI, true, S> : k_product<TA, TB, EPI, false, S>;
+        };
+        const auto k = kSums && g.sums ? pick(std::integral_constant<bool, kSums>{}) : pick(std::false_type{});
+        hipLaunchKernelGGL(k, dim3((unsigned)g.tiles * splits), dim3(mid ? 512 : 256), 0, st, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!g.part && !g.sums) return e;
