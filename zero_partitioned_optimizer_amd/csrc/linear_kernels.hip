@@ -431,8 +431,11 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
     const int lane = threadIdx.x & 63;
     const uint64_t off = d.drop.thr ? drop_offset(d.drop) : 0;
     float* const mine = reinterpret_cast<float*>(lds) + wave * kRun * 16 * kCols;
-    const int c = lane % kLanes;
-    const int64_t q = col_of(c >> 1) + 8 * (c & 1);
+    // A split's sums go four columns to a lane, whole lines to a store instruction
+    // (GPT-2 projection gradient 23.7 -> 22.9 us; f32 outputs, which read and compute as
+    // well, are 5% faster with eight).
+    const int c = g.part ? lane % (2 * kLanes) : lane % kLanes;
+    const int64_t q = g.part ? col_of(c >> 2) + 4 * (c & 3) : col_of(c >> 1) + 8 * (c & 1);
     const int n = d.Q - q >= 8 ? 8 : d.Q - q > 0 ? (int)(d.Q - q) : 0;
     float bias[8];
     epilogue_bias(d, q, g.part ? 0 : n, bias);
@@ -445,16 +448,26 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
                 const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
                 *reinterpret_cast<v4f*>(mine + o * kCols + 4 * (u ^ (o & kMask))) = acc[i0 + i][j];
             }
+        if (g.part) {
+            // rows of ld_part, a multiple of 8, so a lane's columns all have a place
+#pragma unroll 4
+            for (int o = lane / (2 * kLanes); o < 16 * kRun; o += kStep / 2) {
+                const int64_t p = row_of(i0) + o;
+                const v4f v = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * (c ^ (o & kMask)));
+                if (p < d.P && q < g.ld_part)
+                    *reinterpret_cast<v4f*>(g.part + ((int64_t)split * d.P + p) * g.ld_part + q) = v;
+            }
+            continue;
+        }
         // four rows of each lane at a time
 #pragma unroll 1
         for (int o0 = lane / kLanes; o0 < 16 * kRun; o0 += 4 * kStep) {
             EpilogueIn in[4];
-            if (!g.part)
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int64_t p = row_of(i0) + o0 + kStep * u;
-                    if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
-                }
+            for (int u = 0; u < 4; ++u) {
+                const int64_t p = row_of(i0) + o0 + kStep * u;
+                if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
+            }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int o = o0 + kStep * u;
@@ -463,8 +476,7 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
                 const v4f hi = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * ((2 * c + 1) ^ (o & kMask)));
                 float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
                 if (p >= d.P || n <= 0) continue;
-                if (g.part) store8_f(g.part + ((int64_t)split * d.P + p) * g.ld_part + q, v, 8);
-                else epilogue8<EPI>(d, off, p, q, v, in[u], bias, n);
+                epilogue8<EPI>(d, off, p, q, v, in[u], bias, n);
             }
         }
     }
