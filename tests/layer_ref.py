@@ -26,19 +26,28 @@ def philox(counter, key, rounds=10):
 
 def drop_factor(rows, cols, p, seed, offset):
     """[rows, cols] factors: 0 where dropped, 65536 / (65536 - thr) elsewhere."""
+    return _factors(np.arange(rows, dtype=np.uint64), cols, p, seed, offset)
+
+
+def drop_row(row, cols, p, seed, offset):
+    """The factors of one row."""
+    return _factors(np.array([row], dtype=np.uint64), cols, p, seed, offset)[0]
+
+
+def _factors(rows, cols, p, seed, offset):
     thr = int(np.rint(p * 65536))
     if thr == 0:
-        return np.ones((rows, cols))
+        return np.ones((len(rows), cols))
     g = (cols + 7) // 8
-    i, j = np.meshgrid(np.arange(rows, dtype=np.uint64), np.arange(g, dtype=np.uint64), indexing="ij")
+    i, j = np.meshgrid(rows, np.arange(g, dtype=np.uint64), indexing="ij")
     offset &= (1 << 64) - 1
     full = np.ones_like(i)
     w = philox((j, i, full * np.uint64(offset & 0xFFFFFFFF), full * np.uint64(offset >> 32)),
                (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF))
-    draws = np.empty((rows, g, 8), dtype=np.uint64)
+    draws = np.empty((len(rows), g, 8), dtype=np.uint64)
     for k in range(8):
         draws[:, :, k] = (w[k // 2] >> np.uint64(16 * (k % 2))) & np.uint64(0xFFFF)
-    keep = draws.reshape(rows, 8 * g)[:, :cols] >= thr
+    keep = draws.reshape(len(rows), 8 * g)[:, :cols] >= thr
     return keep * (65536.0 / (65536.0 - thr))
 
 

@@ -5,6 +5,8 @@ a base at any element, NaN in what inputs leave unused and a sentinel in what
 outputs must not touch. The bounds are worst-case ones of fp32 sums and a single
 rounding, derived in layer_ref.py.
 """
+import zlib
+
 import numpy as np
 import pytest
 import torch
@@ -51,6 +53,11 @@ def rand(rng, *shape, scale=1.0):
     return (rng.standard_normal(shape) * scale).astype(np.float32)
 
 
+def rng_of(case):
+    """A generator of its own for each case, the same in every run."""
+    return np.random.default_rng(zlib.crc32(repr(case).encode()))
+
+
 def inp(rng, rows, cols, *, dtype=BF, scale=1.0, pad_ld=0, shift=0):
     return Mat(rows, cols, dtype, ld=cols + pad_ld, shift=shift, fill=rand(rng, rows, cols, scale=scale),
                pad=float("nan"))
@@ -91,7 +98,7 @@ def w64(w, layout):
 @pytest.mark.parametrize("size", SIZES, ids=str)
 def test_forward_sizes(Z, size, layout):
     M, K, N = size
-    rng = np.random.default_rng(hash((1,) + size + (layout,)) % 2 ** 32)
+    rng = rng_of((1,) + size + (layout,))
     place = PLACES[(M + K + N) % len(PLACES)]
     x, w = inp(rng, M, K, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place)
     b = torch.from_numpy(rand(rng, N)).to(dev()).to(BF)
@@ -108,7 +115,7 @@ def test_forward_sizes(Z, size, layout):
 @pytest.mark.parametrize("size", SIZES, ids=str)
 def test_grad_input_sizes(Z, size, layout):
     M, K, N = size
-    rng = np.random.default_rng(hash((2,) + size + (layout,)) % 2 ** 32)
+    rng = rng_of((2,) + size + (layout,))
     place = PLACES[(M + K + 2 * N) % len(PLACES)]
     dz, w = inp(rng, M, N, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place)
     dx = Mat(M, K, F32, ld=K + place[0], shift=place[1])
@@ -123,7 +130,7 @@ def test_grad_input_sizes(Z, size, layout):
 @pytest.mark.parametrize("size", SIZES + [(0, 5, 7), (4000, 128, 96), (8200, 24, 136), (2049, 130, 1)], ids=str)
 def test_grad_weight_sizes(Z, size, layout):
     M, K, N = size
-    rng = np.random.default_rng(hash((3,) + size + (layout,)) % 2 ** 32)
+    rng = rng_of((3,) + size + (layout,))
     place = PLACES[(2 * M + K + N) % len(PLACES)]
     out = ("bf16", "f32")[(M + N) % 2]
     accumulate = bool((M + K) % 2)
@@ -146,7 +153,7 @@ def test_grad_weight_sizes(Z, size, layout):
 @pytest.mark.parametrize("size", [(1, 64, 72), (37, 40, 203), (256, 128, 512), (5, 3000, 260)], ids=str)
 def test_forward_epilogue(Z, size, act, out):
     M, K, N = size
-    rng = np.random.default_rng(hash((4,) + size + (act,)) % 2 ** 32)
+    rng = rng_of((4,) + size + (act,))
     layout, place = act % 2, PLACES[(act + M) % len(PLACES)]
     p, seed, offset = (0.0, 0.1, 0.5, 1 - 2.0 ** -16)[(act + N) % 4], 0xFEDCBA9876543210 + act, (1 << 63) + 5
     x, w = inp(rng, M, K, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place, 0.3)
@@ -172,7 +179,7 @@ def test_forward_epilogue(Z, size, act, out):
 @pytest.mark.parametrize("size", [(1, 72, 64), (37, 203, 40), (256, 512, 128), (5, 260, 3000)], ids=str)
 def test_grad_input_epilogue(Z, size, act, out):
     M, K, N = size
-    rng = np.random.default_rng(hash((5,) + size + (act,)) % 2 ** 32)
+    rng = rng_of((5,) + size + (act,))
     layout, place = act % 2, PLACES[(act + M + 1) % len(PLACES)]
     p, seed, offset = (0.3, 0.0, 0.7, 0.1)[(act + N) % 4], 77 + act, 1 << 40
     dz, w = inp(rng, M, N, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place)
@@ -198,7 +205,7 @@ DROP_SIZES = [(1, 1), (1, 7), (3, 8), (5, 9), (64, 768), (17, 1003), (300, 64), 
 @pytest.mark.parametrize("size", DROP_SIZES, ids=str)
 def test_dropout_add(Z, size, types):
     M, N = size
-    rng = np.random.default_rng(hash((6,) + size) % 2 ** 32)
+    rng = rng_of((6,) + size)
     place = PLACES[(M + N) % len(PLACES)]
     p, seed, offset = (0.1, 0.5, 0.9, 0.0)[(M + len(types[0])) % 4], 1 << 33 | M, N
     x = inp(rng, M, N, dtype=TY[types[0]], pad_ld=place[0], shift=place[1])
@@ -225,7 +232,7 @@ def test_dropout_add(Z, size, types):
 @pytest.mark.parametrize("size", DROP_SIZES[:7], ids=str)
 def test_dropout_grad(Z, size, act, types):
     M, N = size
-    rng = np.random.default_rng(hash((7,) + size + (act,)) % 2 ** 32)
+    rng = rng_of((7,) + size + (act,))
     place = PLACES[(M + N + act) % len(PLACES)]
     p, seed, offset = (0.25, 0.0, 0.5)[(M + act) % 3], 3, 1 << 62
     dy = inp(rng, M, N, dtype=TY[types[0]], pad_ld=place[0], shift=place[1])
@@ -438,7 +445,7 @@ def test_captured_calls_draw_anew(Z):
 def test_wide_outputs(Z, rows, inner, layout):
     """Outputs of enough tiles to fill the chip (the largest tiles), with ragged edges
     and reductions that are and are not whole tiles, in each direction."""
-    rng = np.random.default_rng(hash((14, rows, inner, layout)) % 2 ** 32)
+    rng = rng_of((14, rows, inner, layout))
     cols = 4104
     say("wide", rows, inner, layout)
     x, w = inp(rng, rows, inner, pad_ld=-inner % 8), weight(rng, inner, cols, layout, (8, 0))
@@ -473,7 +480,7 @@ def test_wide_outputs(Z, rows, inner, layout):
 def test_bias_gradient_of_wide_weights(Z, M, K, N, layout):
     """The bias gradient beside weight gradients of many tiles, of one row or column of
     tiles, of split sums, and of a weight with no elements."""
-    rng = np.random.default_rng(hash((15, M, K, N, layout)) % 2 ** 32)
+    rng = rng_of((15, M, K, N, layout))
     say("bias", M, K, N, layout)
     dz, x = inp(rng, M, N, pad_ld=-N % 8), inp(rng, M, K, pad_ld=-K % 8)
     r, c = (N, K) if layout == 0 else (K, N)
@@ -516,7 +523,7 @@ def test_rounds_and_quarters(Z, M, K, N):
 def test_few_rows(Z, M, K, N, layout):
     """One to seventeen rows: the products that are bound by the weights' bytes, with
     the whole epilogue, whole and odd reductions, padded and odd rows."""
-    rng = np.random.default_rng(hash((17, M, K, N, layout)) % 2 ** 32)
+    rng = rng_of((17, M, K, N, layout))
     for place in ((0, 0), (8, 0), (3, 1)):
         x, w = inp(rng, M, K, pad_ld=place[0], shift=place[1]), weight(rng, K, N, layout, place)
         b = torch.from_numpy(rand(rng, N)).to(dev()).to(BF)
@@ -537,3 +544,42 @@ def test_few_rows(Z, M, K, N, layout):
         want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="gelu", z=zz.f64(), out="f32")
         close("dx", dx.t, want, err)
         assert dx.intact_outside()
+
+
+@pytest.mark.parametrize("N", [(1 << 26) - 3, (1 << 26) + 9])
+def test_most_columns(Z, N):
+    """Both sides of the width up to which one row takes a launch of its own."""
+    g = torch.Generator(device=dev()).manual_seed(N)
+    x = torch.randn((1, 1), dtype=BF, device=dev(), generator=g)
+    w = torch.randn((N, 1), dtype=BF, device=dev(), generator=g)
+    y = Z.zero_linear_forward(x, w)
+    want = (x.float() * w.float()[:, 0]).to(BF)         # exact in f32, one rounding
+    assert torch.equal(y, want)
+
+
+def test_most_rows(Z):
+    """A million tiles below one another."""
+    M = (1 << 27) + 5
+    g = torch.Generator(device=dev()).manual_seed(M)
+    dz = torch.randn((M, 1), dtype=BF, device=dev(), generator=g)
+    w = torch.randn((1, 1), dtype=BF, device=dev(), generator=g)
+    dx = Z.zero_linear_grad_input(dz, w)
+    assert torch.equal(dx, (dz.float() * w.float()).to(BF))
+
+
+def test_dropout_of_more_than_one_launch(Z):
+    """2^31 threads and more: the rows around the seam and the last ones are as those of
+    a matrix that a call of few rows gives."""
+    N = 8192
+    M = (1 << 21) + 7                                   # 1024 threads a row
+    if torch.cuda.mem_get_info()[0] < 3 * M * N:
+        pytest.skip("not enough free memory")
+    p, seed = 0.25, 11
+    x = torch.empty((M, N), dtype=BF, device=dev())
+    for r in (0, (1 << 21) - 2, (1 << 21) - 1, 1 << 21, M - 1):
+        x[r].fill_(1.0)
+    Z.zero_dropout_add(x, Z.zero_dropout(p, seed, 3), y=x)
+    for r in (0, (1 << 21) - 2, (1 << 21) - 1, 1 << 21, M - 1):
+        want = R.drop_row(r, N, p, seed, 3)
+        got = x[r].float().cpu().numpy().astype(np.float64)
+        assert (np.abs(got - want) <= 2.0 ** -8 * np.abs(want)).all(), r

@@ -58,6 +58,8 @@ INVAL, ALIGN, RANGE = B.ZERO_E_INVAL, B.ZERO_E_ALIGN, B.ZERO_E_RANGE
 @pytest.mark.parametrize("kw,status,word", [
     (dict(M=-1), RANGE, "M=-1"),
     (dict(N=1 << 31), RANGE, "N="),
+    (dict(M=(1 << 29) + 1), RANGE, "2^29 a side"),
+    (dict(M=1 << 20, N=1 << 18, ld_w=1 << 18, ld_y=1 << 18), RANGE, "2^23 tiles"),
     (dict(x=None), INVAL, "x is NULL"),
     (dict(w=None), INVAL, "w is NULL"),
     (dict(y=None), INVAL, "y is NULL"),

@@ -90,6 +90,13 @@ int check_dims(const char* fn, int64_t M, int64_t K, int64_t N) {
     return ZERO_OK;
 }
 
+int check_output(const char* fn, int64_t rows, int64_t cols) {
+    if (zk::product_fits(rows, cols)) return ZERO_OK;
+    set_error("%s: an output of %lld x %lld is more than 2^23 tiles of 128 x 128 or 2^29 a side", fn,
+              (long long)rows, (long long)cols);
+    return ZERO_E_RANGE;
+}
+
 int check_type(const char* fn, const char* name, int32_t ty) {
     if (ty == ZERO_F32 || ty == ZERO_BF16) return ZERO_OK;
     set_error("%s: %s=%d is neither ZERO_F32 nor ZERO_BF16", fn, name, (int)ty);
@@ -166,6 +173,8 @@ size_t zero_linear_workspace_bytes(int32_t kind, int32_t w_layout, int64_t M, in
     if (w_layout != ZERO_W_OUT_IN && w_layout != ZERO_W_IN_OUT) return 0;
     const bool oi = w_layout == ZERO_W_OUT_IN;
     size_t product;
+    const int64_t rows = kind == ZERO_LINEAR_GRAD_WEIGHT ? N : M, cols = kind == ZERO_LINEAR_FORWARD ? N : K;
+    if (!zk::product_fits(rows, cols)) return 0;
     if (kind == ZERO_LINEAR_FORWARD) return zk::product_ws_bytes(M, N, K, false, !oi);
     if (kind == ZERO_LINEAR_GRAD_INPUT) return zk::product_ws_bytes(M, K, N, false, oi);
     if (kind == ZERO_LINEAR_GRAD_WEIGHT) return weight_ws(oi, M, K, N, &product);
@@ -181,7 +190,8 @@ int zero_linear_forward(const zero_linear_args* args, void* stream) {
     const zero_linear_args& a = *args;
     int rc;
     zk::Drop drop;
-    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_type(fn, "y_dtype", a.y_dtype)) ||
+    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_output(fn, a.M, a.N)) ||
+        (rc = check_type(fn, "y_dtype", a.y_dtype)) ||
         (rc = check_act(fn, a.act)) || (rc = check_w_layout(fn, a.w_layout)) ||
         (rc = make_drop(fn, a.dropout, &drop)))
         return rc;
@@ -231,7 +241,8 @@ int zero_linear_grad_input(const zero_linear_grad_input_args* args, void* stream
     const zero_linear_grad_input_args& a = *args;
     int rc;
     zk::Drop drop;
-    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_type(fn, "dx_dtype", a.dx_dtype)) ||
+    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_output(fn, a.M, a.K)) ||
+        (rc = check_type(fn, "dx_dtype", a.dx_dtype)) ||
         (rc = check_act(fn, a.act)) || (rc = check_w_layout(fn, a.w_layout)) ||
         (rc = make_drop(fn, a.dropout, &drop)))
         return rc;
@@ -275,7 +286,8 @@ int zero_linear_grad_weight(const zero_linear_grad_weight_args* args, void* stre
     }
     const zero_linear_grad_weight_args& a = *args;
     int rc;
-    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_type(fn, "grad_dtype", a.grad_dtype)) ||
+    if ((rc = check_dims(fn, a.M, a.K, a.N)) || (rc = check_output(fn, a.N, a.K)) ||
+        (rc = check_type(fn, "grad_dtype", a.grad_dtype)) ||
         (rc = check_w_layout(fn, a.w_layout)))
         return rc;
     const bool oi = a.w_layout == ZERO_W_OUT_IN;

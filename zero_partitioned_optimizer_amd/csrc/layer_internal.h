@@ -54,6 +54,11 @@ struct ProductDesc {
 // for the bias gradient beside it.
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb);
 size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a);
+// Whether the output's tiles fit one launch, whose threads a 32-bit count holds.
+inline bool product_fits(int64_t P, int64_t Q) {
+    constexpr int64_t kSide = int64_t(1) << 29, kTiles = int64_t(1) << 23;
+    return P <= kSide && Q <= kSide && ((P + 127) / 128) * ((Q + 127) / 128) <= kTiles;
+}
 hipError_t launch_product(const ProductDesc& d, hipStream_t st);
 
 // Elementwise over [M, N]: y = res + D(x), or (grad) y = D'(x) * act'(z).

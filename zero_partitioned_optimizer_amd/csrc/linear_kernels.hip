@@ -1183,7 +1183,7 @@ static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
 // reduced rows, 64 columns to a workgroup: where its workgroups' share of memory
 // (55 KB/us each) beats the join's launch and traffic.
 static bool few(int64_t P, int64_t Q, int64_t R, bool tb) {
-    if (P < 1 || P > 16 || Q < 1) return false;
+    if (P < 1 || P > 16 || Q < 1 || Q > (int64_t(1) << 26)) return false;   // 2^31 threads
     if (!tb) return P <= 4 || 2 * Q * R < (int64_t(32) << 20);
     const double bytes = 2.0 * Q * R, groups = (double)((Q + 63) / 64);
     return bytes / ((groups < 256 ? groups : 256) * 55e3) < 5 + bytes / 6e6;
@@ -1237,7 +1237,6 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
     const Plan pl = plan_of(d.P, d.Q, d.R, direct);
     const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;
     const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
-    if (tiles > INT32_MAX / 4) return hipErrorInvalidValue;
     ProductArgs g{};
     g.d = d;
     g.splits = pl.splits;

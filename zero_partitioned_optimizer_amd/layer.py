@@ -7,7 +7,8 @@ slices are the step's replicas, and dropout with a mask that is recomputed and
 never stored. The functions keep the C names of ``include/zero_layer.h`` and take torch
 tensors on the current device: 2-D matrices whose rows may be longer than their
 columns (``stride(0) >= size(1)``, ``stride(1) == 1``). Outputs that are not given
-are allocated; a workspace that is not given is allocated for the call.
+are allocated, and a workspace that is not given is allocated for the call, both on
+the call's stream.
 ``FlatLinear`` puts them together for one linear layer of a flat parameter buffer.
 """
 from __future__ import annotations
