@@ -546,6 +546,43 @@ def test_few_rows(Z, M, K, N, layout):
         assert dx.intact_outside()
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,cols", [(8190, 765), (2900, 1530), (4097, 1152)])
+@pytest.mark.parametrize("inner", [40, 200, 768])
+def test_tiles_of_192_columns(Z, rows, cols, inner, layout):
+    """Outputs of one round of the chip in tiles of 192 columns, of more in tiles of 128,
+    with ragged edges, in each direction and type."""
+    rng = rng_of((18, rows, cols, inner, layout))
+    say("192", rows, cols, inner, layout)
+    pad = -cols % 8
+    x, w = inp(rng, rows, inner), weight(rng, inner, cols, layout, (pad if layout else 0, 0))
+    res = inp(rng, rows, cols, pad_ld=3)
+    y, z = Mat(rows, cols, BF, ld=cols + 5), Mat(rows, cols, BF, ld=cols + pad)
+    b = inp(rng, 1, cols)
+    Z.zero_linear_forward(x.t, w.t, b.t[0], w_layout=layout, act=3, dropout=Z.zero_dropout(0.3, 9, 8), residual=res.t,
+                          y=y.t, preact=z.t)
+    want, err, wz, ez = R.linear_forward(x.f64(), w64(w, layout), b.f64()[0], act_name="silu", p=0.3, seed=9, offset=8,
+                                         residual=res.f64())
+    close("y", y.t, want, err)
+    close("z", z.t, wz, ez)
+    assert y.intact_outside() and z.intact_outside()
+    dz, w = inp(rng, rows, inner), weight(rng, cols, inner, layout, (0 if layout else pad, 0))
+    dx = Mat(rows, cols, F32, ld=cols + 7)
+    Z.zero_linear_grad_input(dz.t, w.t, w_layout=layout, act=2, preact=res.t, dropout=Z.zero_dropout(0.1, 2, 3), dx=dx.t)
+    want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="gelu", z=res.f64(), p=0.1, seed=2, offset=3,
+                                    out="f32")
+    close("dx", dx.t, want, err)
+    assert dx.intact_outside()
+    r, c = (rows, cols) if layout == 0 else (cols, rows)
+    dz, x = inp(rng, inner, rows, pad_ld=-rows % 8), inp(rng, inner, cols, pad_ld=pad)
+    dw = Mat(r, c, BF, ld=c + 1, fill=rand(rng, r, c))
+    old = w64(dw, layout)
+    Z.zero_linear_grad_weight(dz.t, x.t, dw.t, w_layout=layout, accumulate=True)
+    want, err = R.linear_grad_weight(dz.f64(), x.f64(), old=old)
+    close("dw", dw.t if layout == 0 else dw.t.t(), want, err)
+    assert dw.intact_outside()
+
+
 @pytest.mark.parametrize("N", [(1 << 26) - 3, (1 << 26) + 9])
 def test_most_columns(Z, N):
     """Both sides of the width up to which one row takes a launch of its own."""

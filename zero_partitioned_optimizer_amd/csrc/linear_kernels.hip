@@ -38,10 +38,11 @@ struct ProductArgs {
 //   outer rows:   [rows][kBR], chunk c of row o at c ^ (o & 7): the 8 lanes of a
 //                 16-byte read hold 8 rows at one c.
 //   reduced rows: [kBR][cols], chunk c of row r at c ^ perm(r): a transposing read
-//                 takes 4 rows x 32 bytes per 16 lanes, and two such groups 8 rows apart.
+//                 takes 4 rows x 32 bytes per 16 lanes, and two such groups 8 rows apart
+//                 (of 64 columns, even and odd rows have different banks as it is).
 template <int COLS>
 __device__ __forceinline__ int perm_reduced(int r) {
-    return ((r & 3) << 1) | (COLS >= 128 ? ((r >> 3) & 1) << 3 : 0);
+    return COLS >= 128 ? (r & 3) << 1 | (r >> 3 & 1) << 3 : (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1;
 }
 
 // Eight elements (n of them valid, the rest 0) from any element-aligned address.
@@ -417,13 +418,15 @@ __device__ __forceinline__ void put_sums(const ProductArgs& g, int split, const 
 // time, so that a lane gets eight consecutive columns and stores 16 bytes or more.
 // Blocks are computed as (q, p), so a lane holds four consecutive columns of one
 // output row, one 16-byte unit. Each wave has its own part of LDS; unit u of row o
-// lies at u ^ (o & 15), or u ^ (o & 7) where a row has 8. row_of(i) and col_of(j): first row and column of the wave's
-// blocks (i, j) in the output; the rows of a run are consecutive.
+// lies at u ^ (o & 15), or u ^ (o & 7) where a row has 8. row_of(i) and col_of(j): first
+// row and column of the wave's blocks (i, j) in the output; the rows of a run are
+// consecutive.
 template <int EPI, int LDS_BYTES, int WAVES, int FP, int FQ, typename Row, typename Col>
 __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4f (&acc)[FP][FQ], uint16_t* lds, int wave,
                                        Row row_of, Col col_of) {
-    static_assert(FQ == 2 || FQ == 4, "8 or 16 units a row");
-    constexpr int kCols = 16 * FQ, kMask = 4 * FQ - 1, kLanes = 2 * FQ, kStep = 64 / kLanes;
+    static_assert(FQ >= 2 && FQ <= 4, "8 or 16 units a row; of 3 blocks with 4 left empty");
+    constexpr int kBlocks = FQ == 2 ? 2 : 4;
+    constexpr int kCols = 16 * kBlocks, kMask = 4 * kBlocks - 1, kLanes = 2 * kBlocks, kStep = 64 / kLanes;
     constexpr int kFit = LDS_BYTES / (WAVES * 16 * kCols * 4), kRun = kFit >= 4 ? 4 : kFit;
     static_assert(kRun >= 1 && FP % kRun == 0, "the runs cover a wave's rows");
     static_assert(16 * kRun % (4 * kStep) == 0, "whole groups of four rows a lane");
@@ -436,11 +439,23 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
     // well, are 5% faster with eight).
     const int c = g.part ? lane % (2 * kLanes) : lane % kLanes;
     const int64_t q = g.part ? col_of(c >> 2) + 4 * (c & 3) : col_of(c >> 1) + 8 * (c & 1);
-    const int n = d.Q - q >= 8 ? 8 : d.Q - q > 0 ? (int)(d.Q - q) : 0;
+    const bool some = (g.part ? c >> 2 : c >> 1) < FQ;
+    const int n = !some ? 0 : d.Q - q >= 8 ? 8 : d.Q - q > 0 ? (int)(d.Q - q) : 0;
     float bias[8];
     epilogue_bias(d, q, g.part ? 0 : n, bias);
 #pragma unroll
     for (int i0 = 0; i0 < FP; i0 += kRun) {
+        EpilogueIn in[4];
+        const auto load = [&](int o0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t p = row_of(i0) + o0 + kStep * u;
+                if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
+            }
+        };
+        // four rows of each lane at a time, the first four before the sums go to LDS (GPT-2
+        // projection with residual 17.4 -> 16.6 us; all eight at once spill the wide kernel)
+        if (!g.part) load(lane / kLanes);
 #pragma unroll
         for (int i = 0; i < kRun; ++i)
 #pragma unroll
@@ -454,20 +469,14 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
             for (int o = lane / (2 * kLanes); o < 16 * kRun; o += kStep / 2) {
                 const int64_t p = row_of(i0) + o;
                 const v4f v = *reinterpret_cast<const v4f*>(mine + o * kCols + 4 * (c ^ (o & kMask)));
-                if (p < d.P && q < g.ld_part)
+                if (some && p < d.P && q < g.ld_part)
                     *reinterpret_cast<v4f*>(g.part + ((int64_t)split * d.P + p) * g.ld_part + q) = v;
             }
             continue;
         }
-        // four rows of each lane at a time
 #pragma unroll 1
         for (int o0 = lane / kLanes; o0 < 16 * kRun; o0 += 4 * kStep) {
-            EpilogueIn in[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const int64_t p = row_of(i0) + o0 + kStep * u;
-                if (p < d.P && n > 0) in[u].template load<EPI>(d, p, q, n);
-            }
+            if (o0 >= 4 * kStep) load(o0);
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
                 const int o = o0 + kStep * u;
@@ -482,10 +491,11 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
     }
 }
 
-// The 128 x 128 tile of a workgroup: of all of them, or of the quarters of wide tiles.
-template <bool SUM>
+// The tile of 128 rows and COLS columns of a workgroup: of all of them, or (128 columns)
+// of the quarters of wide tiles.
+template <bool SUM, int COLS>
 __device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split, int* tp, int* tq) {
-    int np = (int)((g.d.P + 127) / 128), nq = (int)((g.d.Q + 127) / 128);
+    int np = (int)((g.d.P + 127) / 128), nq = (int)((g.d.Q + COLS - 1) / COLS);
     if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
     const int id = tile_in_turn(g, split);
     if (g.first_wide < 0) {
@@ -511,7 +521,7 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 2 * kTile];
     const ProductDesc& d = g.d;
     int split, tp, tq;
-    SumTurn turn = small_place<SUM>(g, &split, &tp, &tq);
+    SumTurn turn = small_place<SUM, B>(g, &split, &tp, &tq);
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
     if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
     const int64_t r0 = (int64_t)split * g.r_per_split;
@@ -634,25 +644,30 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
                                 [&](int j) { return q0 + wq + 16 * j; });
 }
 
-// 128 x 128 outputs by eight waves, 64 x 32 each, one workgroup to a compute unit: the
+// 128 x 64 FQ outputs (FQ 2 or 3) by eight waves, one workgroup to a compute unit: the
 // wide kernel's turns with a whole tile of 64 reduction elements to a turn, in a ring of
-// four. A wave reads the tile's operands and asks for the tile three ahead; then it
-// multiplies; waves 4-7 are one barrier behind waves 0-3. A tile's place is asked for
-// again one turn after it was read, two barriers or more after its last reads began;
-// each turn ends when the next turn's tile is here, one barrier before anyone reads it.
-template <bool TA, bool TB, int EPI, bool SUM>
+// four. A wave has 64 rows and 16 columns of each run of 64. It reads the tile's operands
+// and asks for the tile three ahead; then it multiplies; waves 4-7 are one barrier behind
+// waves 0-3. A tile's place is asked for again one turn after it was read, two barriers or
+// more after its last reads began; each turn ends when the next turn's tile is here, one
+// barrier before anyone reads it. A turn takes 0.5 us, and what is around the turns 10: for
+// the GPT-2 projection (8192 x 768 x 768 with dropout and residual, 256 tiles of 192
+// columns) 18.4 us, 525 TFLOP/s, 5 of them its epilogue's memory and draws; through the
+// 2304 outputs of qkv 28.9 us, 1.0 PFLOP/s.
+template <bool TA, bool TB, int EPI, bool SUM, int FQ>
 __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
-    constexpr int T = 512, B = 128, FP = 4, FQ = 2, kTile = B * kBR, kSlots = 4;
-    __shared__ __attribute__((aligned(16))) uint16_t lds[kSlots * 2 * kTile];
+    constexpr int T = 512, B = 128, FP = 4, kA = B * kBR, kB = 64 * kBR, kSlot = kA + FQ * kB, kSlots = 4;
+    static_assert(!SUM || FQ == 2, "two waves share a block of b, and sum one each");
+    __shared__ __attribute__((aligned(16))) uint16_t lds[kSlots * kSlot];
     const ProductDesc& d = g.d;
     int split, tp, tq;
-    SumTurn turn = small_place<SUM>(g, &split, &tp, &tq);
-    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    SumTurn turn = small_place<SUM, 64 * FQ>(g, &split, &tp, &tq);
+    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * (64 * FQ);
     if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
     const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int wp = (wave >> 2) * 64, wq = (wave & 3) * 32;
+    const int wp = (wave >> 2) * 64, wq = (wave & 3) * 16;
 
     v4f acc[FP][FQ], sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
@@ -660,14 +675,14 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
 #pragma unroll
         for (int j = 0; j < FQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
     const Fragments<B, TA> ga(wp);
-    const Fragments<B, TB> gb(wq);
+    const Fragments<64, TB> gb(wq);
     const uint32_t base = lds_address(lds);
     v8bf fa[2][FP], fb[2][FQ];
     const auto read = [&](uint32_t tile) {
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
 #pragma unroll
-            for (int j = 0; j < FQ; ++j) fb[s][j] = gb.get(tile + 2 * kTile, j, s);
+            for (int j = 0; j < FQ; ++j) fb[s][j] = gb.get(tile + 2 * (kA + j * kB), 0, s);
 #pragma unroll
             for (int i = 0; i < FP; ++i) fa[s][i] = ga.get(tile, i, s);
         }
@@ -705,16 +720,17 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
     const int n = whole_steps(g, split);
     if (n > 0) {
         Direct<B, TA, T, 1> da;
-        Direct<B, TB, T, 1> db;
-        constexpr int kLoads = Direct<B, TA, T, 1>::kLoads + Direct<B, TB, T, 1>::kLoads;
+        Direct<64, TB, T, FQ> db;
+        constexpr int kLoads = Direct<B, TA, T, 1>::kLoads + FQ * Direct<64, TB, T, FQ>::kLoads;
         da.init(d.a, d.lda, p0, d.P, r0);
         db.init(d.b, d.ldb, q0, d.Q, r0);
         // loads of tiles behind the last are stopped by their buffer's range
         const auto load = [&](int k) {
             const int records = k < n ? kAllRecords : 0;
-            const uint32_t to = base + 4 * kTile * (k % kSlots);
+            const uint32_t to = base + 2 * kSlot * (k % kSlots);
             da.issue(0, da.base, to, wave, records);
-            db.issue(0, db.base, to + 2 * kTile, wave, records);
+#pragma unroll
+            for (int j = 0; j < FQ; ++j) db.issue(j, db.base, to + 2 * (kA + j * kB), wave, records);
             da.base += da.step;
             db.base += db.step;
         };
@@ -725,7 +741,7 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
         if (wave >= 4) meet_waves();
 #pragma unroll 1
         for (int k = 0; k < n; ++k) {
-            read(base + 4 * kTile * (k % kSlots));
+            read(base + 2 * kSlot * (k % kSlots));
             load(k + kSlots - 1);
             loads_landed<(kSlots - 2) * kLoads>();
             meet_waves();
@@ -740,7 +756,8 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
         // what is left of the reduction, with its end masked
         const int64_t r = r0 + (int64_t)n * kBR;
         stage_tail<B, TA, T>(lds, d.a, d.lda, p0, d.P, r, r1);
-        stage_tail<B, TB, T>(lds + kTile, d.b, d.ldb, q0, d.Q, r, r1);
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) stage_tail<64, TB, T>(lds + kA + j * kB, d.b, d.ldb, q0 + 64 * j, d.Q, r, r1);
         meet_waves();
         read(base);
         multiply();
@@ -748,9 +765,9 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
     }
     if constexpr (SUM)
         if (turn.on)
-            put_sums(g, split, turn, g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 16 * (wave >> 2), sum);
+            put_sums(g, split, turn, g.sum_of == 1 ? p0 + wp + 16 * (wave & 3) : q0 + wq + 64 * (wave >> 2), sum);
     finish<EPI, sizeof(lds), 8>(g, split, acc, lds, wave, [&](int i) { return p0 + wp + 16 * i; },
-                                [&](int j) { return q0 + wq + 16 * j; });
+                                [&](int j) { return q0 + wq + 64 * j; });
 }
 
 // 256 x 256 outputs by eight waves, one workgroup to a compute unit. Operand tiles of
@@ -1262,14 +1279,23 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
     if (!pl.wide || pl.full < wide) {
         g.first_wide = pl.wide ? (int32_t)pl.full : -1;
         g.tiles = (int32_t)(pl.wide ? 4 * (wide - pl.full) : tiles);
+        // Tiles that get a compute unit each go to the eight-wave kernel (8192 x 768 x 2304
+        // forward, whose quarters they are, 43.1 -> 40.4 us), more to the four-wave one, two
+        // to a unit (with eight waves the GPT-2 projection 19.5 -> 23.1 us, its gradient by
+        // input over 2304 outputs 34.6 -> 39.9); and where 192 columns a tile make them fit,
+        // to the eight-wave kernel again (those two 19.1 -> 18.4 and 33.1 -> 28.9 us).
         const bool mid = direct && (int64_t)g.tiles * splits <= 256;
+        const int64_t tiles3 = ((P + 127) / 128) * ((Q + 191) / 192);
+        const bool three = direct && !mid && !pl.wide && splits == 1 && !g.sums && tiles3 <= 256;
+        if (three) g.tiles = (int32_t)tiles3;
         const auto pick = [&](auto sums) {
             constexpr bool S = decltype(sums)::value;
-            return mid ? k_product_mid<TA, TB, EPI, S>
+            return mid ? k_product_mid<TA, TB, EPI, S, 2>
                        : direct ? k_product<TA, TB, EPI, true, S> : k_product<TA, TB, EPI, false, S>;
         };
-        const auto k = kSums && g.sums ? pick(std::integral_constant<bool, kSums>{}) : pick(std::false_type{});
-        hipLaunchKernelGGL(k, dim3((unsigned)g.tiles * splits), dim3(mid ? 512 : 256), 0, st, g);
+        const auto k = three ? k_product_mid<TA, TB, EPI, false, 3>
+                             : kSums && g.sums ? pick(std::integral_constant<bool, kSums>{}) : pick(std::false_type{});
+        hipLaunchKernelGGL(k, dim3((unsigned)g.tiles * splits), dim3(mid || three ? 512 : 256), 0, st, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!g.part && !g.sums) return e;
