@@ -583,6 +583,39 @@ def test_tiles_of_192_columns(Z, rows, cols, inner, layout):
     assert dw.intact_outside()
 
 
+@pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("inner", [264, 129, 1])
+@pytest.mark.parametrize("odd", ["a", "b"])
+def test_one_operand_of_odd_rows(Z, odd, inner, layout):
+    """One operand with rows on 16 bytes, the other without, in each direction."""
+    rng = rng_of((19, odd, inner, layout))
+    say("one odd", odd, inner, layout)
+    rows, cols = 301, 203
+
+    def mat(which, r, c):
+        return inp(rng, r, c, scale=0.3, pad_ld=-c % 8 + (5 if which == odd else 0), shift=3 if which == odd else 0)
+
+    x, w = mat("a", rows, inner), mat("b", *((cols, inner) if layout == 0 else (inner, cols)))
+    y = Mat(rows, cols, F32, ld=cols + 1)
+    Z.zero_linear_forward(x.t, w.t, w_layout=layout, y=y.t)
+    want, err, _, _ = R.linear_forward(x.f64(), w64(w, layout), out="f32")
+    close("y", y.t, want, err)
+    dz, w = mat("a", rows, inner), mat("b", *((inner, cols) if layout == 0 else (cols, inner)))
+    dx = Mat(rows, cols, BF, ld=cols + 1)
+    Z.zero_linear_grad_input(dz.t, w.t, w_layout=layout, dx=dx.t)
+    want, err = R.linear_grad_input(dz.f64(), w64(w, layout))
+    close("dx", dx.t, want, err)
+    dz, x = mat("a" if layout == 0 else "b", inner, rows), mat("b" if layout == 0 else "a", inner, cols)
+    r, c = (rows, cols) if layout == 0 else (cols, rows)
+    dw, db = Mat(r, c, F32, ld=c + 3), torch.empty(rows, dtype=F32, device=dev())
+    Z.zero_linear_grad_weight(dz.t, x.t, dw.t, db, w_layout=layout)
+    want, err = R.linear_grad_weight(dz.f64(), x.f64(), out="f32")
+    close("dw", dw.t if layout == 0 else dw.t.t(), want, err)
+    want, err = R.column_sums(dz.f64(), out="f32")
+    close("db", db, want, err)
+    assert y.intact_outside() and dx.intact_outside() and dw.intact_outside()
+
+
 @pytest.mark.parametrize("N", [(1 << 26) - 3, (1 << 26) + 9])
 def test_most_columns(Z, N):
     """Both sides of the width up to which one row takes a launch of its own."""

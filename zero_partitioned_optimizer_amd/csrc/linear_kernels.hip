@@ -511,11 +511,16 @@ __device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split,
     return turn;
 }
 
-// 128 x 128 outputs by four waves, 64 x 64 each (4 x 4 blocks), for outputs of few
-// tiles and, without DIRECT, for operands at any address: tiles of 64 reduction
-// elements, two in LDS, the next one loading while one is multiplied. Two
-// workgroups of 64 KB fit a compute unit and fill each other's waits.
-template <bool TA, bool TB, int EPI, bool DIRECT, bool SUM>
+// 128 x 128 outputs by four waves, 64 x 64 each (4 x 4 blocks), for outputs of more tiles
+// than compute units but too few for the wide kernel, and for operands at any address:
+// tiles of 64 reduction elements, two in LDS, the next one loading while one is
+// multiplied. Two workgroups of 64 KB fit a compute unit and fill each other's waits. An
+// operand goes straight to LDS where its rows allow it (DA, DB), through registers
+// elsewhere: gradient by input of 1023 x 768 through 50,257 outputs, whose dz has odd
+// rows, 101 us, 780 TFLOP/s (113 with both operands through registers; 76 through 50,256
+// outputs, with neither). What bounds it there is the odd rows' loads, which touch two
+// cache lines where aligned ones touch one.
+template <bool TA, bool TB, int EPI, bool DA, bool DB, bool SUM>
 __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 2 * kTile];
@@ -567,7 +572,7 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
         }
     };
 
-    if constexpr (DIRECT) {
+    if constexpr (DA && DB) {
         const int full = whole_steps(g, split);
         Direct<B, TA, T, 1> da;
         Direct<B, TB, T, 1> db;
@@ -597,32 +602,46 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
             multiply(base + 4 * kTile * (full & 1));
         }
     } else {
-        // the next tile waits in registers while one is multiplied
+        // the next tile waits in registers while one is multiplied, or, of an operand
+        // that can, is on its way to LDS
         const int full = whole_steps(g, split);
-        Stage<B, TA, T> sa;
-        Stage<B, TB, T> sb;
+        std::conditional_t<DA, Direct<B, TA, T, 1>, Stage<B, TA, T>> sa;
+        std::conditional_t<DB, Direct<B, TB, T, 1>, Stage<B, TB, T>> sb;
+        const auto load = [&]() {
+            if constexpr (!DA) sa.load(d.P);
+            if constexpr (!DB) sb.load(d.Q);
+        };
+        const auto store = [&](int k) {
+            uint16_t* const to = lds + 2 * kTile * (k & 1);
+            if constexpr (!DA) sa.store(to);
+            if constexpr (!DB) sb.store(to + kTile);
+        };
+        const auto issue = [&](int k) {
+            const uint32_t to = base + 4 * kTile * (k & 1);
+            if constexpr (DA) {
+                sa.issue(0, sa.base, to, wave, kAllRecords);
+                sa.base += sa.step;
+            }
+            if constexpr (DB) {
+                sb.issue(0, sb.base, to + 2 * kTile, wave, kAllRecords);
+                sb.base += sb.step;
+            }
+        };
         if (full > 0) {
             sa.init(d.a, d.lda, p0, d.P, r0);
             sb.init(d.b, d.ldb, q0, d.Q, r0);
-            sa.load(d.P);
-            sb.load(d.Q);
-            sa.store(lds);
-            sb.store(lds + kTile);
-            if (full > 1) {
-                sa.load(d.P);
-                sb.load(d.Q);
-            }
+            issue(0);
+            load();
+            store(0);
+            if (full > 1) load();
         }
         for (int k = 0; k < full; ++k) {
+            if constexpr (DA || DB) loads_landed<0>();
             meet_waves();
             if (k + 1 < full) {
-                uint16_t* const to = lds + 2 * kTile * ((k + 1) & 1);
-                sa.store(to);
-                sb.store(to + kTile);
-                if (k + 2 < full) {
-                    sa.load(d.P);
-                    sb.load(d.Q);
-                }
+                issue(k + 1);
+                store(k + 1);
+                if (k + 2 < full) load();
             }
             multiply(base + 4 * kTile * (k & 1));
         }
@@ -1250,7 +1269,8 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
         }
     const bool some = d.P > 0 && d.Q > 0;
     if (!some && !d.bias_out) return hipSuccess;
-    const bool direct = some && direct_ok(d.a, d.lda, TA ? d.R : d.P) && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
+    const bool da = some && direct_ok(d.a, d.lda, TA ? d.R : d.P), db = some && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
+    const bool direct = da && db;
     const Plan pl = plan_of(d.P, d.Q, d.R, direct);
     const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;
     const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
@@ -1291,7 +1311,8 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
         const auto pick = [&](auto sums) {
             constexpr bool S = decltype(sums)::value;
             return mid ? k_product_mid<TA, TB, EPI, S, 2>
-                       : direct ? k_product<TA, TB, EPI, true, S> : k_product<TA, TB, EPI, false, S>;
+                       : da ? (db ? k_product<TA, TB, EPI, true, true, S> : k_product<TA, TB, EPI, true, false, S>)
+                            : (db ? k_product<TA, TB, EPI, false, true, S> : k_product<TA, TB, EPI, false, false, S>);
         };
         const auto k = three ? k_product_mid<TA, TB, EPI, false, 3>
                              : kSums && g.sums ? pick(std::integral_constant<bool, kSums>{}) : pick(std::false_type{});
