@@ -584,6 +584,44 @@ def test_tiles_of_192_columns(Z, rows, cols, inner, layout):
 
 
 @pytest.mark.parametrize("layout", LAYOUTS)
+@pytest.mark.parametrize("rows,cols", [(8190, 2810), (2810, 8060)])
+def test_rectangles(Z, rows, cols, layout):
+    """Outputs whose last columns, or last rows, go to tiles of 192 columns in a launch
+    behind the largest tiles', in each direction and with all that the epilogue takes."""
+    rng = rng_of((20, rows, cols, layout))
+    say("rectangles", rows, cols, layout)
+    inner, pad = 968, -cols % 8
+    x, w = inp(rng, rows, inner), weight(rng, inner, cols, layout, (pad if layout else 0, 0), 0.03)
+    res, b, y = inp(rng, rows, cols, pad_ld=1), inp(rng, 1, cols), Mat(rows, cols, BF, ld=cols + 5)
+    z = Mat(rows, cols, BF, ld=cols + 2)
+    Z.zero_linear_forward(x.t, w.t, b.t[0], w_layout=layout, act=2, dropout=Z.zero_dropout(0.5, 4, 4), residual=res.t,
+                          y=y.t, preact=z.t)
+    want, err, wz, ez = R.linear_forward(x.f64(), w64(w, layout), b.f64()[0], act_name="gelu", p=0.5, seed=4, offset=4,
+                                         residual=res.f64())
+    close("y", y.t, want, err)
+    close("z", z.t, wz, ez)
+    assert y.intact_outside() and z.intact_outside()
+    dz, w = inp(rng, rows, inner), weight(rng, cols, inner, layout, (0 if layout else pad, 0), 0.03)
+    dx = Mat(rows, cols, BF, ld=cols + 7)
+    Z.zero_linear_grad_input(dz.t, w.t, w_layout=layout, act=3, preact=res.t, dropout=Z.zero_dropout(0.2, 5, 5), dx=dx.t)
+    want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="silu", z=res.f64(), p=0.2, seed=5, offset=5)
+    close("dx", dx.t, want, err)
+    assert dx.intact_outside()
+    r, c = (rows, cols) if layout == 0 else (cols, rows)
+    dz, x = inp(rng, inner, rows, pad_ld=-rows % 8), inp(rng, inner, cols, pad_ld=pad)
+    for bias in (False, True):
+        dw = Mat(r, c, F32, ld=c + 1, fill=rand(rng, r, c))
+        db = torch.zeros(rows, dtype=F32, device=dev()) if bias else None
+        old = w64(dw, layout)
+        Z.zero_linear_grad_weight(dz.t, x.t, dw.t, db, w_layout=layout, accumulate=True)
+        want, err = R.linear_grad_weight(dz.f64(), x.f64(), old=old, out="f32")
+        close("dw", dw.t if layout == 0 else dw.t.t(), want, err)
+        assert dw.intact_outside()
+    want, err = R.column_sums(dz.f64(), out="f32")
+    close("db", db, want, err)
+
+
+@pytest.mark.parametrize("layout", LAYOUTS)
 @pytest.mark.parametrize("inner", [264, 129, 1])
 @pytest.mark.parametrize("odd", ["a", "b"])
 def test_one_operand_of_odd_rows(Z, odd, inner, layout):

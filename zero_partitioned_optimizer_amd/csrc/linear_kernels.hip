@@ -22,8 +22,10 @@ struct ProductArgs {
     int64_t r_per_split;            // multiple of kBR
     int32_t splits;
     int32_t tiles;                  // output tiles of the launch's kind
-    int32_t first_wide;             // k_product: -1, or its workgroups are the quarters of the wide
-                                    // tiles from this one on
+    int32_t np, nq;                 // down and across, the wide tiles where a launch takes their quarters
+    int64_t p0, q0;                 // the first tile's first row and column
+    int32_t first_wide;             // -1, or the workgroups are the quarters of the wide tiles from this
+                                    // one on
     int64_t ld_part;                // row length of a split's partial products
     float* part;                    // [splits, P, ld_part], or nullptr: epilogue in place
     int32_t sum_of;                 // weight gradient with a bias: 1, 2: sums of operand a, b
@@ -493,22 +495,20 @@ __device__ __forceinline__ void finish(const ProductArgs& g, int split, const v4
 
 // The tile of 128 rows and COLS columns of a workgroup: of all of them, or (128 columns)
 // of the quarters of wide tiles.
-template <bool SUM, int COLS>
-__device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split, int* tp, int* tq) {
-    int np = (int)((g.d.P + 127) / 128), nq = (int)((g.d.Q + COLS - 1) / COLS);
-    if (SUM) np = np < 1 ? 1 : np, nq = nq < 1 ? 1 : nq;     // a bias alone
-    const int id = tile_in_turn(g, split);
+template <int COLS>
+__device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split, int64_t* p0, int64_t* q0) {
+    const int id = tile_in_turn(g, split), np = g.np, nq = g.nq;
+    int tp, tq;
     if (g.first_wide < 0) {
-        tile_place(id, np, nq, tp, tq);
-        return g.sum_of == 1 ? SumTurn{*tq, nq, true} : SumTurn{*tp, np, g.sum_of == 2};
+        tile_place(id, np, nq, &tp, &tq);
+        *p0 = g.p0 + (int64_t)tp * 128;
+        *q0 = g.q0 + (int64_t)tq * COLS;
+        return g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
     }
-    np = (np + 1) / 2, nq = (nq + 1) / 2;
-    tile_place(g.first_wide + (id >> 2), np, nq, tp, tq);
-    const SumTurn turn =
-        g.sum_of == 1 ? SumTurn{*tq, nq, (id & 1) == 0} : SumTurn{*tp, np, g.sum_of == 2 && (id & 2) == 0};
-    *tp = 2 * *tp + ((id >> 1) & 1);
-    *tq = 2 * *tq + (id & 1);
-    return turn;
+    tile_place(g.first_wide + (id >> 2), np, nq, &tp, &tq);
+    *p0 = (int64_t)tp * 256 + 128 * ((id >> 1) & 1);
+    *q0 = (int64_t)tq * 256 + 128 * (id & 1);
+    return g.sum_of == 1 ? SumTurn{tq, nq, (id & 1) == 0} : SumTurn{tp, np, g.sum_of == 2 && (id & 2) == 0};
 }
 
 // 128 x 128 outputs by four waves, 64 x 64 each (4 x 4 blocks), for outputs of more tiles
@@ -525,9 +525,9 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 2 * kTile];
     const ProductDesc& d = g.d;
-    int split, tp, tq;
-    SumTurn turn = small_place<SUM, B>(g, &split, &tp, &tq);
-    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    int split;
+    int64_t p0, q0;
+    SumTurn turn = small_place<B>(g, &split, &p0, &q0);
     if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
     const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
@@ -679,9 +679,9 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
     static_assert(!SUM || FQ == 2, "two waves share a block of b, and sum one each");
     __shared__ __attribute__((aligned(16))) uint16_t lds[kSlots * kSlot];
     const ProductDesc& d = g.d;
-    int split, tp, tq;
-    SumTurn turn = small_place<SUM, 64 * FQ>(g, &split, &tp, &tq);
-    const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * (64 * FQ);
+    int split;
+    int64_t p0, q0;
+    SumTurn turn = small_place<64 * FQ>(g, &split, &p0, &q0);
     if (g.first_wide >= 0 && (p0 >= d.P || q0 >= d.Q)) return;
     const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
@@ -815,9 +815,8 @@ __global__ void __launch_bounds__(512) k_product_wide(const ProductArgs g) {
     __shared__ __attribute__((aligned(16))) uint16_t lds[2 * 4 * kHalf];
     const ProductDesc& d = g.d;
     int split, tp, tq;
-    const int np = (int)((d.P + B - 1) / B), nq = (int)((d.Q + B - 1) / B);
-    tile_place(tile_in_turn(g, &split), np, nq, &tp, &tq);
-    SumTurn turn = g.sum_of == 1 ? SumTurn{tq, nq, true} : SumTurn{tp, np, g.sum_of == 2};
+    tile_place(tile_in_turn(g, &split), g.np, g.nq, &tp, &tq);
+    SumTurn turn = g.sum_of == 1 ? SumTurn{tq, g.nq, true} : SumTurn{tp, g.np, g.sum_of == 2};
     const int64_t p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
     const int64_t r0 = (int64_t)split * g.r_per_split;
     const int64_t r1 = r0 + g.r_per_split < d.R ? r0 + g.r_per_split : d.R;
@@ -1165,25 +1164,32 @@ __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
 // products of 256 and more tiles: a 64-deep step of a 256 x 256 tile takes 1.5, one
 // of two 128 x 128 tiles that share a compute unit 1.0 (1.5 through registers), of
 // one alone 0.65; a tile's start and epilogue 7 and 3; a join 3 and its bytes at
-// 4.5 TB/s.
+// 4.5 TB/s. A step of a 128 x 192 tile takes 0.5 in one round and 0.8 in two that
+// follow the wide tiles' (which then run slower, all compute units being busy): 0.72
+// keeps the Llama-7B shaped layer's 8192 x 4096 x 11008 (five rounds of wide tiles and
+// one of 128 x 192, 610 -> 601 us) and the head's weight gradient (50,256 x 768, 88.4 ->
+// 84.2 us) and leaves its f32 weight gradient, whose rest would be two (627 against 638).
 struct Plan {
     bool wide;
     int32_t splits;
     int64_t per;                    // reduction elements per split
-    int64_t full;                   // wide tiles of whole rounds of the chip; the rest as quarters
-};
+    int64_t full;                   // wide tiles of whole rounds of the chip; the rest as quarters,
+    int64_t rows, cols;             // or, where these many tiles down and across are wide, in tiles of
+};                                  // 128 x 192
 static double small_time(int64_t tiles, int64_t steps, bool direct) {
     const double two = direct ? 1.0 : 1.5, one = direct ? 0.65 : 1.0;
     const int64_t full = tiles / 512, rest = tiles % 512;
     return full * (two * steps + 3) + (rest == 0 ? 0 : rest <= 256 ? one * steps + 3 : two * steps + 3);
 }
-static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
+static int64_t over(int64_t n, int64_t by) { return n > 0 ? (n + by - 1) / by : 0; }
+static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct, bool sums) {
     // a bias gradient beside a weight of no elements still has its column of tiles
     if (P < 1) P = 1;
     if (Q < 1) Q = 1;
     const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
     const int64_t steps = (R + kBR - 1) / kBR;
-    Plan best{false, 1, steps > 0 ? steps * kBR : kBR, 0};
+    const int64_t down = over(P, 256), across = over(Q, 256);
+    Plan best{false, 1, steps > 0 ? steps * kBR : kBR, 0, down, across};
     double least = 1e300;
     for (int64_t s = 1; s <= 64 && (s == 1 || (steps + s - 1) / s >= 2); ++s) {
         const int64_t each = steps > 0 ? (steps + s - 1) / s : 1, parts = steps > 0 ? (steps + each - 1) / each : 1;
@@ -1193,7 +1199,7 @@ static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
         const double small = small_time(tiles * parts, each, direct) + join;
         if (small < least) {
             least = small;
-            best = Plan{false, (int32_t)parts, each * kBR, 0};
+            best = Plan{false, (int32_t)parts, each * kBR, 0, down, across};
         }
         if (!direct) continue;
         const int64_t rounds = wide * parts / 256, rest = wide * parts % 256;
@@ -1206,7 +1212,19 @@ static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct) {
         }
         if (t < least) {
             least = t;
-            best = Plan{true, (int32_t)parts, each * kBR, full};
+            best = Plan{true, (int32_t)parts, each * kBR, full, down, across};
+        }
+        if (parts > 1 || sums || rounds == 0 || rest == 0) continue;
+        // the whole rounds as a rectangle, whole columns of tiles or whole rows
+        for (int k = 0; k < 2; ++k) {
+            const int64_t rows = k ? rounds * 256 / across : down, cols = k ? across : rounds * 256 / down;
+            if (rows < 1 || cols < 1) continue;
+            const int64_t left = k ? over(P - 256 * rows, 128) * over(Q, 192) : over(P, 128) * over(Q - 256 * cols, 192);
+            t = over(rows * cols, 256) * round + over(left, 256) * (0.72 * each + 7) + 3;
+            if (t < least) {
+                least = t;
+                best = Plan{true, 1, each * kBR, rows * cols, rows, cols};
+            }
         }
     }
     return best;
@@ -1237,16 +1255,18 @@ static int32_t sum_rows(const Plan& pl, int64_t other) {
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb) {
     if (!ta && !tb && few(P, Q, R, tb)) return 0;       // at any alignment
     size_t most = 0;
-    for (int direct = 0; direct < 2; ++direct) {
-        const size_t b = part_bytes(plan_of(P, Q, R, direct != 0), P, Q);
-        if (b > most) most = b;
-    }
+    for (int direct = 0; direct < 2; ++direct)
+        for (int sums = 0; sums < (ta && tb ? 2 : 1); ++sums) {
+            const size_t b = part_bytes(plan_of(P, Q, R, direct != 0, sums != 0), P, Q);
+            if (b > most) most = b;
+        }
     return most;
 }
 size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a) {
     size_t most = 0;
     for (int direct = 0; direct < 2; ++direct) {
-        const size_t b = (size_t)sum_rows(plan_of(P, Q, R, direct != 0), of_a ? Q : P) * (size_t)up8(of_a ? P : Q) * sizeof(float);
+        const Plan pl = plan_of(P, Q, R, direct != 0, true);
+        const size_t b = (size_t)sum_rows(pl, of_a ? Q : P) * (size_t)up8(of_a ? P : Q) * sizeof(float);
         if (b > most) most = b;
     }
     return most;
@@ -1271,9 +1291,10 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
     if (!some && !d.bias_out) return hipSuccess;
     const bool da = some && direct_ok(d.a, d.lda, TA ? d.R : d.P), db = some && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
     const bool direct = da && db;
-    const Plan pl = plan_of(d.P, d.Q, d.R, direct);
-    const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;
-    const int64_t tiles = ((P + 127) / 128) * ((Q + 127) / 128), wide = ((P + 255) / 256) * ((Q + 255) / 256);
+    const Plan pl = plan_of(d.P, d.Q, d.R, direct, EPI == kEpiGradWeight && d.bias_out);
+    const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;     // a bias alone has tiles too
+    const int64_t tiles = over(P, 128) * over(Q, 128), wide = pl.rows * pl.cols;
+    const bool rectangle = pl.rows * 256 < P || pl.cols * 256 < Q;
     ProductArgs g{};
     g.d = d;
     g.splits = pl.splits;
@@ -1292,22 +1313,34 @@ static hipError_t product(const ProductDesc& d, hipStream_t st) {
     hipError_t e = hipSuccess;
     if (pl.wide) {
         g.tiles = (int32_t)pl.full;
+        g.np = (int32_t)pl.rows;
+        g.nq = (int32_t)pl.cols;
         const auto k = kSums && g.sums ? k_product_wide<TA, TB, EPI, kSums> : k_product_wide<TA, TB, EPI, false>;
         hipLaunchKernelGGL(k, dim3((unsigned)pl.full * splits), dim3(512), 0, st, g);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
-    if (!pl.wide || pl.full < wide) {
-        g.first_wide = pl.wide ? (int32_t)pl.full : -1;
-        g.tiles = (int32_t)(pl.wide ? 4 * (wide - pl.full) : tiles);
+    if (!pl.wide || pl.full < wide || rectangle) {
+        const bool quarters = pl.wide && !rectangle;
+        g.first_wide = quarters ? (int32_t)pl.full : -1;
+        if (!quarters) {
+            if (rectangle && pl.cols * 256 < Q) g.q0 = pl.cols * 256;
+            else if (rectangle) g.p0 = pl.rows * 256;
+            g.np = (int32_t)over(P - g.p0, 128);
+            g.nq = (int32_t)over(Q - g.q0, 128);
+        }
+        g.tiles = (int32_t)(quarters ? 4 * (wide - pl.full) : tiles);
         // Tiles that get a compute unit each go to the eight-wave kernel (8192 x 768 x 2304
         // forward, whose quarters they are, 43.1 -> 40.4 us), more to the four-wave one, two
         // to a unit (with eight waves the GPT-2 projection 19.5 -> 23.1 us, its gradient by
         // input over 2304 outputs 34.6 -> 39.9); and where 192 columns a tile make them fit,
         // to the eight-wave kernel again (those two 19.1 -> 18.4 and 33.1 -> 28.9 us).
-        const bool mid = direct && (int64_t)g.tiles * splits <= 256;
-        const int64_t tiles3 = ((P + 127) / 128) * ((Q + 191) / 192);
-        const bool three = direct && !mid && !pl.wide && splits == 1 && !g.sums && tiles3 <= 256;
-        if (three) g.tiles = (int32_t)tiles3;
+        const bool mid = direct && !rectangle && (int64_t)g.tiles * splits <= 256;
+        const int64_t across3 = over(Q - g.q0, 192), tiles3 = g.np * across3;
+        const bool three = rectangle || (direct && !mid && !pl.wide && splits == 1 && !g.sums && tiles3 <= 256);
+        if (three) {
+            g.nq = (int32_t)across3;
+            g.tiles = (int32_t)tiles3;
+        }
         const auto pick = [&](auto sums) {
             constexpr bool S = decltype(sums)::value;
             return mid ? k_product_mid<TA, TB, EPI, S, 2>
