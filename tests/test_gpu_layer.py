@@ -654,6 +654,68 @@ def test_one_operand_of_odd_rows(Z, odd, inner, layout):
     assert y.intact_outside() and dx.intact_outside() and dw.intact_outside()
 
 
+@pytest.mark.parametrize("rows,cols", [(8190, 765), (8190, 2810), (5000, 4000), (3, 777)])
+def test_empty_reduction(Z, rows, cols):
+    """No inputs at all: the epilogue of zeros, in each kind of tile."""
+    rng = rng_of((21, rows, cols))
+    x, w = torch.empty((rows, 0), dtype=BF, device=dev()), torch.empty((cols, 0), dtype=BF, device=dev())
+    res, b = inp(rng, rows, cols), inp(rng, 1, cols)
+    y = Z.zero_linear_forward(x, w, b.t[0], residual=res.t, dtype=BF)
+    assert torch.equal(y, (res.t.float() + b.t.float()).to(BF))
+    dx = Z.zero_linear_grad_input(x, torch.empty((0, cols), dtype=BF, device=dev()), dtype=F32)
+    assert torch.equal(dx, torch.zeros_like(dx))
+    dw = torch.full((rows, cols), 3.5, dtype=BF, device=dev())
+    dz, a = torch.empty((0, rows), dtype=BF, device=dev()), torch.empty((0, cols), dtype=BF, device=dev())
+    Z.zero_linear_grad_weight(dz, a, dw, accumulate=True)
+    assert bool((dw == 3.5).all())
+    Z.zero_linear_grad_weight(dz, a, dw)
+    assert not bool(dw.any())
+
+
+def test_captured_calls_of_many_tiles(Z):
+    """Products in one launch and in two, split reductions with their join and the bias
+    gradient, captured on one workspace: every replay equals the eager calls, with eager
+    work on a workspace of its own between replays."""
+    rng = rng_of((22,))
+    x, w, dy = inp(rng, 8190, 200), inp(rng, 765, 200, scale=0.1, pad_ld=0), inp(rng, 8190, 765, pad_ld=3)
+    wide = inp(rng, 2810, 968, scale=0.03)
+    h = inp(rng, 8190, 968)
+    need = max(Z.zero_linear_workspace_bytes(k, 0, 8190, a, b) for k in range(3) for a, b in ((200, 765), (968, 2810)))
+    assert need > 0
+
+    def outs():
+        z = lambda r, c, t: torch.zeros((r, c), dtype=t, device=dev())
+        return (z(8190, 765, BF), z(8190, 200, BF), z(765, 200, F32), z(1, 765, F32)[0], z(8190, 2810, BF),
+                torch.empty(need, dtype=torch.uint8, device=dev()))
+
+    def calls(drop, y, dx, dw, db, v, ws):
+        Z.zero_linear_forward(x.t, w.t, dropout=drop, y=y, workspace=ws)
+        Z.zero_linear_grad_input(dy.t, w.t, dropout=drop, dx=dx, workspace=ws)
+        Z.zero_linear_grad_weight(dy.t, x.t, dw, db, accumulate=True, workspace=ws)
+        Z.zero_linear_forward(h.t, wide.t, act=3, dropout=drop, y=v, workspace=ws)
+
+    counter = torch.zeros(1, dtype=torch.int64, device=dev())
+    drop = Z.zero_dropout(0.25, 6, 1, counter=counter)
+    got, want = outs(), outs()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(s):
+        calls(drop, *got)
+        torch.cuda.synchronize()
+        got[2].zero_(), got[3].zero_()
+        with torch.cuda.graph(graph, stream=s):
+            calls(drop, *got)
+    torch.cuda.synchronize()
+    for k in range(4):
+        counter.fill_(k)
+        graph.replay()
+        calls(Z.zero_dropout(0.25, 6, 1 + k), *want)
+        torch.cuda.synchronize()
+        for name, a, b in zip("y dx dw db v".split(), got, want):
+            assert torch.equal(a, b), (k, name)
+
+
 @pytest.mark.parametrize("N", [(1 << 26) - 3, (1 << 26) + 9])
 def test_most_columns(Z, N):
     """Both sides of the width up to which one row takes a launch of its own."""
