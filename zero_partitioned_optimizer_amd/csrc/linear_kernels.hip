@@ -518,8 +518,9 @@ __device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split,
 // operand goes straight to LDS where its rows allow it (DA, DB), through registers
 // elsewhere: gradient by input of 1023 x 768 through 50,257 outputs, whose dz has odd
 // rows, 101 us, 780 TFLOP/s (113 with both operands through registers; 76 through 50,256
-// outputs, with neither). What bounds it there is the odd rows' loads, which touch two
-// cache lines where aligned ones touch one.
+// outputs, with neither, by the wide kernel). From memory it takes 131, aligned loads of
+// the same rows 127: not the addresses bound it but the traffic of small tiles, each
+// operand read from L2 twice as often as the wide kernel does.
 template <bool TA, bool TB, int EPI, bool DA, bool DB, bool SUM>
 __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
