@@ -26,6 +26,49 @@ def test_kernels_use_no_scratch(tmp_path, source, kernel):
     assert not [(n, s) for n, s in zip(names, scratch) if s != 0]
 
 
+def _sgprs(text):
+    out = set()
+    for lo, hi in re.findall(r"\bs\[(\d+):(\d+)\]", text):
+        out |= set(range(int(lo), int(hi) + 1))
+    return out | {int(n) for n in re.findall(r"\bs(\d+)\b", text)}
+
+
+@pytest.mark.skipif(not HIPCC, reason="hipcc not available")
+def test_loads_to_lds_wait_for_their_descriptors(tmp_path):
+    """A scalar register that a vector instruction wrote (v_readfirstlane, v_readlane) may
+    be read by a memory instruction five wait states later. The compiler sees to that for
+    its own instructions but does not look into inline assembly, so each load to LDS there
+    has to bring the distance with it, whatever the compiler puts before it."""
+    from zero_partitioned_optimizer_amd import build as B
+    flags = [f for f in B.HIPCC_FLAGS if f not in ("-fPIC", "-shared")]
+    out = tmp_path / "k.s"
+    subprocess.run([B.hipcc(), *flags, "-I", os.path.join(ROOT, "include"), "-I", B.CSRC, "--cuda-device-only", "-S",
+                    os.path.join(B.CSRC, "linear_kernels.hip"), "-o", str(out)], check=True, capture_output=True)
+    name, before, loads, bad = None, [], 0, []
+    for line in out.read_text().splitlines():
+        line = line.split(";")[0].strip()
+        if line.endswith(":"):              # a block begins: what ran before it is not known
+            name = line if line.startswith("_Z") else name  # the kernel
+            before = ["block"]
+            continue
+        if not line or line.startswith("."):
+            continue
+        if line.startswith("buffer_load") and line.endswith(" lds"):
+            loads += 1
+            reads, states = _sgprs(line), 0
+            for prev in reversed(before):
+                if states >= 5:
+                    break
+                written = prev.startswith("v_") and _sgprs(",".join(prev.split(",")[:2])) & reads
+                if prev == "block" or written:
+                    bad.append((name, states, prev, line))
+                    break
+                states += int(prev.split()[1], 0) + 1 if prev.startswith("s_nop") else 1
+        before = before[-16:] + [line]
+    assert loads > 100
+    assert not bad, (len(bad), bad[:4])
+
+
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="gcc not available")
 def test_header_is_plain_c(tmp_path):
     src = tmp_path / "h.c"

@@ -286,9 +286,13 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 // 16 l behind `to` (the same in all lanes). Written in assembly because the
 // compiler, which sees in its own builtin a store to LDS of unknown extent, waits
 // for it before the next LDS read of any tile. It has no output register; what
-// reads the tile waits with loads_landed first.
+// reads the tile waits with loads_landed first. The descriptor may come from
+// v_readfirstlane (or a spill's v_readlane) right before: a scalar register that a
+// vector instruction wrote takes five wait states until a memory instruction may read
+// it, which the compiler sees to for its own instructions but not inside assembly. The
+// move and the four of s_nop are those five; m0 itself needs one.
 __device__ __forceinline__ void lds_load(v4i rsrc, uint32_t at, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(to), "v"(at), "s"(rsrc)
                  : "memory");
