@@ -69,6 +69,23 @@ def test_loads_to_lds_wait_for_their_descriptors(tmp_path):
     assert not bad, (len(bad), bad[:4])
 
 
+def test_assembly_names_what_it_writes():
+    """A scalar register or flag that inline assembly writes by name is in its list of
+    clobbers: the compiler may otherwise keep a value of its own there."""
+    from zero_partitioned_optimizer_amd import build as B
+    seen = 0
+    for source in B.SOURCES:
+        text = open(os.path.join(B.CSRC, source)).read()
+        for block in re.findall(r"asm volatile\((.*?)\);", text, re.S):
+            code = "".join(re.findall(r'"([^"]*)"', block.split("\n" + " " * 8 + ":")[0].split(" : ")[0]))
+            clobbers = set(re.findall(r'"([^"]*)"', block.split(":")[-1]))
+            written = set(re.findall(r"\b\w+ (m0|vcc|exec)\b,", code)) | (
+                {"scc"} if re.search(r"\bs_(add|sub|and|or|cmp|lshl|lshr)", code) else set())
+            seen += bool(written)
+            assert written <= clobbers, (source, written - clobbers, block)
+    assert seen
+
+
 @pytest.mark.skipif(shutil.which("gcc") is None, reason="gcc not available")
 def test_header_is_plain_c(tmp_path):
     src = tmp_path / "h.c"

@@ -300,20 +300,20 @@ __device__ __forceinline__ void lds_loads(v4i rsrc, const uint32_t* at, uint32_t
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %2, %1, 0 offen lds"
                      :
                      : "s"(to), "s"(rsrc), "v"(at[0])
-                     : "memory");
+                     : "memory", "m0");
     else if constexpr (N == 2)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %3, %1, 0 offen lds\n\t"
                      "s_add_u32 m0, %0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %4, %1, 0 offen lds"
                      :
                      : "s"(to), "s"(rsrc), "n"(STEP), "v"(at[0]), "v"(at[1])
-                     : "memory", "scc");
+                     : "memory", "m0", "scc");
     else if constexpr (N == 3)
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %4, %1, 0 offen lds\n\t"
                      "s_add_u32 m0, %0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %5, %1, 0 offen lds\n\t"
                      "s_add_u32 m0, %0, %3\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %1, 0 offen lds"
                      :
                      : "s"(to), "s"(rsrc), "n"(STEP), "n"(2 * STEP), "v"(at[0]), "v"(at[1]), "v"(at[2])
-                     : "memory", "scc");
+                     : "memory", "m0", "scc");
     else {
         asm volatile("s_mov_b32 m0, %0\n\ts_nop 3\n\tbuffer_load_dwordx4 %5, %1, 0 offen lds\n\t"
                      "s_add_u32 m0, %0, %2\n\ts_nop 0\n\tbuffer_load_dwordx4 %6, %1, 0 offen lds\n\t"
@@ -322,7 +322,7 @@ __device__ __forceinline__ void lds_loads(v4i rsrc, const uint32_t* at, uint32_t
                      :
                      : "s"(to), "s"(rsrc), "n"(STEP), "n"(2 * STEP), "n"(3 * STEP), "v"(at[0]), "v"(at[1]),
                        "v"(at[2]), "v"(at[3])
-                     : "memory", "scc");
+                     : "memory", "m0", "scc");
         if constexpr (N > 4) lds_loads<N - 4, STEP>(rsrc, at + 4, to + 4 * STEP);
     }
 }
