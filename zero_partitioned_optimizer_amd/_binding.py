@@ -484,10 +484,20 @@ class GatherPlan:
 def zero_gather_tensors(shards, shard_S: int, offsets, numels, outs=None, stream=None):
     """Copy whole tensors out of the rank shards (device tensors of shard_S elements,
     2- or 4-byte elements). outs: device tensors to fill, or None to allocate them
-    (same dtype as the shards). Returns the outputs."""
+    (same dtype as the shards) on the stream that the copies run on; the current stream
+    may use them too, once it waits for that one. Returns the outputs."""
     numels = [int(n) for n in numels]
     if outs is None:
-        outs = [torch.empty(n, dtype=shards[0].dtype, device=shards[0].device) for n in numels]
+        def new():
+            return [torch.empty(n, dtype=shards[0].dtype, device=shards[0].device) for n in numels]
+        current = torch.cuda.current_stream()
+        if _stream(stream) == current.cuda_stream:
+            outs = new()
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+                outs = new()
+            for o in outs:
+                o.record_stream(current)
     return GatherPlan(shards, shard_S, offsets, numels, outs)(stream)
 
 

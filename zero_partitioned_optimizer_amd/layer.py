@@ -413,7 +413,8 @@ class FlatLinear:
         self.w, self.b = self._views(params)
 
     def fetch(self, shards, shard_S: int, stream=None) -> None:
-        """Copy the layer's tensors out of the rank shards (bf16 or its bit patterns)."""
+        """Copy the layer's tensors out of the rank shards (bf16 or its bit patterns). Passes
+        may run on the copies' stream, or on the current one once it waits for that."""
         offs = [self.w_off] + ([] if self.b_off is None else [self.b_off])
         nums = [self.K * self.N] + ([] if self.b_off is None else [self.N])
         got = B.zero_gather_tensors(shards, shard_S, offs, nums, stream=stream)
