@@ -57,7 +57,8 @@ typedef enum { ZERO_W_OUT_IN = 0, ZERO_W_IN_OUT = 1 } zero_weight_layout;
 
 /*
  * GELU is the tanh form, z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))); SiLU is
- * z / (1 + exp(-z)); ReLU's slope at 0 is 0.
+ * z / (1 + exp(-z)). ReLU's slope is 1 where z > 0 and 0 elsewhere, at a NaN too
+ * (whose ReLU is NaN); the other slopes at a NaN are NaN.
  */
 typedef enum {
     ZERO_ACT_NONE = 0,

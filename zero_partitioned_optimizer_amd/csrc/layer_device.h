@@ -88,7 +88,7 @@ __device__ __forceinline__ float act_of(int32_t act, float z) {
 // act'(z). Beyond +-32 the smooth activations' slopes are 0 or 1 to far below an
 // fp32 ulp, and holding z there keeps the formulas' products finite for any z.
 __device__ __forceinline__ float act_slope(int32_t act, float z) {
-    if (act == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    if (act == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;            // 0 at a NaN
     const float h = z > 32.0f ? 32.0f : (z < -32.0f ? -32.0f : z);      // NaN stays
     if (act == ZERO_ACT_GELU) {
         const float s = logistic(kGelu2C * fmaf(kGeluA * h, h * h, h));
