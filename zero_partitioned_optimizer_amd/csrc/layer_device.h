@@ -85,11 +85,11 @@ __device__ __forceinline__ float act_of(int32_t act, float z) {
     return z;
 }
 
-// act'(z). Beyond +-32 the smooth activations' slopes are 0 or 1 to far below an
-// fp32 ulp, and holding z there keeps the formulas' products finite for any z.
+// act'(z). Beyond +-128 the logistic is 0 or 1 and the smooth activations' slopes with
+// it, and holding z there keeps the formulas' products finite for any z.
 __device__ __forceinline__ float act_slope(int32_t act, float z) {
     if (act == ZERO_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;            // 0 at a NaN
-    const float h = z > 32.0f ? 32.0f : (z < -32.0f ? -32.0f : z);      // NaN stays
+    const float h = z > 128.0f ? 128.0f : (z < -128.0f ? -128.0f : z);  // NaN stays
     if (act == ZERO_ACT_GELU) {
         const float s = logistic(kGelu2C * fmaf(kGeluA * h, h * h, h));
         return fmaf(h * s * (1.0f - s), kGelu2C * fmaf(3.0f * kGeluA, h * h, 1.0f), s);
