@@ -1275,17 +1275,26 @@ static Plan plan_of(int64_t P, int64_t Q, int64_t R, bool direct, bool sums) {
     return best;
 }
 
-// Whether a product of few rows goes to k_product_few. With b's outer index in rows:
-// up to 4 rows always (one row of GPT-2 qkv 8.2 -> 3.3 us, of a Llama-7B shaped layer
-// 19.9 -> 17.4 us against tiles, splits and a join), up to 16 below 32 MB of b (every
-// workgroup reads all of a: 16 rows of the Llama-7B shaped layer 20.5 -> 23.6 us). With
-// reduced rows, 64 columns to a workgroup: where its workgroups' share of memory
-// (55 KB/us each) beats the join's launch and traffic.
-static bool few(int64_t P, int64_t Q, int64_t R, bool tb) {
+// Whether a product of few rows goes to k_product_few, or to tiles, splits and a join,
+// whichever an estimate in microseconds says is done first.
+// With b's outer index in rows, the eight waves of a workgroup take 1.1 ns for an element
+// of the reduction and 3% of that more for each row of a: one row of GPT-2 qkv 3.3 us, in
+// tiles 8.2; of a Llama-7B shaped layer 17.4 and 19.9; of 8192 through 64 to 768 columns
+// 11.7-12.0 and 12.1-15.1; but of 16,384 through the same 21-24 and 13-19. More than 4 rows
+// go there below 32 MB of b, as every workgroup reads all of a (16 rows of the Llama-7B
+// shaped layer 23.6 and 20.5). Where rows are not on 16 bytes the loads take 3.1 ns an
+// element, and more workgroups than compute units queue: one row of 4097 through 64
+// columns 16.1 and 9.4, through 4096 17.2 and 20.9, through 11,008 43 and 36.
+// With reduced rows, 64 columns to a workgroup: where its workgroups' share of memory
+// (55 KB/us each) beats the join's launch and traffic; rows on 16 bytes only.
+static bool few(int64_t P, int64_t Q, int64_t R, bool tb, bool direct) {
     if (P < 1 || P > 16 || Q < 1 || Q > (int64_t(1) << 26)) return false;   // 2^31 threads
-    if (!tb) return P <= 4 || 2 * Q * R < (int64_t(32) << 20);
     const double bytes = 2.0 * Q * R, groups = (double)((Q + 63) / 64);
-    return bytes / ((groups < 256 ? groups : 256) * 55e3) < 5 + bytes / 6e6;
+    if (tb) return direct && bytes / ((groups < 256 ? groups : 256) * 55e3) < 5 + bytes / 6e6;
+    if (P > 4 && bytes >= (32 << 20)) return false;
+    if (direct) return R * (1.12e-3 + 3.5e-5 * P) < 11 + bytes / 13e6;
+    const double queue = Q > 4096 ? Q / 4096.0 : 1.0;
+    return R < 2048 || R * (3.1e-3 + 1.8e-4 * P) * queue < 6.5 + bytes / 3.3e6;
 }
 
 static int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
@@ -1298,13 +1307,14 @@ static int32_t sum_rows(const Plan& pl, int64_t other) {
 }
 
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb) {
-    if (!ta && !tb && few(P, Q, R, tb)) return 0;       // at any alignment
     size_t most = 0;
-    for (int direct = 0; direct < 2; ++direct)
+    for (int direct = 0; direct < 2; ++direct) {
+        if (!ta && few(P, Q, R, tb, direct != 0)) continue;
         for (int sums = 0; sums < (ta && tb ? 2 : 1); ++sums) {
             const size_t b = part_bytes(plan_of(P, Q, R, direct != 0, sums != 0), P, Q);
             if (b > most) most = b;
         }
+    }
     return most;
 }
 size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a) {
@@ -1324,18 +1334,18 @@ static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
 
 template <bool TA, bool TB, int EPI>
 static hipError_t product(const ProductDesc& d, hipStream_t st) {
+    const bool some = d.P > 0 && d.Q > 0;
+    const bool da = some && direct_ok(d.a, d.lda, TA ? d.R : d.P), db = some && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
+    const bool direct = da && db;
     if constexpr (!TA)
-        if (few(d.P, d.Q, d.R, TB) && (!TB || (direct_ok(d.b, d.ldb, d.R) && direct_ok(d.a, d.lda, d.P)))) {
+        if (few(d.P, d.Q, d.R, TB, direct)) {
             ProductArgs g{};
             g.d = d;
             const int cols = TB ? 64 : 16;
             hipLaunchKernelGGL((k_product_few<TB, EPI>), dim3((unsigned)((d.Q + cols - 1) / cols)), dim3(512), 0, st, g);
             return hipGetLastError();
         }
-    const bool some = d.P > 0 && d.Q > 0;
     if (!some && !d.bias_out) return hipSuccess;
-    const bool da = some && direct_ok(d.a, d.lda, TA ? d.R : d.P), db = some && direct_ok(d.b, d.ldb, TB ? d.R : d.Q);
-    const bool direct = da && db;
     const Plan pl = plan_of(d.P, d.Q, d.R, direct, EPI == kEpiGradWeight && d.bias_out);
     const int64_t P = d.P > 0 ? d.P : 1, Q = d.Q > 0 ? d.Q : 1;     // a bias alone has tiles too
     const int64_t tiles = over(P, 128) * over(Q, 128), wide = pl.rows * pl.cols;
