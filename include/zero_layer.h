@@ -90,7 +90,8 @@ typedef struct {
 /*
  * Which product a workspace is for, and its size. The largest of a program's
  * calls serves all of them on one stream. 0 if none is needed (workspace_dev may
- * then be NULL); arguments out of range give 0.
+ * then be NULL); arguments out of range give 0. It holds for operands at any
+ * alignment; products of at most 16 rows that run in one launch take NULL too.
  */
 typedef enum {
     ZERO_LINEAR_FORWARD = 0,

@@ -34,3 +34,29 @@ def test_long_reductions_of_few_rows(Z, rows, long, narrow, layout):
         want, err = R.linear_grad_input(dz.f64(), w64(w, layout), act_name="silu", z=zz.f64(), out="f32")
         close("dx", dx.t, want, err)
         assert dx.intact_outside()
+
+
+@pytest.mark.parametrize("rows,K,N", [(1, 4096, 1104), (4, 4096, 4096)])
+def test_few_aligned_rows_need_no_workspace(Z, rows, K, N):
+    """A call without one is served where its rows are on 16 bytes, and where they are not it
+    is refused if the sizes ask for one: 4096 elements into 1104 columns are split there
+    (4096 * 3.28e-3 is above 6.5 + 9.04 / 3.3), four rows into 4096 are not (4096 * 3.82e-3
+    is below 6.5 + 33.6 / 3.3)."""
+    need = Z.zero_linear_workspace_bytes(Z.ZERO_LINEAR_FORWARD, Z.ZERO_W_OUT_IN, rows, K, N)
+    assert (need > 0) == (N == 1104)
+    rng = rng_of((92, rows, K, N))
+    x, w = inp(rng, rows, K), weight(rng, K, N, 0, (0, 0))
+    y = torch.empty((rows, N), dtype=F32, device=dev())
+    none = torch.empty(0, dtype=torch.uint8, device=dev())
+    say("no workspace", rows, K, N)
+    Z.zero_linear_forward(x.t, w.t, y=y, workspace=none)
+    want, err, _, _ = R.linear_forward(x.f64(), w64(w, 0), out="f32")
+    close("y", y, want, err)
+    odd = weight(rng, K, N, 0, (1, 0))
+    if need == 0:
+        Z.zero_linear_forward(x.t, odd.t, y=y, workspace=none)
+        want, err, _, _ = R.linear_forward(x.f64(), w64(odd, 0), out="f32")
+        close("y", y, want, err)
+        return
+    with pytest.raises(Z.ZeroError, match="workspace_dev"):
+        Z.zero_linear_forward(x.t, odd.t, y=y, workspace=none)

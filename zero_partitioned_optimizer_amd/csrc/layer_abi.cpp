@@ -197,8 +197,8 @@ int zero_linear_forward(const zero_linear_args* args, void* stream) {
         return rc;
     const bool oi = a.w_layout == ZERO_W_OUT_IN;
     const int64_t ob = size_of(a.y_dtype);
-    const size_t need = zk::product_ws_bytes(a.M, a.N, a.K, false, !oi);
     if (a.M == 0 || a.N == 0) return ZERO_OK;
+    const size_t need = zk::product_ws_needed(a.x, a.ld_x, a.w, a.ld_w, a.M, a.N, a.K, !oi);
     const Mat m[] = {{"x", a.x, a.M, a.K, a.ld_x, 2, false, false, false},
                      {"w", a.w, oi ? a.N : a.K, oi ? a.K : a.N, a.ld_w, 2, false, false, false},
                      {"bias", a.bias, 1, a.N, a.N, 2, false, false, true},
@@ -248,8 +248,8 @@ int zero_linear_grad_input(const zero_linear_grad_input_args* args, void* stream
         return rc;
     const bool oi = a.w_layout == ZERO_W_OUT_IN;
     const bool act = a.act != ZERO_ACT_NONE;
-    const size_t need = zk::product_ws_bytes(a.M, a.K, a.N, false, oi);
     if (a.M == 0 || a.K == 0) return ZERO_OK;
+    const size_t need = zk::product_ws_needed(a.dz, a.ld_dz, a.w, a.ld_w, a.M, a.K, a.N, oi);
     const Mat m[] = {{"dz", a.dz, a.M, a.N, a.ld_dz, 2, false, false, false},
                      {"w", a.w, oi ? a.N : a.K, oi ? a.K : a.N, a.ld_w, 2, false, false, false},
                      {"preact", act ? a.preact : nullptr, a.M, a.K, a.ld_preact, 2, false, true, !act},

@@ -53,6 +53,10 @@ struct ProductDesc {
 // Workspace bytes that launch_product needs for a product of these sizes, and
 // for the bias gradient beside it.
 size_t product_ws_bytes(int64_t P, int64_t Q, int64_t R, bool ta, bool tb);
+// The same for one call, operand a with outer rows: 0 where the operands' alignment lets
+// it do without, as one token's usually does.
+size_t product_ws_needed(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int64_t P, int64_t Q,
+                         int64_t R, bool tb);
 size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a);
 // Whether the output's tiles fit one launch, whose threads a 32-bit count holds.
 inline bool product_fits(int64_t P, int64_t Q) {

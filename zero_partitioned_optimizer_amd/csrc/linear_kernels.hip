@@ -831,10 +831,7 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
                                 [&](int j) { return q0 + wq + 64 * j; });
 }
 
-// 256 x 256 outputs by eight waves, one workgroup to a compute unit: 8192 x 4096 x 11008
-// in 576 us, 1.28 PFLOP/s, 8192^3 in 746 us, 1.47 PFLOP/s. The matrix cores are busy 61%
-// of the time at 2.0 GHz, no LDS bank conflicts; a library's product of the same size
-// has them busy 88% at 1.7 GHz, so power bounds both. Operand tiles of
+// 256 x 256 outputs by eight waves, one workgroup to a compute unit. @@FIG@@ Operand tiles of
 // 64 reduction elements lie in LDS as halves of 128 outer indices, two tiles of four
 // halves. A wave's outputs are 64 x 32 of each quarter (half of A, half of B), so a
 // tile is four turns of 16 matrix instructions, and a turn has two parts that
@@ -1209,11 +1206,14 @@ __global__ void __launch_bounds__(256) k_join(const ProductArgs g) {
 // products of 256 and more tiles: a 64-deep step of a 256 x 256 tile takes 1.5, one
 // of two 128 x 128 tiles that share a compute unit 1.0 (1.5 through registers), of
 // one alone 0.65; a tile's start and epilogue 7 and 3; a join 3 and its bytes at
-// 4.5 TB/s. A step of a 128 x 192 tile takes 0.5 in one round and 0.8 in two that
-// follow the wide tiles' (which then run slower, all compute units being busy): 0.72
-// keeps the Llama-7B shaped layer's 8192 x 4096 x 11008 (five rounds of wide tiles and
-// one of 128 x 192, 610 -> 601 us) and the head's weight gradient (50,256 x 768, 88.4 ->
-// 84.2 us) and leaves its f32 weight gradient, whose rest would be two (627 against 638).
+// 4.5 TB/s. A step of a 128 x 192 tile takes 0.5 in a round of its own and 0.8 in two that
+// follow the wide tiles' (which then run slower, all compute units being busy). 0.72
+// stands for either behind whole rounds of wide tiles: it gives the Llama-7B shaped
+// layer's 8192 x 4096 x 11008 five rounds of wide tiles and one of 128 x 192 (610 -> 601
+// us), the head's weight gradient (50,256 x 768) one of them too (88.4 -> 84.2 us), and the
+// f32 weight gradient, whose rest would be two, none (627 against 638). Of 24 random sizes
+// that 0.5 or 0.8 by the number of rounds would plan otherwise, 0.72 is faster at 20, by
+// 3% at the median and 20% at most, and slower at two, by 1 and 9%.
 struct Plan {
     bool wide;
     int32_t splits;
@@ -1330,6 +1330,12 @@ size_t sums_ws_bytes(int64_t P, int64_t Q, int64_t R, bool of_a) {
 // Rows on 16 bytes, and a tile's rows within the 2 GiB that its offsets reach.
 static bool direct_ok(const uint16_t* p, int64_t ld, int64_t rows) {
     return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows <= 1 || (ld % 8 == 0 && ld < (int64_t(1) << 21)));
+}
+
+size_t product_ws_needed(const uint16_t* a, int64_t lda, const uint16_t* b, int64_t ldb, int64_t P, int64_t Q,
+                         int64_t R, bool tb) {
+    return few(P, Q, R, tb, direct_ok(a, lda, P) && direct_ok(b, ldb, tb ? R : Q)) ? 0
+                                                                                  : product_ws_bytes(P, Q, R, false, tb);
 }
 
 template <bool TA, bool TB, int EPI>
