@@ -133,7 +133,8 @@ typedef struct {
  * without preact, overlap), ZERO_E_ALIGN (a pointer not aligned to its element, a
  * workspace not to 16 bytes), ZERO_E_RANGE (a size outside [0, 2^31 - 1], an output
  * of more than 2^29 rows or columns or 2^23 tiles of 128 x 128, an ld below its
- * columns or above 2^40, a workspace below zero_linear_workspace_bytes), ZERO_E_HIP.
+ * columns or above 2^40, a workspace below zero_linear_workspace_bytes where the call
+ * needs one), ZERO_E_HIP.
  */
 int zero_linear_forward(const zero_linear_args* args, void* stream);
 

@@ -48,7 +48,7 @@ def test_loads_to_lds_wait_for_their_descriptors(tmp_path):
     for line in out.read_text().splitlines():
         line = line.split(";")[0].strip()
         if line.endswith(":"):              # a block begins: what ran before it is not known
-            name = line if line.startswith("_Z") else name  # the kernel
+            name = line if line.startswith("_Z") else name
             before = ["block"]
             continue
         if not line or line.startswith("."):

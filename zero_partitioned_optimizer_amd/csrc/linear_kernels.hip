@@ -559,10 +559,12 @@ __device__ __forceinline__ SumTurn small_place(const ProductArgs& g, int* split,
 // multiplied. Two workgroups of 64 KB fit a compute unit and fill each other's waits. An
 // operand goes straight to LDS where its rows allow it (DA, DB), through registers
 // elsewhere: gradient by input of 1023 x 768 through 50,257 outputs, whose dz has odd
-// rows, 101 us, 780 TFLOP/s (113 with both operands through registers; 76 through 50,256
-// outputs, with neither, by the wide kernel). From memory it takes 131, aligned loads of
-// the same rows 127: not the addresses bound it but the traffic of small tiles, each
-// operand read from L2 twice as often as the wide kernel does.
+// rows, 101 us with its operands in the MALL, 780 TFLOP/s (113 with both operands through
+// registers; 76 through 50,256 outputs, with neither, by the wide kernel). From memory it
+// takes 131, aligned loads of the same rows 127: not the addresses bound it but the
+// traffic of small tiles, each operand read from L2 twice as often as the wide kernel
+// does, and the wait for the direct operand's loads, which takes in the register loads
+// of the tile after it.
 template <bool TA, bool TB, int EPI, bool DA, bool DB, bool SUM>
 __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
     constexpr int T = 256, B = 128, FP = 4, FQ = 4, kTile = B * kBR;
@@ -714,8 +716,9 @@ __global__ void __launch_bounds__(256, 2) k_product(const ProductArgs g) {
 // more after its last reads began; each turn ends when the next turn's tile is here, one
 // barrier before anyone reads it. A turn takes 0.5 us, and what is around the turns 10: for
 // the GPT-2 projection (8192 x 768 x 768 with dropout and residual, 256 tiles of 192
-// columns) 18.4 us, 525 TFLOP/s, 5 of them its epilogue's memory and draws; through the
-// 2304 outputs of qkv 28.9 us, 1.0 PFLOP/s.
+// columns) 18.2 to 20.0 us from memory, by the card, about 510 TFLOP/s, 5 of them its
+// epilogue's memory and draws; gradient by input through the 2304 outputs of qkv 32 us,
+// 905 TFLOP/s (28.9 with its operands in the MALL).
 template <bool TA, bool TB, int EPI, bool SUM, int FQ>
 __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
     constexpr int T = 512, B = 128, FP = 4, kA = B * kBR, kB = 64 * kBR, kSlot = kA + FQ * kB, kSlots = 4;
@@ -831,8 +834,13 @@ __global__ void __launch_bounds__(512) k_product_mid(const ProductArgs g) {
                                 [&](int j) { return q0 + wq + 64 * j; });
 }
 
-// 256 x 256 outputs by eight waves, one workgroup to a compute unit. @@FIG@@ Operand tiles of
-// 64 reduction elements lie in LDS as halves of 128 outer indices, two tiles of four
+// 256 x 256 outputs by eight waves, one workgroup to a compute unit. With the 128 x 192
+// tiles of its rest, 8192 x 4096 x 11008 (SiLU, pre-activation kept) takes 602 to 634 us
+// from memory, by the card it runs on, 1.17-1.23 PFLOP/s; the down projection, two whole
+// rounds, takes 526-546, 1.35-1.41 PFLOP/s, where a library's bare product takes 448-476.
+// The matrix cores are busy 57-71% of the time at 1.9-2.0 GHz, without LDS bank conflicts;
+// as that library has them busy 88% at 1.7 GHz, it is not power that holds the loop.
+// Operand tiles of 64 reduction elements lie in LDS as halves of 128 outer indices, two tiles of four
 // halves. A wave's outputs are 64 x 32 of each quarter (half of A, half of B), so a
 // tile is four turns of 16 matrix instructions, and a turn has two parts that
 // barriers divide: the wave reads what its quarter needs and no turn before it read,
