@@ -69,3 +69,51 @@ def test_fetched_ahead_and_used_on_the_current_stream(Z):
             h, _ = layers[i].forward(h)
             layers[i].release()
         assert torch.equal(h, want)
+
+
+def test_captured_fetch_on_a_side_stream(Z):
+    """Fetch on a forked stream, pass and release inside one graph: every replay copies what
+    the shards hold then."""
+    K, N, M, S = 136, 264, 40, 1 << 15
+    gen = torch.Generator(device=dev())
+    gen.manual_seed(5)
+    shards = [torch.empty(S, dtype=BF, device=dev()) for _ in range(2)]
+    x = torch.randn(M, K, generator=gen, device=dev()).to(BF)
+    layer = Z.FlatLinear([16, 16 + K * N], [K * N, N], 0, 1, K, N)
+    side = torch.cuda.Stream()
+    say("captured fetch", K, N, M)
+
+    def run():
+        cur = torch.cuda.current_stream()
+        side.wait_stream(cur)
+        layer.fetch(shards, S, stream=side)
+        cur.wait_stream(side)
+        y, _ = layer.forward(x)
+        layer.release()
+        side.wait_stream(cur)
+        layer.fetch(shards, S, stream=side)
+        cur.wait_stream(side)
+        z, _ = layer.forward(x, residual=y)
+        layer.release()
+        return z
+
+    for s in shards:
+        s.zero_()
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for it in range(4):
+        flat = (torch.randn(2 * S, generator=gen, device=dev()) * 0.1).to(BF)
+        shards[0].copy_(flat[:S])
+        shards[1].copy_(flat[S:])
+        graph.replay()
+        w, b = flat[16:16 + K * N].view(N, K).clone(), flat[16 + K * N:][:N].clone()
+        want = Z.zero_linear_forward(x, w, b, residual=Z.zero_linear_forward(x, w, b))
+        torch.cuda.synchronize()
+        assert torch.equal(out, want), it
+        assert torch.equal(run(), want), it
