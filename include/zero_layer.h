@@ -215,6 +215,97 @@ typedef struct {
 int zero_dropout_add(const zero_dropout_args* args, void* stream);
 int zero_dropout_grad(const zero_dropout_args* args, void* stream);
 
+/*
+ * The norm of a block's rows and its gradient ("ZeRO Stages": the norms' weights are
+ * among the tensors that stage 3 gathers and whose gradients the step averages; the
+ * pages give no formulas). Over a row x of N columns, with w and b of the norm:
+ *
+ *   forward    s = residual + x                              (or s = x, nothing stored)
+ *              mean = sum(s) / N,  rstd = 1 / sqrt(sum((s - mean)^2) / N + eps)
+ *              y = (s - mean) rstd w + b
+ *   gradient   h = (s - mean) rstd,  g = dy w
+ *              dx = residual_grad + rstd (g - sum(g) / N - h sum(g h) / N)
+ *              dw = [dw +] sum over rows of dy h,  db = [db +] sum over rows of dy
+ *
+ * ZERO_NORM_RMS takes mean as 0 and leaves out sum(g) / N. s is rounded to its own type
+ * before it is normed: the backward pass reads what the forward pass normed, and a call
+ * with a residual gives what an addition and a call without one give. Sums and
+ * statistics are fp32, the variance from the differences to the mean. A row of one
+ * value with eps 0 has rstd = inf and, by the formula, NaN; an infinity or NaN in a row
+ * makes that row's y NaN.
+ */
+typedef enum { ZERO_NORM_LAYER = 0, ZERO_NORM_RMS = 1 } zero_norm_kind;
+
+/*
+ * y, sum and stats of the rows of x. sum is required with a residual and must be NULL
+ * without one. y or sum may be exactly x or residual (same address, type and ld), not
+ * each other. One launch, no workspace.
+ */
+typedef struct {
+    int64_t M, N;
+    const void* x;                 /* [M, N] of x_dtype */
+    int64_t ld_x;
+    const void* residual;          /* [M, N] of sum_dtype, may be NULL */
+    int64_t ld_residual;
+    const uint16_t* weight;        /* bf16 [N], may be NULL: ones */
+    const uint16_t* bias;          /* bf16 [N], may be NULL: zeros */
+    void* y;                       /* [M, N] of y_dtype */
+    int64_t ld_y;
+    void* sum;                     /* [M, N] of sum_dtype: s */
+    int64_t ld_sum;
+    float* stats;                  /* [M, 2]: mean and rstd of each row, may be NULL */
+    int32_t x_dtype;               /* ZERO_BF16 or ZERO_F32, each of the three */
+    int32_t sum_dtype;
+    int32_t y_dtype;
+    int32_t kind;                  /* zero_norm_kind */
+    double eps;
+} zero_norm_args;
+
+/*
+ * Errors of both calls: ZERO_E_INVAL (NULL args or matrix, an unknown kind or type, eps
+ * negative or not finite, a residual without sum or a sum without residual, overlap),
+ * ZERO_E_ALIGN (a pointer not aligned to its element, a workspace not to 16 bytes),
+ * ZERO_E_RANGE (M outside [0, 2^31 - 1], N outside [0, 2^24], an ld below its columns or
+ * above 2^40, a workspace below zero_norm_workspace_bytes), ZERO_E_HIP.
+ */
+int zero_norm_forward(const zero_norm_args* args, void* stream);
+
+/*
+ * The gradient by the rows, with what the residual stream's own gradient adds, and the
+ * gradients by weight and bias, reduced over the rows in an order that depends on the
+ * sizes alone. stats are the forward pass's. dx may be exactly dy, x or residual_grad.
+ * dweight and dbias may each be NULL; without both no workspace is needed. With M = 0
+ * they become 0, or stay.
+ */
+typedef struct {
+    int64_t M, N;
+    const void* dy;                /* [M, N] of dy_dtype */
+    int64_t ld_dy;
+    const void* x;                 /* [M, N] of x_dtype: s of the forward pass */
+    int64_t ld_x;
+    const uint16_t* weight;        /* bf16 [N], may be NULL: ones */
+    const float* stats;            /* [M, 2] */
+    const void* residual_grad;     /* [M, N] of dx_dtype, may be NULL */
+    int64_t ld_residual_grad;
+    void* dx;                      /* [M, N] of dx_dtype */
+    int64_t ld_dx;
+    void* dweight;                 /* [N] of grad_dtype, may be NULL */
+    void* dbias;                   /* [N] of grad_dtype, may be NULL */
+    int32_t dy_dtype;              /* ZERO_BF16 or ZERO_F32, each of the four */
+    int32_t x_dtype;
+    int32_t dx_dtype;
+    int32_t grad_dtype;
+    int32_t kind;                  /* zero_norm_kind */
+    int32_t accumulate;
+    void* workspace_dev;
+    size_t ws_bytes;
+} zero_norm_grad_args;
+
+/* Bytes of zero_norm_grad's workspace; 0 for sizes out of range. */
+size_t zero_norm_workspace_bytes(int64_t M, int64_t N);
+
+int zero_norm_grad(const zero_norm_grad_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

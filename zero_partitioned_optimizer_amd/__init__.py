@@ -7,8 +7,10 @@ the gathered parameter buffer.
 The compute lives in ``libzero.so`` (hand-written HIP for gfx950 behind a C ABI,
 ``include/zero.h``); this package is its ctypes binding (same function names)
 plus ``ShardStep``, which owns buffers and applies the commit rule. ``layer``
-holds the operators of a linear layer between the fetch of its tensors and the
-step: its products, its gradients into the flat gradient buffer, and dropout.
+holds the operators of a layer between the fetch of its tensors and the step: a
+linear layer's products, its gradients into the flat gradient buffer, dropout, and
+norms with their gradients; ``muon`` the step of the tensors that are matrices by an
+orthogonalised momentum.
 There is no CPU fallback: without the built library every call raises.
 """
 from ._binding import (  # noqa: F401
@@ -29,7 +31,12 @@ from ._binding import (  # noqa: F401
 from .shard_step import DeviceShardStep, OffloadShardStep, ShardStep  # noqa: F401
 from .layer import (  # noqa: F401
     ZERO_ACT_GELU, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, ZERO_LINEAR_FORWARD, ZERO_LINEAR_GRAD_INPUT,
-    ZERO_LINEAR_GRAD_WEIGHT, ZERO_W_IN_OUT, ZERO_W_OUT_IN, FlatLinear, zero_dropout, zero_dropout_add,
+    ZERO_LINEAR_GRAD_WEIGHT, ZERO_NORM_LAYER, ZERO_NORM_RMS, ZERO_W_IN_OUT, ZERO_W_OUT_IN, FlatLinear, FlatNorm,
+    zero_dropout, zero_dropout_add,
     zero_dropout_args, zero_dropout_grad, zero_linear_args, zero_linear_forward, zero_linear_grad_input,
     zero_linear_grad_input_args, zero_linear_grad_weight, zero_linear_grad_weight_args,
-    zero_linear_workspace_bytes)
+    zero_linear_workspace_bytes, zero_norm_args, zero_norm_forward, zero_norm_grad, zero_norm_grad_args,
+    zero_norm_workspace_bytes)
+from .muon import (  # noqa: F401
+    ZERO_MUON_COEFFICIENTS, zero_muon_momentum, zero_muon_momentum_args, zero_muon_update, zero_muon_update_args,
+    zero_orthogonalize, zero_orthogonalize_args, zero_orthogonalize_workspace_bytes)

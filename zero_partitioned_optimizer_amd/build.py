@@ -11,7 +11,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libzero.so")
 SOURCES = ["abi.cpp", "layout.cpp", "step_kernels.hip", "gather_kernels.hip", "layer_abi.cpp",
-           "linear_kernels.hip", "dropout_kernels.hip"]
+           "linear_kernels.hip", "dropout_kernels.hip", "norm_kernels.hip", "muon_abi.cpp",
+           "muon_kernels.hip", "orth_kernels.hip"]
 # host-only C++ (no device pass), compiled to an object and linked in
 HOST_SOURCES = ["offload.cpp"]
 HOST_FLAGS = ["-x", "c++", "-O3", "-std=c++17", "-fPIC", "-ffp-contract=off", "-Wall", "-c"]

@@ -1,106 +1,30 @@
 // layer_abi.cpp -- the C entry points of the layer operators (linear products and
-// their gradients, dropout): argument validation and the descriptors of their
-// kernels, which live in linear_kernels.hip and dropout_kernels.hip.
+// their gradients, dropout, norms): argument validation and the descriptors of their
+// kernels, which live in linear_kernels.hip, dropout_kernels.hip and norm_kernels.hip.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include "abi_checks.h"
 #include "layer_internal.h"
 #include "zero_internal.h"
 #include "zero_layer.h"
 
 namespace {
 
-using zl::set_error;
+using namespace zl;
 
 static_assert(sizeof(zero_dropout) == 32 && sizeof(zero_linear_args) == 176 &&
                   sizeof(zero_linear_grad_input_args) == 152 && sizeof(zero_linear_grad_weight_args) == 112 &&
-                  sizeof(zero_dropout_args) == 128,
+                  sizeof(zero_dropout_args) == 128 && sizeof(zero_norm_args) == 128 &&
+                  sizeof(zero_norm_grad_args) == 152,
               "the argument blocks of the ABI");
-
-constexpr int64_t kMaxDim = INT32_MAX;
-constexpr int64_t kMaxLd = int64_t(1) << 40;
-
-// One matrix argument. `written` outputs may not overlap any other matrix, unless
-// both are elementwise (`elem` > 0) and exactly the same.
-struct Mat {
-    const char* name;
-    const void* p;
-    int64_t rows, cols, ld;
-    int64_t esize;
-    bool written;
-    bool elementwise;
-    bool optional;
-};
-
-bool empty(const Mat& m) { return !m.p || m.rows == 0 || m.cols == 0; }
-
-// Whether any element belongs to both: their address ranges meet, and, where both
-// have the same row length, so do their columns within it.
-bool meet(const Mat& a, const Mat& b) {
-    if (empty(a) || empty(b)) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    const uintptr_t la = (uintptr_t)(a.ld * a.esize), lb = (uintptr_t)(b.ld * b.esize);
-    const uintptr_t wa = (uintptr_t)(a.cols * a.esize), wb = (uintptr_t)(b.cols * b.esize);
-    const uintptr_t a1 = a0 + la * (uintptr_t)(a.rows - 1) + wa, b1 = b0 + lb * (uintptr_t)(b.rows - 1) + wb;
-    if (a1 <= b0 || b1 <= a0) return false;
-    if (la != lb || a.rows == 1 || b.rows == 1) return true;
-    const uintptr_t shift = b0 >= a0 ? (b0 - a0) % la : (la - (a0 - b0) % la) % la;
-    return shift < wa || shift + wb > la;
-}
-
-int check_mats(const char* fn, const Mat* m, int n) {
-    for (int i = 0; i < n; ++i) {
-        if (m[i].optional && !m[i].p) continue;
-        if (m[i].rows == 0 || m[i].cols == 0) continue;
-        if (!m[i].p) {
-            set_error("%s: %s is NULL", fn, m[i].name);
-            return ZERO_E_INVAL;
-        }
-        if (reinterpret_cast<uintptr_t>(m[i].p) % (uintptr_t)m[i].esize != 0) {
-            set_error("%s: %s=%p is not aligned to its %d-byte elements", fn, m[i].name, m[i].p,
-                      (int)m[i].esize);
-            return ZERO_E_ALIGN;
-        }
-        if (m[i].ld < m[i].cols || m[i].ld > kMaxLd) {
-            set_error("%s: ld of %s is %lld, outside [%lld, 2^40]", fn, m[i].name, (long long)m[i].ld,
-                      (long long)m[i].cols);
-            return ZERO_E_RANGE;
-        }
-    }
-    for (int i = 0; i < n; ++i)
-        for (int k = i + 1; k < n; ++k) {
-            if (!m[i].written && !m[k].written) continue;
-            if (!meet(m[i], m[k])) continue;
-            const bool same = m[i].elementwise && m[k].elementwise && !(m[i].written && m[k].written) &&
-                              m[i].p == m[k].p && m[i].ld == m[k].ld && m[i].esize == m[k].esize;
-            if (same) continue;
-            set_error("%s: %s and %s overlap", fn, m[i].name, m[k].name);
-            return ZERO_E_INVAL;
-        }
-    return ZERO_OK;
-}
-
-int check_dims(const char* fn, int64_t M, int64_t K, int64_t N) {
-    if (M < 0 || K < 0 || N < 0 || M > kMaxDim || K > kMaxDim || N > kMaxDim) {
-        set_error("%s: sizes M=%lld K=%lld N=%lld outside [0, 2^31 - 1]", fn, (long long)M, (long long)K,
-                  (long long)N);
-        return ZERO_E_RANGE;
-    }
-    return ZERO_OK;
-}
 
 int check_output(const char* fn, int64_t rows, int64_t cols) {
     if (zk::product_fits(rows, cols)) return ZERO_OK;
     set_error("%s: an output of %lld x %lld is more than 2^23 tiles of 128 x 128 or 2^29 a side", fn,
               (long long)rows, (long long)cols);
     return ZERO_E_RANGE;
-}
-
-int check_type(const char* fn, const char* name, int32_t ty) {
-    if (ty == ZERO_F32 || ty == ZERO_BF16) return ZERO_OK;
-    set_error("%s: %s=%d is neither ZERO_F32 nor ZERO_BF16", fn, name, (int)ty);
-    return ZERO_E_INVAL;
 }
 
 int check_act(const char* fn, int32_t act) {
@@ -134,27 +58,19 @@ int make_drop(const char* fn, const zero_dropout& in, zk::Drop* out) {
     return ZERO_OK;
 }
 
-int check_ws(const char* fn, const void* ws, size_t have, size_t need) {
-    if (need == 0) return ZERO_OK;
-    if (!ws) {
-        set_error("%s: workspace_dev is NULL, %zu bytes are needed", fn, need);
-        return ZERO_E_INVAL;
-    }
-    if (reinterpret_cast<uintptr_t>(ws) % 16 != 0) {
-        set_error("%s: workspace_dev=%p is not 16-byte aligned", fn, ws);
-        return ZERO_E_ALIGN;
-    }
-    if (have < need) {
-        set_error("%s: ws_bytes=%zu, %zu are needed", fn, have, need);
+// Norms of rows up to this length: what joins the columns' sums fits one launch.
+constexpr int64_t kMaxNorm = int64_t(1) << 24;
+
+int check_norm(const char* fn, int64_t M, int64_t N, int32_t kind) {
+    int rc;
+    if ((rc = check_dims(fn, M, 0, N))) return rc;
+    if (N > kMaxNorm) {
+        set_error("%s: rows of N=%lld, above 2^24", fn, (long long)N);
         return ZERO_E_RANGE;
     }
-    return ZERO_OK;
-}
-
-int64_t size_of(int32_t ty) { return ty == ZERO_F32 ? 4 : 2; }
-
-Mat ws_mat(void* ws, size_t need) {
-    return Mat{"workspace_dev", need ? ws : nullptr, 1, (int64_t)need, (int64_t)need, 1, true, false, true};
+    if (kind == ZERO_NORM_LAYER || kind == ZERO_NORM_RMS) return ZERO_OK;
+    set_error("%s: unknown kind %d", fn, (int)kind);
+    return ZERO_E_INVAL;
 }
 
 // Bytes of the weight gradient's product and, behind it, of the bias gradient.
@@ -374,6 +290,112 @@ int zero_dropout_add(const zero_dropout_args* args, void* stream) {
 
 int zero_dropout_grad(const zero_dropout_args* args, void* stream) {
     return dropout("zero_dropout_grad", args, true, stream);
+}
+
+int zero_norm_forward(const zero_norm_args* args, void* stream) {
+    static const char* fn = "zero_norm_forward";
+    if (!args) {
+        set_error("%s: args is NULL", fn);
+        return ZERO_E_INVAL;
+    }
+    const zero_norm_args& a = *args;
+    int rc;
+    if ((rc = check_norm(fn, a.M, a.N, a.kind)) || (rc = check_type(fn, "x_dtype", a.x_dtype)) ||
+        (rc = check_type(fn, "sum_dtype", a.sum_dtype)) || (rc = check_type(fn, "y_dtype", a.y_dtype)))
+        return rc;
+    if (!(a.eps >= 0.0 && a.eps <= 1e30)) {
+        set_error("%s: eps=%g outside [0, 1e30]", fn, a.eps);
+        return ZERO_E_INVAL;
+    }
+    if (a.M == 0 || a.N == 0) return ZERO_OK;
+    if (!a.residual != !a.sum) {
+        set_error("%s: %s", fn, a.sum ? "a sum without a residual" : "a residual without a sum to store");
+        return ZERO_E_INVAL;
+    }
+    const int64_t xb = size_of(a.x_dtype), sb = size_of(a.sum_dtype), yb = size_of(a.y_dtype);
+    const Mat m[] = {{"x", a.x, a.M, a.N, a.ld_x, xb, false, true, false},
+                     {"residual", a.residual, a.M, a.N, a.ld_residual, sb, false, true, true},
+                     {"weight", a.weight, 1, a.N, a.N, 2, false, false, true},
+                     {"bias", a.bias, 1, a.N, a.N, 2, false, false, true},
+                     {"y", a.y, a.M, a.N, a.ld_y, yb, true, true, false},
+                     {"sum", a.sum, a.M, a.N, a.ld_sum, sb, true, true, true},
+                     {"stats", a.stats, a.M, 2, 2, 4, true, false, true}};
+    if ((rc = check_mats(fn, m, 7))) return rc;
+    zk::NormDesc d{};
+    d.M = a.M;
+    d.N = a.N;
+    d.x = a.x;
+    d.res = a.residual;
+    d.sum = a.sum;
+    d.y = a.y;
+    d.ld_x = a.ld_x;
+    d.ld_res = a.ld_residual;
+    d.ld_sum = a.ld_sum;
+    d.ld_y = a.ld_y;
+    d.x_f32 = a.x_dtype == ZERO_F32;
+    d.sum_f32 = a.sum_dtype == ZERO_F32;
+    d.y_f32 = a.y_dtype == ZERO_F32;
+    d.rms = a.kind == ZERO_NORM_RMS;
+    d.eps = (float)a.eps;
+    d.w = a.weight;
+    d.b = a.bias;
+    d.stats = a.stats;
+    return zl::hip_error(zk::launch_norm(d, static_cast<hipStream_t>(stream)), fn);
+}
+
+size_t zero_norm_workspace_bytes(int64_t M, int64_t N) {
+    return M < 0 || N < 1 || M > kMaxDim || N > kMaxNorm ? 0 : zk::norm_ws_bytes(M, N);
+}
+
+int zero_norm_grad(const zero_norm_grad_args* args, void* stream) {
+    static const char* fn = "zero_norm_grad";
+    if (!args) {
+        set_error("%s: args is NULL", fn);
+        return ZERO_E_INVAL;
+    }
+    const zero_norm_grad_args& a = *args;
+    int rc;
+    if ((rc = check_norm(fn, a.M, a.N, a.kind)) || (rc = check_type(fn, "dy_dtype", a.dy_dtype)) ||
+        (rc = check_type(fn, "x_dtype", a.x_dtype)) || (rc = check_type(fn, "dx_dtype", a.dx_dtype)) ||
+        (rc = check_type(fn, "grad_dtype", a.grad_dtype)))
+        return rc;
+    const bool sums = a.dweight || a.dbias;
+    if (a.N == 0 || (a.M == 0 && !sums)) return ZERO_OK;
+    const int64_t db = size_of(a.dy_dtype), xb = size_of(a.x_dtype), ob = size_of(a.dx_dtype), gb = size_of(a.grad_dtype);
+    const size_t need = sums ? zk::norm_ws_bytes(a.M, a.N) : 0;
+    const Mat m[] = {{"dy", a.dy, a.M, a.N, a.ld_dy, db, false, true, false},
+                     {"x", a.x, a.M, a.N, a.ld_x, xb, false, true, false},
+                     {"weight", a.weight, 1, a.N, a.N, 2, false, false, true},
+                     {"stats", a.stats, a.M, 2, 2, 4, false, false, false},
+                     {"residual_grad", a.residual_grad, a.M, a.N, a.ld_residual_grad, ob, false, true, true},
+                     {"dx", a.dx, a.M, a.N, a.ld_dx, ob, true, true, false},
+                     {"dweight", a.dweight, 1, a.N, a.N, gb, true, false, true},
+                     {"dbias", a.dbias, 1, a.N, a.N, gb, true, false, true},
+                     ws_mat(a.workspace_dev, need)};
+    if ((rc = check_ws(fn, a.workspace_dev, a.ws_bytes, need)) || (rc = check_mats(fn, m, 9))) return rc;
+    zk::NormGradDesc d{};
+    d.M = a.M;
+    d.N = a.N;
+    d.dy = a.dy;
+    d.x = a.x;
+    d.res = a.residual_grad;
+    d.dx = a.dx;
+    d.ld_dy = a.ld_dy;
+    d.ld_x = a.ld_x;
+    d.ld_res = a.ld_residual_grad;
+    d.ld_dx = a.ld_dx;
+    d.dy_f32 = a.dy_dtype == ZERO_F32;
+    d.x_f32 = a.x_dtype == ZERO_F32;
+    d.dx_f32 = a.dx_dtype == ZERO_F32;
+    d.rms = a.kind == ZERO_NORM_RMS;
+    d.w = a.weight;
+    d.stats = a.stats;
+    d.dw = a.dweight;
+    d.db = a.dbias;
+    d.grad_f32 = a.grad_dtype == ZERO_F32;
+    d.accumulate = a.accumulate != 0;
+    d.ws = static_cast<float*>(a.workspace_dev);
+    return zl::hip_error(zk::launch_norm_grad(d, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

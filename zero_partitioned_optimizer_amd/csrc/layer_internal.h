@@ -1,6 +1,6 @@
 // layer_internal.h -- internal interface between the C entry points of the layer
 // operators (layer_abi.cpp) and their gfx950 kernels (linear_kernels.hip,
-// dropout_kernels.hip). Not installed, not part of the ABI.
+// dropout_kernels.hip, norm_kernels.hip). Not installed, not part of the ABI.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -82,5 +82,39 @@ struct DropoutDesc {
     Drop drop;
 };
 hipError_t launch_dropout(const DropoutDesc& d, bool grad, hipStream_t st);
+
+// A norm of each row of [M, N], and its gradient. `_f32` flags: f32 in place of bf16.
+struct NormDesc {
+    int64_t M, N;
+    const void* x;
+    const void* res;                // of sum's type, or nullptr (then sum is too)
+    void* sum;
+    void* y;
+    int64_t ld_x, ld_res, ld_sum, ld_y;
+    bool x_f32, sum_f32, y_f32, rms;
+    float eps;
+    const uint16_t* w;              // or nullptr: ones
+    const uint16_t* b;              // or nullptr: zeros
+    float* stats;                   // [M, 2], or nullptr
+};
+hipError_t launch_norm(const NormDesc& d, hipStream_t st);
+
+struct NormGradDesc {
+    int64_t M, N;
+    const void* dy;
+    const void* x;
+    const void* res;                // of dx's type, or nullptr
+    void* dx;
+    int64_t ld_dy, ld_x, ld_res, ld_dx;
+    bool dy_f32, x_f32, dx_f32, rms;
+    const uint16_t* w;              // or nullptr: ones
+    const float* stats;
+    void* dw;                       // or nullptr, both
+    void* db;
+    bool grad_f32, accumulate;
+    float* ws;                      // norm_ws_bytes, where dw or db is wanted
+};
+size_t norm_ws_bytes(int64_t M, int64_t N);
+hipError_t launch_norm_grad(const NormGradDesc& d, hipStream_t st);
 
 }  // namespace zk

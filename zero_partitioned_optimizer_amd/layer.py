@@ -1,15 +1,16 @@
-"""The layer operators of libzero: a linear layer's products and dropout.
+"""The layer operators of libzero: a linear layer's products, dropout and norms.
 
 Between the fetch of a layer's tensors (``zero_gather_tensors``) and the optimizer
 step: the product with the fetched weights and its epilogue, its gradient by the
 layer's input, its gradient by the weights into the flat gradient buffer whose
-slices are the step's replicas, and dropout with a mask that is recomputed and
-never stored. The functions keep the C names of ``include/zero_layer.h`` and take torch
+slices are the step's replicas, dropout with a mask that is recomputed and
+never stored, and the norm of a block's rows with its gradient. The functions keep the C names of ``include/zero_layer.h`` and take torch
 tensors on the current device: 2-D matrices whose rows may be longer than their
 columns (``stride(0) >= size(1)``, ``stride(1) == 1``). Outputs that are not given
 are allocated, and a workspace that is not given is allocated for the call, both on
 the call's stream.
-``FlatLinear`` puts them together for one linear layer of a flat parameter buffer.
+``FlatLinear`` puts them together for one linear layer of a flat parameter buffer,
+``FlatNorm`` for one norm.
 """
 from __future__ import annotations
 
@@ -26,6 +27,7 @@ from ._binding import f64, i32, i64, sz, vp
 ZERO_W_OUT_IN, ZERO_W_IN_OUT = 0, 1
 ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_GELU, ZERO_ACT_SILU = 0, 1, 2, 3
 ZERO_LINEAR_FORWARD, ZERO_LINEAR_GRAD_INPUT, ZERO_LINEAR_GRAD_WEIGHT = 0, 1, 2
+ZERO_NORM_LAYER, ZERO_NORM_RMS = 0, 1
 u64 = ctypes.c_uint64
 
 _TYPES = {torch.bfloat16: B.ZERO_BF16, torch.float32: B.ZERO_F32}
@@ -78,6 +80,21 @@ class zero_dropout_args(ctypes.Structure):
                 ("dropout", zero_dropout)]
 
 
+class zero_norm_args(ctypes.Structure):
+    _fields_ = [("M", i64), ("N", i64), ("x", vp), ("ld_x", i64), ("residual", vp), ("ld_residual", i64),
+                ("weight", vp), ("bias", vp), ("y", vp), ("ld_y", i64), ("sum", vp), ("ld_sum", i64),
+                ("stats", vp), ("x_dtype", i32), ("sum_dtype", i32), ("y_dtype", i32), ("kind", i32),
+                ("eps", f64)]
+
+
+class zero_norm_grad_args(ctypes.Structure):
+    _fields_ = [("M", i64), ("N", i64), ("dy", vp), ("ld_dy", i64), ("x", vp), ("ld_x", i64), ("weight", vp),
+                ("stats", vp), ("residual_grad", vp), ("ld_residual_grad", i64), ("dx", vp), ("ld_dx", i64),
+                ("dweight", vp), ("dbias", vp), ("dy_dtype", i32), ("x_dtype", i32), ("dx_dtype", i32),
+                ("grad_dtype", i32), ("kind", i32), ("accumulate", i32), ("workspace_dev", vp),
+                ("ws_bytes", sz)]
+
+
 assert ctypes.sizeof(zero_dropout) == 32
 
 # The argument blocks above as struct formats: the calls below fill theirs in one
@@ -87,10 +104,14 @@ _FORWARD = struct.Struct("@qqqQqQqiiQQqQqiiQq" + _DROP + "QQ")
 _GRAD_INPUT = struct.Struct("@qqqQqQqiiQqQqii" + _DROP + "QQ")
 _GRAD_WEIGHT = struct.Struct("@qqqQqQqQqQiiiiQQ")
 _DROPOUT = struct.Struct("@qqQqQqQqQqiiii" + _DROP)
+_NORM = struct.Struct("@qqQqQqQQQqQqQiiiid")
+_NORM_GRAD = struct.Struct("@qqQqQqQQQqQqQQiiiiiiQQ")
 assert _FORWARD.size == ctypes.sizeof(zero_linear_args)
 assert _GRAD_INPUT.size == ctypes.sizeof(zero_linear_grad_input_args)
 assert _GRAD_WEIGHT.size == ctypes.sizeof(zero_linear_grad_weight_args)
 assert _DROPOUT.size == ctypes.sizeof(zero_dropout_args)
+assert _NORM.size == ctypes.sizeof(zero_norm_args)
+assert _NORM_GRAD.size == ctypes.sizeof(zero_norm_grad_args)
 
 _NO_DROP = (0.0, 0, 0, 0)
 _BF16, _F32 = torch.bfloat16, torch.float32
@@ -107,13 +128,17 @@ def _lib() -> ctypes.CDLL:
                            ("zero_linear_grad_input", zero_linear_grad_input_args),
                            ("zero_linear_grad_weight", zero_linear_grad_weight_args),
                            ("zero_dropout_add", zero_dropout_args),
-                           ("zero_dropout_grad", zero_dropout_args)):
+                           ("zero_dropout_grad", zero_dropout_args),
+                           ("zero_norm_forward", zero_norm_args),
+                           ("zero_norm_grad", zero_norm_grad_args)):
             getattr(L, name).argtypes = [P(args), vp]
             getattr(L, name).restype = ctypes.c_int
             # the same entry point, for an argument block that is packed already
             _call[name] = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_char_p, vp)((name, L))
         L.zero_linear_workspace_bytes.argtypes = [i32, i32, i64, i64, i64]
         L.zero_linear_workspace_bytes.restype = sz
+        L.zero_norm_workspace_bytes.argtypes = [i64, i64]
+        L.zero_norm_workspace_bytes.restype = sz
         _declared = L
     return _declared
 
@@ -232,14 +257,19 @@ def _cuda(device: int) -> torch.device:
 
 
 def _workspace(fn: str, kind: int, w_layout: int, M: int, K: int, N: int, given, device: int, stream):
-    """(address, bytes, tensor) of a call's workspace."""
+    """(address, bytes, tensor) of a product's workspace."""
+    return _scratch(fn, lambda: _workspace_need(kind, w_layout, M, K, N), given, device, stream)
+
+
+def _scratch(fn: str, bytes_needed, given, device: int, stream):
+    """(address, bytes, tensor) of a call's workspace: the given one, or a new one."""
     if given is not None:
         if given.get_device() != device:
             _bad(fn, f"workspace is on {given.device}, not on the current device")
         if not given.is_contiguous():
             _bad(fn, "workspace is not contiguous")
         return given.data_ptr(), given.numel() * given.element_size(), given
-    need = _workspace_need(kind, w_layout, M, K, N)
+    need = bytes_needed()
     if need == 0:
         return 0, 0, None
     ws = _new(need, torch.uint8, device, stream)
@@ -374,6 +404,107 @@ def zero_dropout_grad(dy, dropout: Optional[zero_dropout], *, act: int = ZERO_AC
     return dz
 
 
+@functools.lru_cache(maxsize=4096)
+def _norm_need(M: int, N: int) -> int:
+    return int(_lib().zero_norm_workspace_bytes(M, N))
+
+
+def zero_norm_workspace_bytes(M: int, N: int) -> int:
+    return _norm_need(int(M), int(N))
+
+
+def zero_norm_forward(x, weight=None, bias=None, *, kind: int = ZERO_NORM_LAYER, eps: float = 1e-5, residual=None,
+                      sum=None, y=None, stats=None, dtype=None, stream=None):
+    """The norm of each row of x, or of s = residual + x. Returns y; with a residual or
+    with stats a tuple (y, s, stats) of those that there are. ``sum``: the tensor that
+    receives s (of the residual's type; new if None). ``stats``: a float32 [M, 2] tensor
+    that receives each row's mean and 1 / standard deviation, which the gradient takes, or
+    True for a new one. ``dtype`` is that of a new y (x's by default)."""
+    fn = "zero_norm_forward"
+    dev = _on_device(fn, "x", x)
+    tx = _type(fn, "x", x.dtype)
+    px, ldx = _mat(fn, "x", x, x.dtype, dev)
+    M, N = x.shape
+    if y is None:
+        y = _new_like(x, dtype or x.dtype, dev, stream)
+    elif dtype is not None and y.dtype is not dtype:
+        _bad(fn, f"y is {y.dtype}, not {dtype}")
+    ty = _type(fn, "y", y.dtype)
+    py, ldy = _mat(fn, "y", y, y.dtype, dev, M, N)
+    pr = ldr = ps = lds = pt = pw = pb = ts = 0
+    if residual is not None:
+        ts = _type(fn, "residual", residual.dtype)
+        pr, ldr = _mat(fn, "residual", residual, residual.dtype, dev, M, N)
+        if sum is None:
+            sum = _new_like(residual, residual.dtype, dev, stream)
+        ps, lds = _mat(fn, "sum", sum, residual.dtype, dev, M, N)
+    elif sum is not None:
+        _bad(fn, "a sum without a residual")
+    if weight is not None:
+        pw = _vec(fn, "weight", weight, _BF16, dev, N)
+    if bias is not None:
+        pb = _vec(fn, "bias", bias, _BF16, dev, N)
+    if stats is False:
+        stats = None
+    if stats is not None:
+        if stats is True:
+            stats = _new((M, 2), _F32, dev, stream)
+        pt = _stats(fn, stats, dev, M)
+    _enqueue(fn, _NORM.pack(M, N, px, ldx, pr, ldr, pw, pb, py, ldy, ps, lds, pt, tx, ts, ty, kind, eps), stream)
+    if residual is None:
+        return y if stats is None else (y, stats)
+    return (y, sum) if stats is None else (y, sum, stats)
+
+
+def _stats(fn: str, t: torch.Tensor, device: int, M: int) -> int:
+    if M == 0 and t.numel() == 0:       # whatever its strides say
+        return 0
+    p, ld = _mat(fn, "stats", t, _F32, device, M, 2)
+    if ld != 2:
+        _bad(fn, f"stats has row stride {ld}, not 2")
+    return p
+
+
+def zero_norm_grad(dy, x, weight=None, stats=None, *, kind: int = ZERO_NORM_LAYER, residual_grad=None, dx=None,
+                   dtype=None, dweight=None, dbias=None, accumulate: bool = False, workspace=None, stream=None):
+    """dx = residual_grad + the norm's gradient by its rows, from dy, the rows x that were
+    normed (s, where there was a residual) and their stats; and, where they are given,
+    dweight and dbias [+]= the gradients by weight and bias (bf16 or f32, views of a flat
+    gradient buffer). ``dtype`` is that of a new dx (the residual_grad's, or dy's, by default)."""
+    fn = "zero_norm_grad"
+    dev = _on_device(fn, "dy", dy)
+    td = _type(fn, "dy", dy.dtype)
+    pd, ldd = _mat(fn, "dy", dy, dy.dtype, dev)
+    M, N = dy.shape
+    tx = _type(fn, "x", x.dtype)
+    px, ldx = _mat(fn, "x", x, x.dtype, dev, M, N)
+    if stats is None:
+        _bad(fn, "stats of the forward pass are missing")
+    pt = _stats(fn, stats, dev, M)
+    if dx is None:
+        dx = _new_like(dy, dtype or (residual_grad.dtype if residual_grad is not None else dy.dtype), dev, stream)
+    elif dtype is not None and dx.dtype is not dtype:
+        _bad(fn, f"dx is {dx.dtype}, not {dtype}")
+    to = _type(fn, "dx", dx.dtype)
+    po, ldo = _mat(fn, "dx", dx, dx.dtype, dev, M, N)
+    pr = ldr = pw = pgw = pgb = ws = nws = tg = 0
+    if residual_grad is not None:
+        pr, ldr = _mat(fn, "residual_grad", residual_grad, dx.dtype, dev, M, N)
+    if weight is not None:
+        pw = _vec(fn, "weight", weight, _BF16, dev, N)
+    if dweight is not None:
+        tg = _type(fn, "dweight", dweight.dtype)
+        pgw = _vec(fn, "dweight", dweight, dweight.dtype, dev, N)
+    if dbias is not None:
+        tg = _type(fn, "dbias", dbias.dtype)
+        pgb = _vec(fn, "dbias", dbias, dbias.dtype if dweight is None else dweight.dtype, dev, N)
+    if dweight is not None or dbias is not None:
+        ws, nws, keep = _scratch(fn, lambda: _norm_need(M, N), workspace, dev, stream)
+    _enqueue(fn, _NORM_GRAD.pack(M, N, pd, ldd, px, ldx, pw, pt, pr, ldr, po, ldo, pgw, pgb, td, tx, to, tg, kind,
+                                 1 if accumulate else 0, ws, nws), stream)
+    return dx
+
+
 class FlatLinear:
     """One linear layer of a model whose parameters and gradients lie in flat
     buffers: tensors ``weight`` and ``bias`` (indices, bias optional) of a layout,
@@ -453,3 +584,67 @@ class FlatLinear:
         act, preact, dropout = below if below is not None else (ZERO_ACT_NONE, None, None)
         return zero_linear_grad_input(dz, self.w, w_layout=self.w_layout, act=act, preact=preact,
                                       dropout=dropout, dtype=dtype, workspace=workspace, stream=stream)
+
+
+class FlatNorm:
+    """One norm of a model whose parameters and gradients lie in flat buffers: tensors
+    ``weight`` and ``bias`` (indices, bias optional) of a layout, ``width`` elements each.
+    ``fetch``, ``use`` and ``release`` as of ``FlatLinear``; ``backward`` writes or
+    accumulates the gradients of weight and bias in place at the tensors' offsets of a
+    flat gradient buffer."""
+
+    def __init__(self, offsets: Sequence[int], numels: Sequence[int], weight: int, bias: Optional[int], width: int, *,
+                 kind: int = ZERO_NORM_LAYER, eps: float = 1e-5):
+        for i in (weight, bias):
+            if i is not None and numels[i] != width:
+                _bad("FlatNorm", f"tensor {i} holds {numels[i]} elements, not {width}")
+        if kind not in (ZERO_NORM_LAYER, ZERO_NORM_RMS):
+            _bad("FlatNorm", f"unknown kind {kind}")
+        self.N, self.kind, self.eps = int(width), int(kind), float(eps)
+        self.w_off = int(offsets[weight])
+        self.b_off = None if bias is None else int(offsets[bias])
+        self.w = self.b = None
+
+    def _views(self, flat: torch.Tensor):
+        offs = [self.w_off] + ([] if self.b_off is None else [self.b_off])
+        if flat.dim() != 1 or flat.stride(0) != 1 or flat.numel() < max(offs) + self.N:
+            _bad("FlatNorm", f"a flat buffer of shape {tuple(flat.shape)} does not hold the norm's tensors")
+        got = [flat[o:o + self.N] for o in offs]
+        return got[0], got[1] if self.b_off is not None else None
+
+    def use(self, params: torch.Tensor) -> None:
+        """Take the norm's tensors from a flat bf16 parameter buffer (no copy)."""
+        self.w, self.b = self._views(params)
+
+    def fetch(self, shards, shard_S: int, stream=None) -> None:
+        """Copy the norm's tensors out of the rank shards (bf16 or its bit patterns). Passes
+        may run on the copies' stream, or on the current one once it waits for that."""
+        offs = [self.w_off] + ([] if self.b_off is None else [self.b_off])
+        got = B.zero_gather_tensors(shards, shard_S, offs, [self.N] * len(offs), stream=stream)
+        self.w = got[0].view(torch.bfloat16)
+        self.b = got[1].view(torch.bfloat16) if self.b_off is not None else None
+
+    def release(self) -> None:
+        """Drop the norm's tensors (after its pass, under stage 3)."""
+        self.w = self.b = None
+
+    def _here(self, fn: str):
+        if self.w is None:
+            _bad(fn, "the norm's tensors are not here: fetch or use first")
+
+    def forward(self, x, *, residual=None, sum=None, dtype=None, stream=None):
+        """(y, s, stats): the norm of s = residual + x (x itself without a residual), and what
+        ``backward`` takes."""
+        self._here("FlatNorm.forward")
+        got = zero_norm_forward(x, self.w, self.b, kind=self.kind, eps=self.eps, residual=residual, sum=sum,
+                                stats=True, dtype=dtype, stream=stream)
+        return got if residual is not None else (got[0], x, got[1])
+
+    def backward(self, dy, s, stats, grads: Optional[torch.Tensor], *, accumulate: bool = False, residual_grad=None,
+                 dx=None, dtype=None, workspace=None, stream=None):
+        """The gradient by s, the residual stream's own added; the weight's and the bias's go
+        into ``grads`` (skipped if None)."""
+        self._here("FlatNorm.backward")
+        dw, db = self._views(grads) if grads is not None else (None, None)
+        return zero_norm_grad(dy, s, self.w, stats, kind=self.kind, residual_grad=residual_grad, dx=dx, dtype=dtype,
+                              dweight=dw, dbias=db, accumulate=accumulate, workspace=workspace, stream=stream)
