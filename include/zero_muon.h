@@ -78,16 +78,17 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * of `steps` triples a, b, c, or NULL for (3.4445, -4.7750, 2.0315) in every step.
  *
  * o is bf16. The products run on the matrix cores with fp16 operands and fp32 sums; X is
- * carried with 22 bits and the diagonals of A and b A + c A A in fp32. With the default
+ * carried with 18 bits and the diagonals of A and b A + c A A in fp32. With the default
  * coefficients the result is about 1e-3 of its norm from the formula's (2e-3 was not
  * passed, 4e-3 where a side is below 32), plus o's own rounding, whatever the fall of the
- * singular values. X's elements must stay
- * below 64 and those of b A + c A A too, which they do for coefficients that keep the
- * singular values below 8; beyond, the result is not finite. A matrix of zeros gives
- * zeros. A matrix that holds an infinity or a NaN gives NaN in all its elements, and does
- * not reach the others. The sum of squares is fp64: no scale of x overflows it.
+ * singular values. X's elements must stay below 16 and those of A and b A + c A A off their
+ * diagonals below 64, as they do for coefficients that keep the singular values below 3;
+ * beyond, results are NaN. A matrix of zeros gives zeros. A matrix that holds an infinity
+ * or a NaN gives NaN in all its elements, and does not reach the others. The sum of squares
+ * is fp64: no scale of x overflows it.
  * Matrices are processed in groups whose intermediate results take 4 GiB at most, one
- * matrix at least; the result does not depend on the batch that a matrix is in.
+ * matrix at least. The same call gives the same bits; how sums are split, and so a
+ * result's last bits, depends on the sizes and on how many matrices there are.
  * Errors: ZERO_E_INVAL (NULL, an unknown type, steps outside [1, 64], eps not in
  * [1e-30, 1e30], scale or a coefficient not finite or beyond 1e4 in magnitude, overlap of the extents of x,
  * o and the workspace), ZERO_E_ALIGN (a pointer not aligned to its element, a workspace

@@ -32,9 +32,20 @@ def _half(v):
     return (v * np.float32(1024)).astype(np.float16).astype(np.float32) / np.float32(1024)
 
 
+def _split(X):
+    """X as hi, fp16 of 4096 X with ties away from zero, and X again with 8 more bits."""
+    v = X * np.float32(4096)
+    v = np.where(np.abs(v) < 2.0 ** -14, np.float32(0), v)
+    t = v.view(np.uint32) + np.uint32(1 << 12)
+    hi = (t & np.uint32(0xFFFFE000)).view(np.float32)
+    x = ((t & np.uint32(0xFFFFFFE0)) - np.uint32(1 << 12)).view(np.float32)
+    zero = v == 0
+    return [np.where(zero, np.float32(0), w) / np.float32(4096) for w in (hi, x)]
+
+
 def model(x, *, steps=5, coefficients=None, eps=1e-7, scale=1.0):
     """The same with the roundings that the kernels make before o's own: fp16 operands, fp32
-    sums and diagonals, X as hi + lo. In fp32; its sums are in another order."""
+    sums and diagonals, X with 18 bits. In fp32; its sums are in another order."""
     X = np.asarray(x, np.float64)
     tall = X.shape[0] > X.shape[1]
     X = (X / (np.sqrt((X * X).sum()) + eps)).astype(np.float32)
@@ -42,8 +53,7 @@ def model(x, *, steps=5, coefficients=None, eps=1e-7, scale=1.0):
         X = np.ascontiguousarray(X.T)
     for k, (a, b, c) in enumerate(triples(coefficients, steps)):
         a, b, c = np.float32(a), np.float32(b), np.float32(c)
-        hi = _half(X)
-        lo = _half((X - hi) * np.float32(2048)) / np.float32(2048)
+        hi, X = _split(X)
         A = hi @ hi.T
         d = np.diagonal(A).copy()
         np.fill_diagonal(A, 0)
@@ -52,7 +62,7 @@ def model(x, *, steps=5, coefficients=None, eps=1e-7, scale=1.0):
         e = b * d + c * (d * d + np.diagonal(FF))
         G = b * F + c * (FF + (d[:, None] + d[None, :]) * F)
         np.fill_diagonal(G, 0)
-        X = a * (hi + lo) + e[:, None] * (hi + lo if steps - 1 - k <= 2 else hi) + _half(G) @ hi
+        X = a * X + e[:, None] * (X if steps - 1 - k <= 2 else hi) + _half(G) @ hi
     X = np.float32(scale) * X
     return X.T if tall else X
 

@@ -111,16 +111,29 @@ def test_parameters(Z, kw):
         check(Z.zero_orthogonalize(x, **kw), x, **kw)
 
 
+def apart(a, b):
+    """The norm of a - b over that of b, matrix by matrix. Two results for the same matrix are
+    each within 2e-3 and o's rounding (2^-9) of the formula's."""
+    a, b = a.double(), b.double()
+    return float(((a - b).square().sum((-2, -1)) / b.square().sum((-2, -1))).sqrt().max())
+
+
+BOTH = 2 * (2e-3 + 2.0 ** -9)
+
+
 def test_a_matrix_alone_in_a_stack_and_transposed(Z):
-    """The result does not depend on the batch, the same call gives the same bits, and a
-    2-D tensor is a stack of one."""
+    """The same call gives the same bits; a stack and its matrices alone, whose sums may be
+    split in other ways, the same within twice the bound; a 2-D tensor is a stack of one."""
     rng = rng_of(4)
     x = torch.from_numpy(falling(rng, 7, 200, 330)).to(dev()).to(BF)
     o = Z.zero_orthogonalize(x)
     assert torch.equal(o, Z.zero_orthogonalize(x))
     for k in range(7):
-        assert torch.equal(Z.zero_orthogonalize(x[k]), o[k])
-    assert torch.equal(Z.zero_orthogonalize(x[::2]), o[::2])
+        one = Z.zero_orthogonalize(x[k])
+        check(one[None], x[k][None])
+        assert torch.equal(one, Z.zero_orthogonalize(x[k:k + 1])[0])
+        assert apart(one, o[k]) <= BOTH
+    check(Z.zero_orthogonalize(x[::2]), x[::2])
     t = Z.zero_orthogonalize(x.transpose(1, 2).contiguous())
     check(t.transpose(1, 2), x)
 
@@ -175,7 +188,7 @@ def test_large(Z, size):
 
 def test_groups(Z):
     """A stack whose intermediate results pass 4 GiB goes in groups."""
-    B, r, c = 150, 1024, 4096
+    B, r, c = 180, 1024, 4096
     need = Z.zero_orthogonalize_workspace_bytes(B, r, c)
     assert need <= 4 << 30 and need < B * Z.zero_orthogonalize_workspace_bytes(1, r, c)
     g = torch.Generator(device=dev()).manual_seed(11)
@@ -183,7 +196,7 @@ def test_groups(Z):
     o = Z.zero_orthogonalize(x)
     n = need // Z.zero_orthogonalize_workspace_bytes(1, r, c)
     for k in (0, n - 1, n, B - 1):
-        assert torch.equal(Z.zero_orthogonalize(x[k]), o[k]), k
+        assert apart(Z.zero_orthogonalize(x[k]), o[k]) <= BOTH, k
 
 
 def test_streams_and_graphs(Z):

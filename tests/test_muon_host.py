@@ -138,7 +138,7 @@ def test_workspace():
     need = Z.zero_orthogonalize_workspace_bytes
     assert need(0, 8, 8) == need(1, 0, 8) == need(-1, 8, 8) == need(1, 1 << 16, 1 << 16) == 0
     one = need(1, 768, 2304)
-    assert one >= 768 * 2304 * 6 + 768 * 768 * 4 and need(12, 768, 2304) == 12 * one
+    assert one >= 768 * 2304 * 5 + 768 * 768 * 4 and need(12, 768, 2304) == 12 * one
     assert need(1, 2304, 768) == one
     most = need(100000, 768, 2304)
     assert most <= 4 << 30 and most == need(200000, 768, 2304) and most % one == 0

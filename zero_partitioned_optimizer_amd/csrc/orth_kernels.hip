@@ -6,11 +6,12 @@
 // A step is three products on the matrix cores: the Gram product A, whose two triangles
 // are equal, the square's, likewise, and the update's. Their operands are fp16, their sums
 // fp32. What is rounded to 16 bits, and what is not:
-//   X        kept as two fp16 numbers, hi + lo / 2048, about 22 bits; hi is the operand. The
-//            update adds a X from both. A step multiplies directions that X does not hold
-//            by a, 485 times in five steps: rounding noise of X in both its missing rows
-//            and columns grows by that (X in fp16 alone leaves a rank-8 matrix 4% off, in
-//            bf16 33%), while the noise of an operand lies in rows or columns that X holds.
+//   X        kept as an fp16 number hi, X rounded, and lo, the next 8 bits of its fp32 mantissa:
+//            18 bits in 3 bytes; hi is the operand. The update adds a X from both.
+//            A step multiplies directions that X does not hold by a, 485 times in five
+//            steps: rounding noise of X in both its missing rows and columns grows by that (X
+//            in fp16 alone leaves a rank-8 matrix 4% off, in bf16 33%), while the noise of an
+//            operand lies in rows or columns that X holds.
 //   A        off its diagonal. The diagonal, near 1 once X is nearly orthogonal and then
 //            most of A, stays in fp32, in a vector.
 //   b A + c A A   likewise. Its diagonal multiplies hi and lo in the last three steps, hi alone
@@ -21,11 +22,13 @@
 // rank 1, rank 4 and falling spectra at 32 x 32 to 512 x 2048 (up to 1.6e-3 there, 2.5e-3
 // at 8 x 8); with the diagonals in fp16 1.0 to 2.4e-3; with lo in every step 0.4 to 1.0e-3 on
 // normal numbers but 4e-3 on rank 1 at 64 x 256, in none 1.1 to 1.6e-3 on normal numbers.
-// fp16 holds X, A and b A + c A A times 1024: a 4096 x 11008 X starts with elements of 1.5e-4,
-// and none of the three has elements above 10 with the default coefficients.
+// fp16 holds A and b A + c A A times 1024 and X times 4096, of which a 4096 x 11008 one starts
+// with elements of 1.5e-4; with the default coefficients no element of them passes 3.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
+
+#include <initializer_list>
 
 #include "layer_device.h"
 #include "muon_internal.h"
@@ -38,7 +41,7 @@ typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kBR = 64;                     // reduction elements per staged tile
 constexpr int kSide = 128;                  // all sides are padded to this, with zeros
-constexpr float kScale = 1024.0f, kLow = 2048.0f;
+constexpr float kScale = 1024.0f, kScaleX = 4096.0f;
 constexpr int kSquareParts = 256;           // partial sums of squares of a matrix, at most
 
 enum OrthOp { kGram, kSquare, kUpdate };
@@ -50,7 +53,8 @@ struct OrthArgs {
     int64_t lda, ldb, step_a, step_b;       // row lengths, and from one matrix to the next
     int64_t P, Q;                           // multiples of kSide
     int32_t turns;                          // reduction tiles of kBR
-    int32_t np, nq, tiles, all;             // output tiles: down, across, of a matrix, of all
+    int32_t np, nq, tiles;                  // output tiles: down, across, of a matrix
+    int32_t first, all;                     // the launch's first one, of all matrices', and how many
     const _Float16* in;                     // square: A, update: X hi; of C's shape
     int64_t ld_in, step_in;
     const float* diag_in;                   // square: of A, update: of b A + c A A
@@ -58,25 +62,29 @@ struct OrthArgs {
     int64_t ld_out, step_out;
     float* diag_out;
     int64_t step_diag;
-    _Float16* lo;                           // update: X lo, in place, laid out as `in`
+    uint8_t* lo;                             // update: X lo, in place, laid out as `in`
     float ca, cb, cc;
-    float low;                              // update: what of lo the diagonal meets, 1 / kLow or 0
+    bool low;                               // update: whether the diagonal meets lo too
     bool by_column;                         // update: the diagonal goes by column
     uint16_t* o;                            // the last update's output and its size
     int64_t ld_o, step_o, rows, cols;
     float scale;
+    float* part;                            // split tiles' partial sums
 };
 
 // ---------------------------------------------------------------------------
 // tiles in LDS
 // ---------------------------------------------------------------------------
 
-// A staged tile has 128 outer indices and kBR reduction elements in chunks of eight (16
-// bytes), permuted so that lanes that read together meet different banks: with the outer
-// index in rows chunk c of row o lies at c ^ (o & 7); with the reduction in rows (T), chunk
-// c of row r at c ^ perm(r), as a transposing read takes 4 rows x 32 bytes per 16 lanes,
-// two such groups 8 rows apart.
-__device__ __forceinline__ int perm_rows(int r) { return (r & 3) << 1 | (r >> 3 & 1) << 3; }
+// A staged tile has 64 or 128 outer indices and kBR reduction elements in chunks of eight
+// (16 bytes), permuted so that lanes that read together meet different banks: with the outer
+// index in rows chunk c of row o lies at c ^ (o & 7); with the reduction in rows (T), chunk c
+// of row r at c ^ perm(r), as a transposing read takes 4 rows x 32 bytes per 16 lanes, two
+// such groups 8 rows apart (of 64 columns, even and odd rows have different banks as it is).
+template <int COLS>
+__device__ __forceinline__ int perm_rows(int r) {
+    return COLS >= 128 ? (r & 3) << 1 | (r >> 3 & 1) << 3 : (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1;
+}
 
 typedef __attribute__((address_space(3))) const _Float16 lds_f16;
 typedef __attribute__((address_space(3))) const h8 lds_h8;
@@ -113,12 +121,13 @@ __device__ __forceinline__ void meet_waves() {
     asm volatile("s_barrier" : : : "memory");
 }
 
-// PARTS runs of 128 outer indices from memory to LDS, a thread's chunks at byte offsets
-// from `base` that every tile of the reduction shares. A run that lies outside the operand
-// reads its last one instead, which reaches no output.
-template <bool T, int THREADS, int PARTS>
+// PARTS runs of ROWS outer indices from memory to LDS, a thread's chunks at byte offsets
+// from `base` that every tile of the reduction shares; THREADS consecutive threads load a
+// run. A run that lies outside the operand reads its last one instead, which reaches no
+// output.
+template <int ROWS, bool T, int THREADS, int PARTS>
 struct Loader {
-    static constexpr int kLoads = kSide * kBR / 8 / THREADS;
+    static constexpr int kLoads = ROWS * kBR / 8 / THREADS;
     static_assert(kLoads % 2 == 0, "pairs of loads");
     uint32_t at[PARTS][kLoads];
     const char* base;
@@ -126,12 +135,12 @@ struct Loader {
     __device__ __forceinline__ void init(const _Float16* src, int64_t ld, int64_t o0, int64_t O) {
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
-            const int64_t run = o0 + kSide * h < O ? kSide * h : O - kSide - o0;
+            const int64_t run = o0 + ROWS * h < O ? ROWS * h : O - ROWS - o0;
 #pragma unroll
             for (int i = 0; i < kLoads; ++i) {
-                const int id = threadIdx.x + i * THREADS;
+                const int id = threadIdx.x % THREADS + i * THREADS;
                 if constexpr (T) {
-                    const int r = id / (kSide / 8), c = 8 * ((id % (kSide / 8)) ^ perm_rows(r));
+                    const int r = id / (ROWS / 8), c = 8 * ((id % (ROWS / 8)) ^ perm_rows<ROWS>(r));
                     at[h][i] = (uint32_t)((r * ld + run + c) * 2);
                 } else {
                     const int o = id / (kBR / 8), c = 8 * ((id % (kBR / 8)) ^ (o & 7));
@@ -142,8 +151,9 @@ struct Loader {
         base = reinterpret_cast<const char*>(src + (T ? o0 : o0 * ld));
         step = (T ? kBR * ld : kBR) * 2;
     }
-    // Run h of the tile at `from` to LDS byte address `tile`; `wave` is the same in all
-    // lanes. With `records` 0 the buffer's range check stops the loads (which still count).
+    // Run h of the tile at `from` to LDS byte address `tile`; `wave` (of those that load the
+    // run) is the same in all lanes. With `records` 0 the buffer's range check stops the
+    // loads (which still count).
     __device__ __forceinline__ void issue(int h, const char* from, uint32_t tile, int wave, int records) const {
         const uintptr_t b = reinterpret_cast<uintptr_t>(from);
         const v4i rsrc = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
@@ -155,16 +165,17 @@ struct Loader {
 };
 constexpr int kAllRecords = 0x7FFFFFFF;
 
-// The matrix instruction's operands: for block i, lane l holds outer index o0 + 16 i + (l & 15)
-// and reduction elements 32 s + 8 (l >> 4) .. + 7. o0 is a multiple of 32.
-template <bool T>
+// The matrix instruction's operands from a tile of ROWS outer indices: for block i, lane l
+// holds outer index o0 + 16 i + (l & 15) and reduction elements 32 s + 8 (l >> 4) .. + 7. o0 is a
+// multiple of what the wave's blocks cover.
+template <int ROWS, bool T>
 struct Fragments {
     uint32_t at;
     __device__ __forceinline__ explicit Fragments(int o0) {
         const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
         if constexpr (T) {
             const int r = 8 * g + (i >> 2), chunk = (o0 >> 3) + ((i & 3) >> 1);
-            at = 2 * (r * kSide + 8 * (chunk ^ perm_rows(r)) + 4 * (i & 1));
+            at = 2 * (r * ROWS + 8 * (chunk ^ perm_rows<ROWS>(r)) + 4 * (i & 1));
         } else {
             const int o = o0 + i;
             at = 2 * (o * kBR + 8 * (g ^ (o & 7)));
@@ -173,9 +184,9 @@ struct Fragments {
     __device__ __forceinline__ h8 get(uint32_t tile, int i, int s) const {
         if constexpr (T) {
             // rows 32 further on have the same permutation
-            const uint32_t p = tile + (at ^ (32u * i)) + 2 * 32 * kSide * s;
+            const uint32_t p = tile + (at ^ (32u * i)) + 2 * 32 * ROWS * s;
             const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 2 * 4 * kSide));
+            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 2 * 4 * ROWS));
             return __builtin_bit_cast(h8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
         } else {
             return *(lds_h8*)(tile + (at ^ (64u * s)) + 2 * 16 * kBR * i);
@@ -189,12 +200,12 @@ __device__ __forceinline__ int in_turn(int all) {
     const int id = blockIdx.x, xcd = id & 7, each = all >> 3, more = all & 7;
     return xcd * each + (xcd < more ? xcd : more) + (id >> 3);
 }
-// The matrix and the tile of a workgroup: of a symmetric product those on and below the
+// The matrix and the place of tile t of all: of a symmetric product those on and below the
 // diagonal, row by row, else down blocks of eight rows of tiles, column by column, so that
 // the tiles that run at a time share operand rows.
 template <bool SYM>
-__device__ __forceinline__ int place(const OrthArgs& g, int* tp, int* tq) {
-    const int t = in_turn(g.all), m = t / g.tiles, in = t - m * g.tiles;
+__device__ __forceinline__ int place(const OrthArgs& g, int t, int* tp, int* tq) {
+    const int m = t / g.tiles, in = t - m * g.tiles;
     int p, q;
     if constexpr (SYM) {
         p = (int)((__builtin_sqrtf(8.0f * (float)in + 1.0f) - 1.0f) * 0.5f);
@@ -224,110 +235,227 @@ __device__ __forceinline__ void put_h8(_Float16* p, const float v[8]) {
     *reinterpret_cast<h8*>(p) = t;
 }
 
-// Columns q .. q + 7 of row p of matrix m, from their sums v.
-template <int OP>
-__device__ __forceinline__ void epilogue8(const OrthArgs& g, int64_t m, int64_t p, int64_t q, float v[8]) {
-    constexpr float kOnce = 1.0f / kScale, kTwice = kOnce * kOnce;
-    if constexpr (OP == kGram) {
+// X (times kScaleX) as hi and lo: with half of hi's last place added to its bits, hi is what
+// fp16 holds of them (rounded to nearest, then; ties away from zero) and lo the next 8. Below
+// fp16's normal numbers, 1.5e-8 of X itself, it is 0; beyond its largest it is NaN.
+constexpr uint32_t kHalfPlace = 1u << 12;
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+__device__ __forceinline__ void split_x8(const float v[8], h8* hi, v2u* lo) {
+    uint32_t t[8], h[4];
+    float most = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            if (p == q + k) {
-                g.diag_out[m * g.step_diag + p] = v[k] * kTwice;
-                v[k] = 0.0f;
-            }
-            v[k] *= kOnce;
-        }
-        put_h8(g.out + m * g.step_out + p * g.ld_out + q, v);
-    } else if constexpr (OP == kSquare) {
-        // A = D + F, its diagonal and the rest: A A = F F + D F + F D + D D
-        const h8 f = *reinterpret_cast<const h8*>(g.in + m * g.step_in + p * g.ld_in + q);
-        const float* const d = g.diag_in + m * g.step_diag;
-        const float dp = d[p];
-        float dq[8];
-        load8_f(dq, d + q, 8);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float fk = (float)f[k], ff = v[k] * kOnce;
-            v[k] = fmaf(g.cc, fmaf(dp + dq[k], fk, ff), g.cb * fk);
-            if (p == q + k) {
-                g.diag_out[m * g.step_diag + p] = fmaf(g.cc, fmaf(dp, dp, ff * kOnce), g.cb * dp);
-                v[k] = 0.0f;
-            }
-        }
-        put_h8(g.out + m * g.step_out + p * g.ld_out + q, v);
-    } else {
-        const int64_t at = m * g.step_in + p * g.ld_in + q;
-        const h8 hi = *reinterpret_cast<const h8*>(g.in + at), lo = *reinterpret_cast<const h8*>(g.lo + at);
-        const float* const e = g.diag_in + m * g.step_diag;
-        float eq[8];
-        if (g.by_column) load8_f(eq, e + q, 8);
-        const float ep = e[g.by_column ? 0 : p];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float h = (float)hi[k], l = (float)lo[k];
-            v[k] = fmaf(g.ca, fmaf(l, 1.0f / kLow, h), fmaf(g.by_column ? eq[k] : ep, fmaf(l, g.low, h), v[k] * kOnce));
-        }
-        if (g.out) {
-            h8 h, l;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                h[k] = (_Float16)v[k];
-                l[k] = (_Float16)((v[k] - (float)h[k]) * kLow);
-            }
-            *reinterpret_cast<h8*>(g.out + at) = h;
-            *reinterpret_cast<h8*>(g.lo + at) = l;
-        } else if (p < g.rows && q < g.cols) {
-            const int n = g.cols - q < 8 ? (int)(g.cols - q) : 8;
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] *= g.scale * kOnce;
-            store8_bf(g.o + m * g.step_o + p * g.ld_o + q, v, n);
-        }
+    for (int k = 0; k < 8; ++k) {
+        const float x = fabsf(v[k]) < 0x1p-14f ? 0.0f : v[k];
+        most = fmaxf(most, fabsf(x));
+        t[k] = __float_as_uint(x) + kHalfPlace;
     }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(t[2 * k]), __uint_as_float(t[2 * k + 1])));
+        if (!(most < 65504.0f)) h[k] = 0x7E007E00u;
+    }
+    *hi = __builtin_bit_cast(h8, v4u{h[0], h[1], h[2], h[3]});
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        (*lo)[k] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t[4 * k + 3] >> 5, t[4 * k + 2] >> 5, 0x0C0C0400u),
+                                         __builtin_amdgcn_perm(t[4 * k + 1] >> 5, t[4 * k] >> 5, 0x0C0C0400u), 0x05040100u);
+}
+__device__ __forceinline__ float joined(float hi, const v2u& lo, int k) {
+    return __uint_as_float((__float_as_uint(hi) | (lo[k >> 2] >> 8 * (k & 3) & 255u) << 5) - kHalfPlace);
 }
 
-// A wave's blocks, (FP 16) x 64 outputs, through its 16 KB of LDS, 64 rows at a time, so that
-// a lane has eight consecutive columns. Blocks are computed as (q, p): a lane holds four
-// consecutive columns of a row, a 16-byte unit, unit u of row o at u ^ (o & 15). Below the
-// diagonal of a symmetric product the same outputs go to their mirrored places too, eight
-// consecutive rows to a lane.
-template <int OP, int FP, typename Row, typename Col>
-__device__ __forceinline__ void finish(const OrthArgs& g, int64_t m, const v4f (&acc)[FP][4], float* mine, bool mirror,
-                                       Row row_of, Col col_of) {
-    const int lane = threadIdx.x & 63, c = lane & 7;
+// What a product makes of its sums, for a lane's eight columns q .. q + 7 of matrix m: what
+// the columns need is loaded once (the constructor), what a row needs ahead of its use (In,
+// load), so that many rows' loads are under way.
+template <int OP>
+struct OrthEpilogue;
+
+// A: F off the diagonal, the diagonal in fp32.
+template <>
+struct OrthEpilogue<kGram> {
+    static constexpr float kOff = kScale / (kScaleX * kScaleX);
+    struct In {};
+    const OrthArgs& g;
+    _Float16* out;
+    float* diag;
+    const int64_t q;
+    __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t col)
+        : g(a), out(a.out + m * a.step_out + col), diag(a.diag_out + m * a.step_diag), q(col) {}
+    __device__ __forceinline__ void load(In&, int64_t) const {}
+    // v: in, the sums; out, what the matrix holds, here and, of a symmetric one, at the mirrored place
+    __device__ __forceinline__ void put(const In&, int64_t p, float v[8]) const {
 #pragma unroll
-    for (int i0 = 0; i0 < FP; i0 += 4) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
-                *reinterpret_cast<v4f*>(mine + 64 * o + 4 * (u ^ (o & 15))) = acc[i0 + i][j];
-            }
-        const int64_t p0 = row_of(i0), q = col_of(c >> 1) + 8 * (c & 1);
-        if (p0 < g.P && q < g.Q) {
-#pragma unroll 2
-            for (int o = lane >> 3; o < 64; o += 8) {
-                const v4f lo = *reinterpret_cast<const v4f*>(mine + 64 * o + 4 * ((2 * c) ^ (o & 15)));
-                const v4f hi = *reinterpret_cast<const v4f*>(mine + 64 * o + 4 * ((2 * c + 1) ^ (o & 15)));
-                float v[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
-                epilogue8<OP>(g, m, p0 + o, q, v);
+        for (int k = 0; k < 8; ++k) {
+            v[k] *= kOff;
+            if (p == q + k) {
+                diag[p] = v[k] * (1.0f / kScale);
+                v[k] = 0.0f;
             }
         }
-        if (OP != kUpdate && mirror && p0 < g.P) {
-#pragma unroll 2
-            for (int j = lane >> 3; j < 64; j += 8) {
-                const int64_t row = col_of(j >> 4) + (j & 15);
-                if (row >= g.Q) continue;
-                float v[8];
+        put_h8(out + p * g.ld_out, v);
+    }
+};
+
+// b A + c A A, where A = D + F: A A = F F + D F + F D + D D.
+template <>
+struct OrthEpilogue<kSquare> {
+    static constexpr float kOnce = 1.0f / kScale;
+    struct In {
+        h8 f;
+        float d;
+    };
+    const OrthArgs& g;
+    const _Float16* in;
+    const float* from;
+    _Float16* out;
+    float* diag;
+    const int64_t q;
+    float dq[8];
+    __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t col)
+        : g(a), in(a.in + m * a.step_in + col), from(a.diag_in + m * a.step_diag), out(a.out + m * a.step_out + col),
+          diag(a.diag_out + m * a.step_diag), q(col) {
+        load8_f(dq, from + q, 8);
+    }
+    __device__ __forceinline__ void load(In& r, int64_t p) const {
+        r.f = *reinterpret_cast<const h8*>(in + p * g.ld_in);
+        r.d = from[p];
+    }
+    __device__ __forceinline__ void put(const In& r, int64_t p, float v[8]) const {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const int o = 8 * c + k;
-                    v[k] = mine[64 * o + 4 * ((j >> 2) ^ (o & 15)) + (j & 3)];
+        for (int k = 0; k < 8; ++k) {
+            const float f = (float)r.f[k], ff = v[k] * kOnce;
+            v[k] = fmaf(g.cc, fmaf(r.d + dq[k], f, ff), g.cb * f);
+            if (p == q + k) {
+                diag[p] = fmaf(g.cc, fmaf(r.d, r.d, ff * kOnce), g.cb * r.d);
+                v[k] = 0.0f;
+            }
+        }
+        put_h8(out + p * g.ld_out, v);
+    }
+};
+
+// a X + (b A + c A A) X.
+template <>
+struct OrthEpilogue<kUpdate> {
+    static constexpr float kOnce = 1.0f / kScale;
+    struct In {
+        h8 hi;
+        v2u lo;
+        float e;
+    };
+    const OrthArgs& g;
+    const int64_t at;
+    const float* from;
+    uint16_t* o;
+    const int n;                            // of the columns in the last step's output
+    float eq[8];
+    __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t q)
+        : g(a), at(m * a.step_in + q), from(a.diag_in + m * a.step_diag), o(a.o + m * a.step_o + q),
+          n(a.cols - q >= 8 ? 8 : a.cols > q ? (int)(a.cols - q) : 0) {
+        if (g.by_column) load8_f(eq, from + q, 8);
+    }
+    __device__ __forceinline__ void load(In& r, int64_t p) const {
+        r.hi = *reinterpret_cast<const h8*>(g.in + at + p * g.ld_in);
+        r.lo = *reinterpret_cast<const v2u*>(g.lo + at + p * g.ld_in);
+        r.e = from[g.by_column ? 0 : p];
+    }
+    __device__ __forceinline__ void put(const In& r, int64_t p, float v[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float h = (float)r.hi[k], x = joined(h, r.lo, k);
+            v[k] = fmaf(g.ca, x, fmaf(g.by_column ? eq[k] : r.e, g.low ? x : h, v[k] * kOnce));
+        }
+        if (g.out) {
+            h8 h;
+            v2u l;
+            split_x8(v, &h, &l);
+            *reinterpret_cast<h8*>(g.out + at + p * g.ld_in) = h;
+            *reinterpret_cast<v2u*>(g.lo + at + p * g.ld_in) = l;
+        } else if (p < g.rows && n > 0) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] *= g.scale * (1.0f / kScaleX);
+            store8_bf(o + p * g.ld_o, v, n);
+        }
+    }
+};
+
+// A wave's blocks, four times FQ at a time, through its part of LDS (64 rows of 16 FQ floats),
+// so that a lane has eight consecutive columns, the same in all its rows of a run. Blocks are
+// computed as (q, p): a lane holds four consecutive columns of a row, a 16-byte unit, unit u
+// of row o at u ^ (o & mask). What a lane's rows need is asked for a run ahead, and (ask) of the
+// first run together: before the reduction by k_orth_mid, behind it by the others, which
+// gain nothing from it or lose (12 updates of 768 x 2304 55 to 59 us). Below the diagonal of a
+// symmetric product the results go back to LDS, and from there to their mirrored places,
+// eight consecutive rows to a lane. row_of(i): first row of block i, an even one's before the
+// next's; col_of(run): first of its columns.
+template <int OP, int FQ, int RUNS, typename Row, typename Col>
+struct Finish {
+    static constexpr int kCols = 16 * FQ, kMask = 4 * FQ - 1, kGroups = 2 * FQ, kStep = 64 / kGroups, kRows = 64 / kStep;
+    const OrthArgs& g;
+    const int64_t m;
+    const Row row_of;
+    const Col col_of;
+    const int lane, c, o0;
+    const OrthEpilogue<OP> epi[2];
+    typename OrthEpilogue<OP>::In in[kRows];
+
+    __device__ __forceinline__ Finish(const OrthArgs& a, int64_t matrix, Row rows, Col cols)
+        : g(a), m(matrix), row_of(rows), col_of(cols), lane(threadIdx.x & 63), c(lane % kGroups), o0(lane / kGroups),
+          epi{{a, m, inside(0)}, {a, m, inside(RUNS - 1)}} {}
+    __device__ __forceinline__ int64_t row(int o) const { return row_of(o >> 4) + (o & 15); }
+    __device__ __forceinline__ int64_t column(int run) const { return col_of(run) + 8 * c; }
+    __device__ __forceinline__ int64_t inside(int run) const { return column(run) < g.Q ? column(run) : 0; }
+    __device__ __forceinline__ void load(int run, int u) {
+        const int64_t p = row(o0 + kStep * u);
+        if (column(run) < g.Q && p < g.P) epi[run].load(in[u], p);
+    }
+    __device__ __forceinline__ void ask() {
+#pragma unroll
+        for (int u = 0; u < kRows; ++u) load(0, u);
+    }
+    __device__ __forceinline__ void operator()(const v4f (&acc)[4][FQ * RUNS], float* mine, bool mirror) {
+        const int r = lane & 7;
+#pragma unroll
+        for (int run = 0; run < RUNS; ++run) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < FQ; ++j) {
+                    const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
+                    *reinterpret_cast<v4f*>(mine + kCols * o + 4 * (u ^ (o & kMask))) = acc[i][FQ * run + j];
                 }
-                epilogue8<OP>(g, m, row, p0 + 8 * c, v);
+#pragma unroll
+            for (int u = 0; u < kRows; ++u) {
+                const int o = o0 + kStep * u;
+                v4f* const lo = reinterpret_cast<v4f*>(mine + kCols * o + 4 * ((2 * c) ^ (o & kMask)));
+                v4f* const hi = reinterpret_cast<v4f*>(mine + kCols * o + 4 * ((2 * c + 1) ^ (o & kMask)));
+                float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
+                if (column(run) < g.Q && row(o) < g.P) epi[run].put(in[u], row(o), v);
+                if (OP != kUpdate && mirror) {
+                    *lo = v4f{v[0], v[1], v[2], v[3]};
+                    *hi = v4f{v[4], v[5], v[6], v[7]};
+                }
+                if (run + 1 < RUNS) load(run + 1, u);
+            }
+            if (OP != kUpdate && mirror && row(8 * r) < g.P) {
+#pragma unroll 2
+                for (int j = lane >> 3; j < kCols; j += 8) {
+                    float v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int o = 8 * r + k;
+                        v[k] = mine[kCols * o + 4 * ((j >> 2) ^ (o & kMask)) + (j & 3)];
+                    }
+                    const int64_t q = col_of(run) + j;
+                    if (q < g.Q) put_h8(g.out + m * g.step_out + q * g.ld_out + row(8 * r), v);
+                }
             }
         }
     }
+};
+template <int OP, int FQ, int RUNS, typename Row, typename Col>
+__device__ __forceinline__ Finish<OP, FQ, RUNS, Row, Col> finish(const OrthArgs& g, int64_t m, Row row_of, Col col_of) {
+    return Finish<OP, FQ, RUNS, Row, Col>(g, m, row_of, col_of);
 }
 
 // ---------------------------------------------------------------------------
@@ -335,27 +463,126 @@ __device__ __forceinline__ void finish(const OrthArgs& g, int64_t m, const v4f (
 // ---------------------------------------------------------------------------
 
 __device__ __forceinline__ v4f mul(h8 a, h8 b, v4f c) { return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0); }
+template <int FP, int FQ>
+__device__ __forceinline__ void clear(v4f (&acc)[FP][FQ]) {
+#pragma unroll
+    for (int i = 0; i < FP; ++i)
+#pragma unroll
+        for (int j = 0; j < FQ; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
+}
+
+// 64 x 64 outputs by eight waves, for outputs of few tiles: two groups of four waves take
+// every other reduction tile, each with a ring of four in LDS, and their sums are joined
+// there. A wave has 32 x 32.
+template <int OP, bool TA, bool TB>
+__global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
+    constexpr bool SYM = OP != kUpdate;
+    constexpr int H = 64, kTile = H * kBR, kSlot = 2 * kTile, kSlots = 4;
+    __shared__ __attribute__((aligned(16))) _Float16 lds[2 * kSlots * kSlot];
+    int tp, tq;
+    const int64_t m = place<SYM>(g, g.first + in_turn(g.all), &tp, &tq), p0 = (int64_t)tp * H, q0 = (int64_t)tq * H;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
+    const int wp = (wave >> 1 & 1) * 32, wq = (wave & 1) * 32;
+    v4f acc[2][2];
+    clear(acc);
+    const Fragments<H, TA> ga(wp);
+    const Fragments<H, TB> gb(wq);
+    const uint32_t base = lds_address(lds) + 2 * kSlots * kSlot * half;
+    Loader<H, TA, 256, 1> la;
+    Loader<H, TB, 256, 1> lb;
+    constexpr int kLoads = 2 * Loader<H, TA, 256, 1>::kLoads;
+    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
+    la.base += half * la.step;
+    lb.base += half * lb.step;
+    const int n = g.turns / 2;              // sides are padded to 128: an even number
+    // loads of tiles behind the last are stopped by their buffer's range
+    const auto load = [&](int k) {
+        const int records = k < n ? kAllRecords : 0;
+        const uint32_t to = base + 2 * kSlot * (k % kSlots);
+        la.issue(0, la.base, to, wave & 3, records);
+        lb.issue(0, lb.base, to + 2 * kTile, wave & 3, records);
+        la.base += 2 * la.step;
+        lb.base += 2 * lb.step;
+    };
+#pragma unroll
+    for (int k = 0; k < kSlots - 1; ++k) load(k);
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        loads_landed<(kSlots - 2) * kLoads>();
+        meet_waves();
+        load(k + kSlots - 1);
+        const uint32_t tile = base + 2 * kSlot * (k % kSlots);
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+            h8 fa[2], fb[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                fa[i] = ga.get(tile, i, s);
+                fb[i] = gb.get(tile + 2 * kTile, i, s);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mul(fb[j], fa[i], acc[i][j]);
+        }
+    }
+    loads_landed<0>();
+    const OrthEpilogue<OP> epi(g, m, q0 + 8 * (threadIdx.x & 7));
+    typename OrthEpilogue<OP>::In in;
+    epi.load(in, p0 + (threadIdx.x >> 3));
+    meet_waves();
+    // [64][64] floats, unit u of row o at u ^ (o & 15)
+    float* const sums = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int turn = 1; turn >= 0; --turn) {
+        if (half == turn)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int o = wp + 16 * i + ((int)threadIdx.x & 15), u = (wq >> 2) + 4 * j + ((int)threadIdx.x >> 4 & 3);
+                    v4f* const at = reinterpret_cast<v4f*>(sums + 64 * o + 4 * (u ^ (o & 15)));
+                    if (turn) *at = acc[i][j];
+                    else *at = acc[i][j] + *at;
+                }
+        meet_waves();
+    }
+    const int o = threadIdx.x >> 3, c = threadIdx.x & 7;
+    v4f* const lo = reinterpret_cast<v4f*>(sums + 64 * o + 4 * ((2 * c) ^ (o & 15)));
+    v4f* const hi = reinterpret_cast<v4f*>(sums + 64 * o + 4 * ((2 * c + 1) ^ (o & 15)));
+    float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
+    epi.put(in, p0 + o, v);
+    if (SYM && tp != tq) {
+        *lo = v4f{v[0], v[1], v[2], v[3]};
+        *hi = v4f{v[4], v[5], v[6], v[7]};
+        meet_waves();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int row = 8 * c + k;
+            v[k] = sums[64 * row + 4 * ((o >> 2) ^ (row & 15)) + (o & 3)];
+        }
+        put_h8(g.out + m * g.step_out + (q0 + o) * g.ld_out + p0 + 8 * c, v);
+    }
+}
 
 // 128 x 128 outputs by four waves, 64 x 64 each; two tiles of the reduction in LDS, the next
 // one loading while one is multiplied. Two workgroups fit a compute unit.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
     constexpr bool SYM = OP != kUpdate;
-    constexpr int kTile = kSide * kBR;
+    constexpr int H = 128, kTile = H * kBR;
     __shared__ __attribute__((aligned(16))) _Float16 lds[4 * kTile];
     int tp, tq;
-    const int64_t m = place<SYM>(g, &tp, &tq), p0 = (int64_t)tp * kSide, q0 = (int64_t)tq * kSide;
+    const int64_t m = place<SYM>(g, g.first + in_turn(g.all), &tp, &tq), p0 = (int64_t)tp * H, q0 = (int64_t)tq * H;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = (wave >> 1) * 64, wq = (wave & 1) * 64;
     v4f acc[4][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = v4f{0.0f, 0.0f, 0.0f, 0.0f};
-    const Fragments<TA> ga(wp);
-    const Fragments<TB> gb(wq);
+    clear(acc);
+    const Fragments<H, TA> ga(wp);
+    const Fragments<H, TB> gb(wq);
     const uint32_t base = lds_address(lds);
-    Loader<TA, 256, 1> la;
-    Loader<TB, 256, 1> lb;
+    Loader<H, TA, 256, 1> la;
+    Loader<H, TB, 256, 1> lb;
     la.init(g.a + m * g.step_a, g.lda, p0, g.P);
     lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
     la.issue(0, la.base, base, wave, kAllRecords);
@@ -383,8 +610,277 @@ __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
         }
     }
     meet_waves();
-    finish<OP, 4>(g, m, acc, reinterpret_cast<float*>(lds) + wave * 64 * 64, tp != tq, [&](int i) { return p0 + wp + 16 * i; },
-                  [&](int j) { return q0 + wq + 16 * j; });
+    auto end = finish<OP, 4, 1>(g, m, [&](int i) { return p0 + wp + 16 * i; }, [&](int) { return q0 + wq; });
+    end.ask();
+    end(acc, reinterpret_cast<float*>(lds) + wave * 64 * 64, tp != tq);
+}
+
+// 128 x 128 outputs by eight waves, 64 x 32 each, one workgroup to a compute unit: a ring of
+// four reduction tiles, in turns that barriers divide into two parts. A wave reads the
+// turn's operands and asks for the tile three ahead; then it multiplies; waves 4-7 are one
+// barrier behind waves 0-3, which share their SIMDs, so that one wave of each pair
+// multiplies while the other reads. A tile's place is asked for again one turn after it was
+// read, two barriers or more after its last reads began; each turn ends when the next turn's
+// tile is here, one barrier before anyone reads it.
+template <int OP, bool TA, bool TB>
+__global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
+    constexpr bool SYM = OP != kUpdate;
+    constexpr int H = 128, kTile = H * kBR, kSlot = 2 * kTile, kSlots = 4;
+    __shared__ __attribute__((aligned(16))) _Float16 lds[kSlots * kSlot];
+    int tp, tq;
+    const int64_t m = place<SYM>(g, g.first + in_turn(g.all), &tp, &tq), p0 = (int64_t)tp * H, q0 = (int64_t)tq * H;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = (wave >> 2) * 64, wq = (wave & 3) * 32;
+    v4f acc[4][2];
+    clear(acc);
+    const Fragments<H, TA> ga(wp);
+    const Fragments<H, TB> gb(wq);
+    const uint32_t base = lds_address(lds);
+    Loader<H, TA, 512, 1> la;
+    Loader<H, TB, 512, 1> lb;
+    constexpr int kLoads = 2 * Loader<H, TA, 512, 1>::kLoads;
+    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
+    const int n = g.turns;
+    const auto load = [&](int k) {
+        const int records = k < n ? kAllRecords : 0;
+        const uint32_t to = base + 2 * kSlot * (k % kSlots);
+        la.issue(0, la.base, to, wave, records);
+        lb.issue(0, lb.base, to + 2 * kTile, wave, records);
+        la.base += la.step;
+        lb.base += lb.step;
+    };
+    auto end = finish<OP, 2, 1>(g, m, [&](int i) { return p0 + wp + 16 * i; }, [&](int) { return q0 + wq; });
+    end.ask();
+#pragma unroll
+    for (int k = 0; k < kSlots - 1; ++k) load(k);
+    loads_landed<(kSlots - 2) * kLoads>();
+    meet_waves();
+    if (wave >= 4) meet_waves();
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const uint32_t tile = base + 2 * kSlot * (k % kSlots);
+        h8 fa[2][4], fb[2][2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) fb[s][j] = gb.get(tile + 2 * kTile, j, s);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fa[s][i] = ga.get(tile, i, s);
+        }
+        load(k + kSlots - 1);
+        loads_landed<(kSlots - 2) * kLoads>();
+        meet_waves();
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) acc[i][j] = mul(fb[s][j], fa[s][i], acc[i][j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+        meet_waves();
+    }
+    if (wave < 4) meet_waves();
+    loads_landed<0>();
+    meet_waves();
+    end(acc, reinterpret_cast<float*>(lds) + wave * 64 * 32, tp != tq);
+}
+
+// 256 x 256 outputs by eight waves, one workgroup to a compute unit. Reduction tiles lie in
+// LDS as halves of 128 outer indices, two tiles of four halves. A wave's outputs are 32 x 64
+// of each quarter (half of A, half of B), so that it stores whole lines. A tile is two turns
+// of 32 matrix instructions, and a turn has two parts that barriers divide: the wave reads
+// what its turn needs and no turn before it read, and asks for halves of the tiles to come;
+// then it multiplies. Waves 4-7 are one barrier behind waves 0-3, so that one wave of each
+// pair multiplies while the other reads.
+//
+//   turn      reads                asks for                        multiplies
+//   2k        A0(k) A1(k) B0(k)    B1(k + 1)                       A0 B0, A1 B0
+//   2k + 1    B1(k)                A0(k + 2) A1(k + 2) B0(k + 2)   A0 B1, A1 B1
+//
+// A half is read in one turn only, by all waves within the two barrier intervals that begin
+// with that turn of waves 0-3, and asked for again one turn later: after them. What turn f
+// reads was asked for in turn f - 3, or before, or in the prologue; turn f - 1 waits until at
+// most the four halves of the two latest turns are under way, and its barrier comes before
+// anyone's turn f.
+// (Four turns of 16 instructions, eight barriers a tile in place of four: the Gram product
+// of 4096 x 11008 242 us in place of 200. Half of the first turn's reads a turn ahead, 12 KB in
+// every turn in place of 16 and 8: 208 us there, and the update's 340 in place of 348. The
+// 32 x 32 matrix instruction, with four turns: 5-8% slower.)
+//
+// The workgroup takes reduction tiles first .. last of output tile `t`: WHOLE, or a part,
+// whose sums go to memory for k_orth_join, a wave's as they lie in its registers.
+template <int OP, bool TA, bool TB, bool WHOLE>
+__device__ __forceinline__ void wide_tile(const OrthArgs& g, int t, int first, int last, _Float16* lds, float* part) {
+    constexpr bool SYM = OP != kUpdate;
+    constexpr int H = 128, B = 256, kHalf = H * kBR;
+    int tp, tq;
+    const int64_t m = place<SYM>(g, t, &tp, &tq), p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), wp = (wave & 3) * 32, wq = (wave >> 2) * 64;
+    v4f acc[4][8];                          // blocks (2 a + i, 4 b + j): block (i, j) of the quarter of halves a and b
+    clear(acc);
+    const Fragments<H, TA> ga(wp);
+    const Fragments<H, TB> gb(wq);
+    h8 fa[2][2][2], fb[2][4];               // [half][step][block], [step][block]
+    const uint32_t base = lds_address(lds);
+    const auto half = [&](int k, int h) { return base + 2 * kHalf * (4 * (k & 1) + h); };   // A0, A1, B0, B1 of tile k
+    const auto read_a = [&](int h, uint32_t from) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) fa[h][s][i] = ga.get(from, i, s);
+    };
+    const auto read_b = [&](uint32_t from) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) fb[s][j] = gb.get(from, j, s);
+    };
+    const auto multiply = [&](int b) {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[2 * a + i][4 * b + j] = mul(fb[s][j], fa[a][s][i], acc[2 * a + i][4 * b + j]);
+        __builtin_amdgcn_s_setprio(0);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    Loader<H, TA, 512, 2> la;
+    Loader<H, TB, 512, 2> lb;
+    constexpr int kLoads = Loader<H, TA, 512, 2>::kLoads;
+    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
+    la.base += first * la.step;
+    lb.base += first * lb.step;
+    const int n = last - first;
+    // loads of tiles behind the last are stopped by their buffer's range
+    const auto there = [&](int k) { return k < n ? kAllRecords : 0; };
+    la.issue(0, la.base, half(0, 0), wave, kAllRecords);
+    la.issue(1, la.base, half(0, 1), wave, kAllRecords);
+    lb.issue(0, lb.base, half(0, 2), wave, kAllRecords);
+    lb.issue(1, lb.base, half(0, 3), wave, kAllRecords);
+    la.issue(0, la.base + la.step, half(1, 0), wave, there(1));
+    la.issue(1, la.base + la.step, half(1, 1), wave, there(1));
+    lb.issue(0, lb.base + lb.step, half(1, 2), wave, there(1));
+    la.base += 2 * la.step;                 // of tile k + 2
+    lb.base += 2 * lb.step;
+    loads_landed<4 * kLoads>();
+    meet_waves();
+    if (wave >= 4) meet_waves();
+#pragma unroll 1
+    for (int k = 0; k < n; ++k) {
+        const int one = there(k + 1), two = there(k + 2);
+        read_a(0, half(k, 0));
+        read_b(half(k, 2));
+        read_a(1, half(k, 1));
+        lb.issue(1, lb.base - lb.step, half(k + 1, 3), wave, one);
+        loads_landed<4 * kLoads>();
+        meet_waves();
+        multiply(0);
+        meet_waves();
+        read_b(half(k, 3));
+        la.issue(0, la.base, half(k, 0), wave, two);
+        la.issue(1, la.base, half(k, 1), wave, two);
+        lb.issue(0, lb.base, half(k, 2), wave, two);
+        la.base += la.step;
+        lb.base += lb.step;
+        loads_landed<4 * kLoads>();
+        meet_waves();
+        multiply(1);
+        meet_waves();
+    }
+    if (wave < 4) meet_waves();
+    loads_landed<0>();
+    meet_waves();
+    if constexpr (WHOLE) {
+        auto end = finish<OP, 4, 2>(g, m, [&](int i) { return p0 + H * (i >> 1) + wp + 16 * (i & 1); },
+                                    [&](int run) { return q0 + H * run + wq; });
+        end.ask();
+        end(acc, reinterpret_cast<float*>(lds) + wave * 64 * 64, SYM && tp != tq);
+    } else {
+        float* const to = part + wave * (64 * 128) + 4 * ((int)threadIdx.x & 63);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) *reinterpret_cast<v4f*>(to + 256 * (16 * (j >> 2) + 4 * i + (j & 3))) = acc[i][j];
+    }
+}
+template <int OP, bool TA, bool TB>
+__global__ void __launch_bounds__(512) k_orth_wide(const OrthArgs g) {
+    __shared__ __attribute__((aligned(16))) _Float16 lds[2 * 4 * kSide * kBR];
+    wide_tile<OP, TA, TB, true>(g, g.first + in_turn(g.all), 0, g.turns, lds, nullptr);
+}
+
+// Fewer tiles than kSplit, shared by kSplit workgroups, all of them at the same place of the
+// reduction as those that share operand rows with them: workgroup w < a s takes slice w / a of
+// s of tile w % a; the r tiles that are left over are cut likewise, into t slices, for a
+// second part of each workgroup's work. k_orth_join puts the parts together, in order.
+// (Runs of consecutive reduction tiles, whatever tile they are of, share no operand rows in
+// the caches: the Gram product of 4096 x 11008 took 240 us, 2.2 a tile's turns.)
+constexpr int kSplit = 256;
+constexpr int64_t kPartFloats = 256 * 256;
+struct Slices {
+    int32_t s, a, r, t;
+};
+__host__ __device__ __forceinline__ Slices slices_of(int32_t tiles) {
+    Slices c;
+    c.s = (kSplit + tiles - 1) / tiles;
+    c.a = kSplit / c.s;
+    c.r = tiles - c.a;
+    c.t = c.r > 0 ? kSplit / c.r : 0;
+    return c;
+}
+
+template <int OP, bool TA, bool TB>
+__global__ void __launch_bounds__(512) k_orth_split(const OrthArgs g) {
+    __shared__ __attribute__((aligned(16))) _Float16 lds[2 * 4 * kSide * kBR];
+    const int w = in_turn(kSplit);
+    const Slices c = slices_of(g.all);
+#pragma unroll 1
+    for (int part = 0; part < 2; ++part) {
+        const int tiles = part ? c.r : c.a, n = part ? c.t : c.s;
+        if (w >= tiles * n) continue;
+        // the same in all lanes, which the divisions hide from the compiler
+        const int slice = __builtin_amdgcn_readfirstlane(w / tiles);
+        const int first = __builtin_amdgcn_readfirstlane(g.turns * slice / n);
+        const int last = __builtin_amdgcn_readfirstlane(g.turns * (slice + 1) / n);
+        wide_tile<OP, TA, TB, false>(g, g.first + (part ? c.a : 0) + w - slice * tiles, first, last, lds,
+                                     g.part + (kSplit * part + w) * kPartFloats);
+    }
+}
+// A wave to half of what one of the waves that computed it had of a tile, a workgroup each.
+template <int OP>
+__global__ void __launch_bounds__(64) k_orth_join(const OrthArgs g) {
+    __shared__ __attribute__((aligned(16))) float lds[64 * 64];
+    constexpr bool SYM = OP != kUpdate;
+    constexpr int H = 128, B = 256;
+    const int t = blockIdx.x >> 4, wave = blockIdx.x >> 1 & 7, half = blockIdx.x & 1;
+    const int wp = (wave & 3) * 32, wq = (wave >> 2) * 64;
+    const Slices c = slices_of(g.all);
+    const int tiles = t < c.a ? c.a : c.r, n = t < c.a ? c.s : c.t;
+    const float* from = g.part + (t < c.a ? t : kSplit + t - c.a) * kPartFloats + wave * (64 * 128) + half * (64 * 64) +
+                        4 * threadIdx.x;
+    v4f acc[4][4];
+    clear(acc);
+#pragma unroll 2
+    for (int k = 0; k < n; ++k, from += tiles * kPartFloats)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) acc[i][j] += *reinterpret_cast<const v4f*>(from + 256 * (4 * i + j));
+    int tp, tq;
+    const int64_t m = place<SYM>(g, g.first + t, &tp, &tq), p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
+    auto end = finish<OP, 4, 1>(g, m, [&](int i) { return p0 + H * (i >> 1) + wp + 16 * (i & 1); },
+                                [&](int) { return q0 + H * half + wq; });
+    end.ask();
+    end(acc, lds, SYM && tp != tq);
 }
 
 // ---------------------------------------------------------------------------
@@ -396,7 +892,7 @@ struct StartArgs {
     int64_t ld_x, step_x, rows, cols;
     int64_t Rp, Cp;
     _Float16* hi;
-    _Float16* lo;
+    uint8_t* lo;
     double* parts;                  // [matrix][kSquareParts]
     int32_t n_parts;
     double eps;
@@ -452,23 +948,22 @@ __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
     const int64_t m = blockIdx.y, chunks = g.Cp / 8, all = g.Rp * chunks;
     const double square = block_sum((int)threadIdx.x < g.n_parts ? g.parts[m * kSquareParts + threadIdx.x] : 0.0);
     const double norm = sqrt(square), inv = 1.0 / (double)chunks;
-    const double by = norm < INFINITY ? (double)kScale / (norm + g.eps) : (double)NAN;
+    const double by = (double)kScaleX / (norm + g.eps);
+    const bool fine = norm < INFINITY;
 #pragma unroll 2
     for (int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x; id < all; id += (int64_t)gridDim.x * 256) {
         int64_t c;
         const int64_t row = row_of_chunk(id, chunks, inv, &c);
         float v[8];
         load_x8<XF>(v, g, m, row, 8 * c);
-        h8 h, l;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float x = (float)((double)v[k] * by);
-            h[k] = (_Float16)x;
-            l[k] = (_Float16)((x - (float)h[k]) * kLow);
-        }
+        for (int k = 0; k < 8; ++k) v[k] = fine ? (float)((double)v[k] * by) : NAN;
+        h8 h;
+        v2u l;
+        split_x8(v, &h, &l);
         const int64_t at = m * g.Rp * g.Cp + row * g.Cp + 8 * c;
         *reinterpret_cast<h8*>(g.hi + at) = h;
-        *reinterpret_cast<h8*>(g.lo + at) = l;
+        *reinterpret_cast<v2u*>(g.lo + at) = l;
     }
 }
 
@@ -478,13 +973,54 @@ __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
 
 static int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
 
+static int64_t over(int64_t n, int64_t by) { return (n + by - 1) / by; }
+static int64_t tiles_of(int64_t P, int64_t Q, int64_t side, bool sym) {
+    const int64_t p = over(P, side), q = over(Q, side);
+    return sym ? p * (p + 1) / 2 : p * q;
+}
+
+// How a product of n matrices runs, by an estimate of its time in microseconds.
+enum OrthKind { kFew, kMid, kTwo, kWide };
+struct OrthPlan {
+    OrthKind kind;
+    int64_t split;                  // kWide: of all tiles, the last ones that are split
+};
+static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym) {
+    const int64_t few = n * tiles_of(P, Q, 64, sym), mid = n * tiles_of(P, Q, 128, sym), wide = n * tiles_of(P, Q, 256, sym);
+    OrthPlan best{kTwo, 0};
+    double least = 1e300;
+    const auto offer = [&](OrthKind k, int64_t split, double time) {
+        if (time < least) {
+            least = time;
+            best = OrthPlan{k, split};
+        }
+    };
+    // us for a reduction tile (turn) and for a tile's start and end, in a round of the chip:
+    // measured at 768 x 768 to 4096 x 11008, one matrix to twelve
+    const int64_t rest = mid % 512;
+    offer(kTwo, 0, mid / 512 * (0.9 * turns + 9) + (rest == 0 ? 0 : rest <= 256 ? 0.65 * turns + 8.5 : 0.9 * turns + 9));
+    offer(kFew, 0, over(few, 256) * (0.185 * turns + 3.4));
+    if (mid <= 256) offer(kMid, 0, 0.49 * turns + 8.5);
+    const int64_t left = wide % kSplit;
+    const double ends = sym ? 12 : 18, rounds = wide / 256 * (1.4 * turns + ends);
+    offer(kWide, 0, rounds + (left == 0 ? 0 : (left <= 160 ? 1.15 : 1.4) * turns + ends));
+    if (left > 0) {
+        const Slices c = slices_of((int32_t)left);
+        const double each = (double)turns / c.s + (c.r > 0 ? (double)turns / c.t : 0);
+        if (turns >= 2 * c.s && turns >= c.t)       // two reduction tiles to a slice, one to the others
+            offer(kWide, left, rounds + 1.4 * each + 15 + 0.088 * (c.a * c.s + c.r * c.t));
+    }
+    return best;
+}
+
 // What a group of matrices has in the workspace, in this order: X hi twice and lo, A and
-// b A + c A A, their diagonals, the partial sums of squares.
+// b A + c A A, their diagonals, the partial sums of squares, those of split tiles.
 struct OrthShape {
     int64_t Rp, Cp, m;              // padded sides, the smaller one
     int64_t x, a;                   // elements
     size_t each;                    // bytes of a matrix
     int64_t group;                  // matrices at a time
+    size_t part;                    // bytes of split tiles' partial sums
 };
 static OrthShape shape_of(int64_t batch, int64_t rows, int64_t cols) {
     OrthShape s{};
@@ -493,53 +1029,69 @@ static OrthShape shape_of(int64_t batch, int64_t rows, int64_t cols) {
     s.m = s.Rp < s.Cp ? s.Rp : s.Cp;
     s.x = s.Rp * s.Cp;
     s.a = s.m * s.m;
-    s.each = (size_t)(6 * s.x + 4 * s.a + 8 * s.m) + kSquareParts * sizeof(double);
+    s.each = (size_t)(5 * s.x + 4 * s.a + 8 * s.m) + kSquareParts * sizeof(double);
     const int64_t most = (int64_t)((size_t(4) << 30) / s.each);
-    s.group = most < 1 ? 1 : most > 16384 ? 16384 : most;
+    s.group = most < 1 ? 1 : most > 16384 ? 16384 : most;     // a grid's y
     if (s.group > batch) s.group = batch;
+    // the last group may have fewer matrices, and split what the others need not
+    const int64_t last = batch - (batch - 1) / s.group * s.group, gram = (rows > cols ? s.Rp : s.Cp) / kBR, square = s.m / kBR;
+    bool split = false;
+    for (const int64_t n : {s.group, last})
+        split = split || plan_of(n, s.m, s.m, gram, true).split || plan_of(n, s.m, s.m, square, true).split ||
+                plan_of(n, s.Rp, s.Cp, square, false).split;
+    s.part = split ? 2 * kSplit * kPartFloats * sizeof(float) : 0;
     return s;
 }
 
 size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
     if (batch < 1 || rows < 1 || cols < 1) return 0;
     const OrthShape s = shape_of(batch, rows, cols);
-    return (size_t)s.group * s.each;
+    return (size_t)s.group * s.each + s.part;
 }
 
 template <int OP, bool TA, bool TB>
-static hipError_t product(OrthArgs g, int64_t n, hipStream_t st) {
-    g.np = (int32_t)(g.P / kSide);
-    g.nq = (int32_t)(g.Q / kSide);
-    g.tiles = OP == kUpdate ? g.np * g.nq : g.np * (g.np + 1) / 2;
-    // as many matrices to a launch as its 2^31 threads hold
-    const int64_t most = (int64_t(1) << 23) / g.tiles, first_launch = most < 1 ? 1 : most;
-    for (int64_t done = 0; done < n; done += first_launch) {
-        const int64_t some = n - done < first_launch ? n - done : first_launch;
-        g.all = (int32_t)(g.tiles * some);
-        hipLaunchKernelGGL((k_orth<OP, TA, TB>), dim3((unsigned)g.all), dim3(256), 0, st, g);
+static hipError_t run(const OrthPlan& plan, OrthArgs g, int64_t n, hipStream_t st) {
+    constexpr bool SYM = OP != kUpdate;
+    const OrthKind kind = plan.kind;
+    const int side = kind == kFew ? 64 : kind == kWide ? 256 : 128, threads = kind == kTwo ? 256 : 512;
+    g.np = (int32_t)over(g.P, side);
+    g.nq = (int32_t)over(g.Q, side);
+    g.tiles = (int32_t)tiles_of(g.P, g.Q, side, SYM);
+    const auto k = kind == kFew ? k_orth_few<OP, TA, TB> : kind == kMid ? k_orth_mid<OP, TA, TB>
+                   : kind == kTwo ? k_orth<OP, TA, TB> : k_orth_wide<OP, TA, TB>;
+    // a launch holds 2^31 threads
+    const int64_t whole = n * g.tiles - plan.split, most = int64_t(1) << 22;
+    for (int64_t done = 0; done < whole; done += most) {
+        g.first = (int32_t)done;
+        g.all = (int32_t)(whole - done < most ? whole - done : most);
+        hipLaunchKernelGGL(k, dim3((unsigned)g.all), dim3(threads), 0, st, g);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
-        g.a += some * g.step_a;
-        g.b += some * g.step_b;
-        if (g.in) g.in += some * g.step_in;
-        if (g.lo) g.lo += some * g.step_in;
-        if (g.out) g.out += some * g.step_out;
-        if (g.diag_in) g.diag_in += some * g.step_diag;
-        if (g.diag_out) g.diag_out += some * g.step_diag;
-        if (g.o) g.o += some * g.step_o;
     }
-    return hipSuccess;
+    if (plan.split == 0) return hipSuccess;
+    g.first = (int32_t)whole;
+    g.all = (int32_t)plan.split;
+    hipLaunchKernelGGL((k_orth_split<OP, TA, TB>), dim3(kSplit), dim3(512), 0, st, g);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_orth_join<OP>), dim3(16 * (unsigned)g.all), dim3(64), 0, st, g);
+    return hipGetLastError();
+}
+template <int OP, bool TA, bool TB>
+static hipError_t product(const OrthArgs& g, int64_t n, hipStream_t st) {
+    return run<OP, TA, TB>(plan_of(n, g.P, g.Q, g.turns, OP != kUpdate), g, n, st);
 }
 
 static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t first, int64_t n, hipStream_t st) {
     const int64_t x_all = s.group * s.x, a_all = s.group * s.a;
     _Float16* hi[2] = {static_cast<_Float16*>(d.ws), static_cast<_Float16*>(d.ws) + x_all};
-    _Float16* const lo = hi[1] + x_all;
-    _Float16* const A = lo + x_all;
+    uint8_t* const lo = reinterpret_cast<uint8_t*>(hi[1] + x_all);
+    _Float16* const A = reinterpret_cast<_Float16*>(lo + x_all);
     _Float16* const B = A + a_all;
     float* const da = reinterpret_cast<float*>(B + a_all);
     float* const db = da + s.group * s.m;
     double* const parts = reinterpret_cast<double*>(db + s.group * s.m);
+    float* const part = reinterpret_cast<float*>(parts + s.group * kSquareParts);
     const bool tall = d.rows > d.cols;
 
     StartArgs b{};
@@ -573,6 +1125,7 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
         g.cb = (float)d.coefficients[3 * k + 1];
         g.cc = (float)d.coefficients[3 * k + 2];
         g.step_diag = s.m;
+        g.part = part;
         // A
         OrthArgs p = g;
         p.a = p.b = X;
@@ -614,7 +1167,7 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
         p.lo = lo;
         p.diag_in = db;
         p.by_column = tall;
-        p.low = d.steps - 1 - k <= 2 ? 1.0f / kLow : 0.0f;
+        p.low = d.steps - 1 - k <= 2;
         if (k + 1 < d.steps) {
             p.out = hi[(k + 1) & 1];
         } else {
