@@ -44,7 +44,7 @@ constexpr int kSide = 128;                  // all sides are padded to this, wit
 constexpr float kScale = 1024.0f, kScaleX = 4096.0f;
 constexpr int kSquareParts = 256;           // partial sums of squares of a matrix, at most
 
-enum OrthOp { kGram, kSquare, kUpdate };
+enum OrthOp { kGram, kSquare, kUpdate, kUpdateTall };        // of a matrix that is taller than wide
 
 // C[p, q] = sum_r A(p, r) B(q, r) for each matrix of a group.
 struct OrthArgs {
@@ -65,7 +65,6 @@ struct OrthArgs {
     uint8_t* lo;                             // update: X lo, in place, laid out as `in`
     float ca, cb, cc;
     bool low;                               // update: whether the diagonal meets lo too
-    bool by_column;                         // update: the diagonal goes by column
     uint16_t* o;                            // the last update's output and its size
     int64_t ld_o, step_o, rows, cols;
     float scale;
@@ -334,36 +333,37 @@ struct OrthEpilogue<kSquare> {
     }
 };
 
-// a X + (b A + c A A) X.
-template <>
-struct OrthEpilogue<kUpdate> {
+// a X + (b A + c A A) X, the diagonal by row; or X on the left of it, by column.
+template <bool TALL>
+struct UpdateEpilogue {
     static constexpr float kOnce = 1.0f / kScale;
     struct In {
         h8 hi;
         v2u lo;
-        float e;
+        float d;
     };
     const OrthArgs& g;
     const int64_t at;
     const float* from;
     uint16_t* o;
     const int n;                            // of the columns in the last step's output
-    float eq[8];
-    __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t q)
+    float dq[8];
+    __device__ __forceinline__ UpdateEpilogue(const OrthArgs& a, int64_t m, int64_t q)
         : g(a), at(m * a.step_in + q), from(a.diag_in + m * a.step_diag), o(a.o + m * a.step_o + q),
           n(a.cols - q >= 8 ? 8 : a.cols > q ? (int)(a.cols - q) : 0) {
-        if (g.by_column) load8_f(eq, from + q, 8);
+        if constexpr (TALL) load8_f(dq, from + q, 8);
     }
     __device__ __forceinline__ void load(In& r, int64_t p) const {
         r.hi = *reinterpret_cast<const h8*>(g.in + at + p * g.ld_in);
         r.lo = *reinterpret_cast<const v2u*>(g.lo + at + p * g.ld_in);
-        r.e = from[g.by_column ? 0 : p];
+        if constexpr (!TALL) r.d = from[p];
     }
     __device__ __forceinline__ void put(const In& r, int64_t p, float v[8]) const {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float h = (float)r.hi[k], x = joined(h, r.lo, k);
-            v[k] = fmaf(g.ca, x, fmaf(g.by_column ? eq[k] : r.e, g.low ? x : h, v[k] * kOnce));
+            // a x + d x, or a x + d hi
+            const float d = TALL ? dq[k] : r.d, h = (float)r.hi[k], x = joined(h, r.lo, k);
+            v[k] = fmaf(g.low ? g.ca + d : g.ca, x, fmaf(g.low ? 0.0f : d, h, v[k] * kOnce));
         }
         if (g.out) {
             h8 h;
@@ -378,6 +378,15 @@ struct OrthEpilogue<kUpdate> {
         }
     }
 };
+template <>
+struct OrthEpilogue<kUpdate> : UpdateEpilogue<false> {
+    using UpdateEpilogue<false>::UpdateEpilogue;
+};
+template <>
+struct OrthEpilogue<kUpdateTall> : UpdateEpilogue<true> {
+    using UpdateEpilogue<true>::UpdateEpilogue;
+};
+constexpr bool symmetric(int op) { return op < kUpdate; }
 
 // A wave's blocks, four times FQ at a time, through its part of LDS (64 rows of 16 FQ floats),
 // so that a lane has eight consecutive columns, the same in all its rows of a run. Blocks are
@@ -431,13 +440,13 @@ struct Finish {
                 v4f* const hi = reinterpret_cast<v4f*>(mine + kCols * o + 4 * ((2 * c + 1) ^ (o & kMask)));
                 float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
                 if (column(run) < g.Q && row(o) < g.P) epi[run].put(in[u], row(o), v);
-                if (OP != kUpdate && mirror) {
+                if (symmetric(OP) && mirror) {
                     *lo = v4f{v[0], v[1], v[2], v[3]};
                     *hi = v4f{v[4], v[5], v[6], v[7]};
                 }
                 if (run + 1 < RUNS) load(run + 1, u);
             }
-            if (OP != kUpdate && mirror && row(8 * r) < g.P) {
+            if (symmetric(OP) && mirror && row(8 * r) < g.P) {
 #pragma unroll 2
                 for (int j = lane >> 3; j < kCols; j += 8) {
                     float v[8];
@@ -476,7 +485,7 @@ __device__ __forceinline__ void clear(v4f (&acc)[FP][FQ]) {
 // there. A wave has 32 x 32.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     constexpr int H = 64, kTile = H * kBR, kSlot = 2 * kTile, kSlots = 4;
     __shared__ __attribute__((aligned(16))) _Float16 lds[2 * kSlots * kSlot];
     int tp, tq;
@@ -570,7 +579,7 @@ __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
 // one loading while one is multiplied. Two workgroups fit a compute unit.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     constexpr int H = 128, kTile = H * kBR;
     __shared__ __attribute__((aligned(16))) _Float16 lds[4 * kTile];
     int tp, tq;
@@ -624,7 +633,7 @@ __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
 // tile is here, one barrier before anyone reads it.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     constexpr int H = 128, kTile = H * kBR, kSlot = 2 * kTile, kSlots = 4;
     __shared__ __attribute__((aligned(16))) _Float16 lds[kSlots * kSlot];
     int tp, tq;
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
 // whose sums go to memory for k_orth_join, a wave's as they lie in its registers.
 template <int OP, bool TA, bool TB, bool WHOLE>
 __device__ __forceinline__ void wide_tile(const OrthArgs& g, int t, int first, int last, _Float16* lds, float* part) {
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     constexpr int H = 128, B = 256, kHalf = H * kBR;
     int tp, tq;
     const int64_t m = place<SYM>(g, t, &tp, &tq), p0 = (int64_t)tp * B, q0 = (int64_t)tq * B;
@@ -859,7 +868,7 @@ __global__ void __launch_bounds__(512) k_orth_split(const OrthArgs g) {
 template <int OP>
 __global__ void __launch_bounds__(64) k_orth_join(const OrthArgs g) {
     __shared__ __attribute__((aligned(16))) float lds[64 * 64];
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     constexpr int H = 128, B = 256;
     const int t = blockIdx.x >> 4, wave = blockIdx.x >> 1 & 7, half = blockIdx.x & 1;
     const int wp = (wave & 3) * 32, wq = (wave >> 2) * 64;
@@ -1051,7 +1060,7 @@ size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
 
 template <int OP, bool TA, bool TB>
 static hipError_t run(const OrthPlan& plan, OrthArgs g, int64_t n, hipStream_t st) {
-    constexpr bool SYM = OP != kUpdate;
+    constexpr bool SYM = symmetric(OP);
     const OrthKind kind = plan.kind;
     const int side = kind == kFew ? 64 : kind == kWide ? 256 : 128, threads = kind == kTwo ? 256 : 512;
     g.np = (int32_t)over(g.P, side);
@@ -1079,7 +1088,7 @@ static hipError_t run(const OrthPlan& plan, OrthArgs g, int64_t n, hipStream_t s
 }
 template <int OP, bool TA, bool TB>
 static hipError_t product(const OrthArgs& g, int64_t n, hipStream_t st) {
-    return run<OP, TA, TB>(plan_of(n, g.P, g.Q, g.turns, OP != kUpdate), g, n, st);
+    return run<OP, TA, TB>(plan_of(n, g.P, g.Q, g.turns, symmetric(OP)), g, n, st);
 }
 
 static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t first, int64_t n, hipStream_t st) {
@@ -1166,7 +1175,6 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
         p.step_in = p.step_out = s.x;
         p.lo = lo;
         p.diag_in = db;
-        p.by_column = tall;
         p.low = d.steps - 1 - k <= 2;
         if (k + 1 < d.steps) {
             p.out = hi[(k + 1) & 1];
@@ -1178,7 +1186,7 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
             p.cols = d.cols;
             p.scale = d.scale;
         }
-        e = tall ? product<kUpdate, false, false>(p, n, st) : product<kUpdate, false, true>(p, n, st);
+        e = tall ? product<kUpdateTall, false, false>(p, n, st) : product<kUpdate, false, true>(p, n, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
