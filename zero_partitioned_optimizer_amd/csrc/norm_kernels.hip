@@ -2,8 +2,13 @@
 //   forward   s = residual + x; y = (s - mean) rstd w + b
 //   gradient  h = (x - mean) rstd, g = dy w: dx = residual_grad + rstd (g - mean(g) - h mean(g h)),
 //             dw = [dw +] sum of dy h over the rows, db = [db +] sum of dy
-// Bound by HBM: each matrix is read or written once. A row stays in registers between its
-// sums and its outputs, eight columns to a lane and 16 bytes to a load.
+// Bound by HBM where rows are long: each matrix is read or written once. A row stays in
+// registers between its sums and its outputs, eight columns to a lane and 16 bytes to a load.
+// 8192 x 4096, bf16 rows added to an f32 stream, RMS: 77 us, 5.2 TB/s; back through it with the
+// stream's gradient in bf16 61 us, 5.5 TB/s, 4.8 of them the second launch. Rows of 768 in bf16
+// are bound by their instructions as much: 8192 of them forward 11.3 us, 4.5 TB/s, back 16.0 and
+// 3.2 (12.1 and 4 the two launches). Divisions, masks of columns that do not exist and 64-bit
+// products of addresses out of the loops were 3 of 19 us there, and of 45 at 2304 columns 7.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -15,6 +20,9 @@ template <bool F>
 __device__ __forceinline__ void load8(float v[8], const void* p, int64_t at, int n) {
     if constexpr (F) load8_f(v, static_cast<const float*>(p) + at, n);
     else load8_bf(v, static_cast<const uint16_t*>(p) + at, n);
+}
+__device__ __forceinline__ v4u load_once(const void* p) {
+    return __builtin_nontemporal_load(static_cast<const v4u_any*>(p));
 }
 template <bool F>
 __device__ __forceinline__ void store8(void* p, int64_t at, const float v[8], int n) {
@@ -34,10 +42,114 @@ __device__ __forceinline__ void weights8(float v[8], const uint16_t* w, int64_t 
     for (int k = 0; k < 8; ++k) v[k] = 1.0f;
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
+// Eight elements of a row as they lie in memory: asked for ahead of their use, converted then.
+// Inputs are read once and do not stay in the caches.
+template <bool F>
+struct Raw {
+    v4u lo, hi;
+    __device__ __forceinline__ void load(const void* base, int64_t at, int n) {
+        // zeros first: written behind a load of other lanes they would wait for it
+        lo = hi = v4u{0, 0, 0, 0};
+        if constexpr (F) {
+            const float* const p = static_cast<const float*>(base) + at;
+            if (n >= 8) {
+                lo = load_once(p);
+                hi = load_once(p + 4);
+            } else if (n > 0) {
 #pragma unroll
-    for (int m = 32; m > 0; m >>= 1) v += __shfl_xor(v, m);
-    return v;
+                for (int k = 0; k < 4; ++k) {
+                    if (k < n) lo[k] = __float_as_uint(p[k]);
+                    if (4 + k < n) hi[k] = __float_as_uint(p[4 + k]);
+                }
+            }
+        } else {
+            const uint16_t* const p = static_cast<const uint16_t*>(base) + at;
+            if (n >= 8) {
+                lo = load_once(p);
+            } else if (n > 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < n) lo[k >> 1] |= (uint32_t)p[k] << (16 * (k & 1));
+            }
+        }
+    }
+    __device__ __forceinline__ void set(const float v[8]) {
+        if constexpr (F) {
+            lo = v4u{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+            hi = v4u{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+        } else {
+            lo = v4u{bf_pack(v[0], v[1]), bf_pack(v[2], v[3]), bf_pack(v[4], v[5]), bf_pack(v[6], v[7])};
+        }
+    }
+    __device__ __forceinline__ void store(void* base, int64_t at, int n) const {
+        if constexpr (F) {
+            float* const p = static_cast<float*>(base) + at;
+            if (n >= 8) {
+                *reinterpret_cast<v4u_any*>(p) = lo;
+                *reinterpret_cast<v4u_any*>(p + 4) = hi;
+            } else if (n > 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k < n) p[k] = __uint_as_float(lo[k]);
+                    if (4 + k < n) p[4 + k] = __uint_as_float(hi[k]);
+                }
+            }
+        } else {
+            uint16_t* const p = static_cast<uint16_t*>(base) + at;
+            if (n >= 8) {
+                *reinterpret_cast<v4u_any*>(p) = lo;
+            } else if (n > 0) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < n) p[k] = (uint16_t)(lo[k >> 1] >> (16 * (k & 1)));
+            }
+        }
+    }
+    // What is made of it from here on is made anew.
+    __device__ __forceinline__ void keep() {
+        asm volatile("" : "+v"(lo));
+        if constexpr (F) asm volatile("" : "+v"(hi));
+    }
+    __device__ __forceinline__ void get(float v[8]) const {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[F ? k : 2 * k] = F ? __uint_as_float(lo[k]) : bf_lo(lo[k]);
+            v[F ? 4 + k : 2 * k + 1] = F ? __uint_as_float(hi[k]) : bf_hi(lo[k]);
+        }
+    }
+};
+// Eight of a norm's bf16 weights (`none`: what their halves are without any), kept as they are.
+struct RawWeights {
+    v4u w;
+    __device__ __forceinline__ void load(const uint16_t* p, int64_t j, int n, uint32_t none) {
+        w = v4u{none, none, none, none};
+        if (!p || n <= 0) return;
+        if (n >= 8) {
+            w = *reinterpret_cast<const v4u_any*>(p + j);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) w[k >> 1] = (w[k >> 1] & (k & 1 ? 0xFFFFu : 0xFFFF0000u)) | (uint32_t)p[j + k] << (16 * (k & 1));
+        }
+    }
+    __device__ __forceinline__ float get(int k) const { return k & 1 ? bf_hi(w[k >> 1]) : bf_lo(w[k >> 1]); }
+};
+constexpr uint32_t kOnes = 0x3F803F80u;
+
+template <int CONTROL>
+__device__ __forceinline__ float add_across(float v) {
+    return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(v), CONTROL, 0xF, 0xF, true));
+}
+__device__ __forceinline__ float lane_of(float v, int lane) {
+    return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(v), lane));
+}
+// The same in all lanes: 16 lanes' sums by exchanges within them, then the four.
+__device__ __forceinline__ float wave_sum(float v) {
+    v = add_across<0xB1>(v);            // lanes 1, 0, 3, 2 of four
+    v = add_across<0x4E>(v);            // 2, 3, 0, 1
+    v = add_across<0x141>(v);           // mirrored in eight
+    v = add_across<0x140>(v);           // and in sixteen
+    return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 // Sums over the W waves that share a row; `part` is W floats of LDS that nothing else has
 // used since the last barrier but one.
@@ -84,46 +196,94 @@ __device__ __forceinline__ void norm8(const float v[8], const NormDesc& d, float
     store8<YF>(d.y, row * d.ld_y + j, y, n);
 }
 
-// W waves to a row of at most 512 W C columns, held in registers.
+// W waves to a row of at most 512 W C columns, held in registers; one or (W = 1) four rows to a
+// workgroup at a time, which takes every `stride`-th group of them and asks for the next row
+// before it works on one. Loads that stay in the caches: 8192 x 2304 33.6 in place of 29.2 us.
 template <bool XF, bool SF, bool YF, int W, int C>
-__global__ void __launch_bounds__(kNormBlock) k_norm(const NormDesc d, int64_t first) {
-    __shared__ float part[2][4];
+__global__ void __launch_bounds__(W > 4 ? 512 : kNormBlock) k_norm(const NormDesc d, int64_t stride) {
+    constexpr int G = W == 1 ? 4 : 1;
+    __shared__ float part[2][2][W];
     const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
-    const int64_t row = first + (W == 1 ? (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6) : blockIdx.x);
+    int64_t row = (int64_t)blockIdx.x * G + (W == 1 ? threadIdx.x >> 6 : 0);
     if (row >= d.M) return;
-    float v[C][8], sum = 0.0f, sq = 0.0f, mean = 0.0f;
+    int j[C], n[C];
+    RawWeights w[C], b[C];
+    Raw<XF> x[C];
+    Raw<SF> r[C];
+    const auto ask = [&](int64_t at) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int64_t j = 8 * (t + 64 * W * i);
-        const int n = valid8(d.N, j);
-        sum8<XF, SF>(v[i], d, row, j, n);
-    }
-    if (!d.rms) {
-#pragma unroll
-        for (int i = 0; i < C; ++i)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) sum += v[i][k];
-        mean = row_sum<W>(sum, part[0]) / (float)d.N;
-    }
-#pragma unroll
-    for (int i = 0; i < C; ++i) {
-        const int n = valid8(d.N, 8 * (t + 64 * W * i));
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float e = k < n ? v[i][k] - mean : 0.0f;
-            sq = fmaf(e, e, sq);
+        for (int i = 0; i < C; ++i) {
+            x[i].load(d.x, at * d.ld_x + j[i], n[i]);
+            if (d.res) r[i].load(d.res, at * d.ld_res + j[i], n[i]);
         }
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<W>(sq, part[1]) / (float)d.N + d.eps);
-    if (d.stats && t == 0) {
-        d.stats[2 * row] = mean;
-        d.stats[2 * row + 1] = rstd;
-    }
+    };
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t j = 8 * (t + 64 * W * i);
-        const int n = valid8(d.N, j);
-        if (n > 0) norm8<YF>(v[i], d, mean, rstd, row, j, n);
+        j[i] = 8 * (t + 64 * W * i);
+        n[i] = valid8(d.N, j[i]);
+    }
+    ask(row);
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        w[i].load(d.w, j[i], n[i], kOnes);
+        b[i].load(d.b, j[i], n[i], 0);
+    }
+    int turn = 0;
+#pragma unroll 1
+    for (;; turn ^= 1) {
+        float v[C][8], sum = 0.0f, sq = 0.0f, mean = 0.0f;
+        Raw<SF> s[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            x[i].get(v[i]);
+            if (d.res) {
+                float add[8];
+                r[i].get(add);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[i][k] += add[k];
+                s[i].set(v[i]);
+                if constexpr (!SF) s[i].get(v[i]);          // what is stored is what is normed
+            }
+        }
+        const int64_t next = row + stride * G;
+        if (next < d.M) ask(next);
+        if (d.res)
+#pragma unroll
+            for (int i = 0; i < C; ++i) s[i].store(d.sum, row * d.ld_sum + j[i], n[i]);
+        if (!d.rms) {
+#pragma unroll
+            for (int i = 0; i < C; ++i)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += v[i][k];
+            mean = row_sum<W>(sum, part[turn][0]) / (float)d.N;
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            const float m = n[i] > 0 ? mean : 0.0f;         // of no column: zeros, and 0 to the sum
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] -= m;
+            if (n[i] > 0 && n[i] < 8)
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k >= n[i]) v[i][k] = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) sq = fmaf(v[i][k], v[i][k], sq);
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<W>(sq, part[turn][1]) / (float)d.N + d.eps);
+        if (d.stats && t == 0) {
+            d.stats[2 * row] = mean;
+            d.stats[2 * row + 1] = rstd;
+        }
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * rstd * w[i].get(k) + b[i].get(k);
+            Raw<YF> y;
+            y.set(v[i]);
+            y.store(d.y, row * d.ld_y + j[i], n[i]);
+        }
+        if (next >= d.M) return;
+        row = next;
     }
 }
 
@@ -166,24 +326,30 @@ __global__ void __launch_bounds__(kNormBlock) k_norm_long(const NormDesc d, int6
 
 template <bool XF, bool SF, bool YF>
 static hipError_t norm_typed(const NormDesc& d, hipStream_t st) {
-    const bool one = d.N <= 1024;                       // a wave to a row, four rows to a workgroup
+    if (d.N > 16384) {
+        // a launch's threads are counted in 32 bits
+        constexpr int64_t kLaunch = (int64_t(1) << 31) / kNormBlock;
+        for (int64_t done = 0; done < d.M; done += kLaunch) {
+            const unsigned blocks = (unsigned)(d.M - done < kLaunch ? d.M - done : kLaunch);
+            hipLaunchKernelGGL((k_norm_long<XF, SF, YF>), dim3(blocks), dim3(kNormBlock), 0, st, d, done);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess) return e;
+        }
+        return hipSuccess;
+    }
+    const int W = d.N <= 1024 ? 1 : d.N <= 4096 ? 4 : 8;
     const auto k = d.N <= 512     ? k_norm<XF, SF, YF, 1, 1>
                    : d.N <= 1024  ? k_norm<XF, SF, YF, 1, 2>
                    : d.N <= 2048  ? k_norm<XF, SF, YF, 4, 1>
                    : d.N <= 4096  ? k_norm<XF, SF, YF, 4, 2>
-                   : d.N <= 8192  ? k_norm<XF, SF, YF, 4, 4>
-                   : d.N <= 16384 ? k_norm<XF, SF, YF, 4, 8>
-                                  : k_norm_long<XF, SF, YF>;
-    const int64_t rows = one ? 4 : 1, all = (d.M + rows - 1) / rows;
-    // a launch's threads are counted in 32 bits
-    constexpr int64_t kLaunch = (int64_t(1) << 31) / kNormBlock;
-    for (int64_t done = 0; done < all; done += kLaunch) {
-        const unsigned blocks = (unsigned)(all - done < kLaunch ? all - done : kLaunch);
-        hipLaunchKernelGGL(k, dim3(blocks), dim3(kNormBlock), 0, st, d, done * rows);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-    }
-    return hipSuccess;
+                   : d.N <= 8192  ? k_norm<XF, SF, YF, 8, 2>
+                   : d.N <= 12288 ? k_norm<XF, SF, YF, 8, 3>
+                                  : k_norm<XF, SF, YF, 8, 4>;
+    // sixteen waves to a compute unit, which then take rows in turn
+    const int64_t groups = W == 1 ? (d.M + 3) / 4 : d.M, most = W == 8 ? 512 : 1024;
+    const int64_t blocks = groups < most ? groups : most;
+    hipLaunchKernelGGL(k, dim3((unsigned)blocks), dim3(W == 8 ? 512 : kNormBlock), 0, st, d, blocks);
+    return hipGetLastError();
 }
 
 hipError_t launch_norm(const NormDesc& d, hipStream_t st) {
@@ -203,10 +369,16 @@ constexpr int kGradBlock = 512, kGradWaves = kGradBlock / 64;
 
 // Workgroups of a gradient by M rows of N columns, each of which leaves a row of partial
 // sums for the weight and one for the bias.
-static int64_t grad_rows(int64_t N) { return N <= 1024 ? kGradWaves : 1; }       // at a time
+// k_norm_grad's waves: as many as its registers leave room for.
+template <int C>
+constexpr int kRowWaves = C == 1 ? 16 : 8;
+static int grad_waves(int64_t N) {          // to a row
+    return N <= 512 ? 1 : N <= 1024 ? 2 : N <= 2048 ? 4 : N <= 4096 || N > 8192 ? 8 : 16;
+}
+static int64_t grad_rows(int64_t N) { return N <= 8192 ? 16 / grad_waves(N) : 1; }      // at a time
 static int64_t grad_blocks(int64_t M, int64_t N) {
     const int64_t need = (M + grad_rows(N) - 1) / grad_rows(N);
-    return need < 512 ? need : 512;
+    return need < 256 ? need : 256;
 }
 static int64_t up8(int64_t n) { return (n + 7) / 8 * 8; }
 
@@ -239,62 +411,139 @@ __device__ __forceinline__ void put_dx8(const float g[8], const float h[8], cons
     store8<OF>(d.dx, row * d.ld_dx + j, o, n);
 }
 
-// W waves to a row of at most 512 W C columns; a workgroup takes every parts-th group of
-// 8 / W rows and keeps the columns' sums in registers.
+// W waves to a row of at most 512 W C columns; a workgroup takes every parts-th group of G
+// rows and keeps the columns' sums in registers. The next rows' loads are under way while
+// the sums of one are made, if C = 1 and at most one matrix is f32. Of C = 3 a row stays as it was loaded between its sums and dx,
+// half the registers where it is bf16.
 template <bool DF, bool XF, bool OF, int W, int C>
-__global__ void __launch_bounds__(kGradBlock) k_norm_grad(const NormGradArgs a) {
-    constexpr int G = kGradWaves / W, kCols = 512 * W * C;
-    __shared__ float part[2][2][kGradWaves];
+__global__ void __launch_bounds__(64 * kRowWaves<C>) k_norm_grad(const NormGradArgs a) {
+    constexpr int G = kRowWaves<C> / W, kCols = 512 * W * C;
+    constexpr bool kAhead = C == 1 && DF + XF + OF < 2;
+    __shared__ float part[2][G][W][2];
     __shared__ float cols[G > 1 ? G * kCols : 1];
     const NormGradDesc& d = a.d;
-    const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x, group = W == 1 ? threadIdx.x >> 6 : 0;
-    float w[C][8], aw[C][8], ab[C][8];
+    const int t = threadIdx.x % (64 * W), group = threadIdx.x / (64 * W);
+    float aw[C][8], ab[C][8];
+    int j[C], n[C];
+    RawWeights w[C];
+    Raw<DF> dy[C];
+    Raw<XF> x[C];
+    Raw<OF> res[C];
+    float mean = 0.0f, rstd = 0.0f;
+    const int64_t stride = a.parts * G;
+    int64_t base = (int64_t)blockIdx.x * G;
+    // where the next row's loads and this one's stores go, advanced instead of multiplied anew
+    const int64_t row0 = base + group;
+    int64_t at_dy = row0 * d.ld_dy, at_x = row0 * d.ld_x, at_res = row0 * d.ld_res, at_dx = row0 * d.ld_dx, at_stats = 2 * row0;
+    const auto ask = [&](bool on) {
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            dy[i].load(d.dy, at_dy + j[i], on ? n[i] : 0);
+            x[i].load(d.x, at_x + j[i], on ? n[i] : 0);
+            if (d.res) res[i].load(d.res, at_res + j[i], on ? n[i] : 0);
+        }
+        mean = on ? d.stats[at_stats] : 0.0f;
+        rstd = on ? d.stats[at_stats + 1] : 0.0f;
+        at_dy += stride * d.ld_dy;
+        at_x += stride * d.ld_x;
+        at_res += stride * d.ld_res;
+        at_stats += 2 * stride;
+    };
 #pragma unroll
     for (int i = 0; i < C; ++i) {
-        const int64_t j = 8 * (t + 64 * W * i);
-        weights8(w[i], d.w, j, valid8(d.N, j));
+        j[i] = 8 * (t + 64 * W * i);
+        n[i] = valid8(d.N, j[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) aw[i][k] = ab[i][k] = 0.0f;
     }
+    if (kAhead) ask(row0 < d.M);
+#pragma unroll
+    for (int i = 0; i < C; ++i) w[i].load(d.w, j[i], n[i], kOnes);
+    const float per_n = 1.0f / (float)d.N;
     int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * G + group; row < d.M; row += a.parts * G, turn ^= 1) {
-        const float mean = d.stats[2 * row], rstd = d.stats[2 * row + 1];
-        float g[C][8], h[C][8], sg = 0.0f, sgh = 0.0f;
+    // the same turns for all waves: the last rows may be there for some groups only. Columns
+    // that do not exist have dy 0, and so add nothing to the sums whatever h is there.
+#pragma unroll 1
+    for (; base < d.M; base += stride, turn ^= 1) {
+        const int64_t row = base + group;
+        if (!kAhead) ask(row < d.M);
+        float sg = 0.0f, sgh = 0.0f;
+        const float r = rstd, m = mean;
+        Raw<DF> dy0[C];
+        Raw<XF> x0[C];
+        Raw<OF> add0[C];
+        float g[8], h[8];
+        const auto row8 = [&](int i) {          // dy w and h of a chunk
+            dy0[i].get(g);
+            x0[i].get(h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) h[k] = (h[k] - m) * r;
+        };
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int64_t j = 8 * (t + 64 * W * i);
-            grad8<DF, XF>(g[i], h[i], d, mean, rstd, row, j, valid8(d.N, j));
-        }
-#pragma unroll
-        for (int i = 0; i < C; ++i)
+            dy0[i] = dy[i];
+            x0[i] = x[i];
+            if (d.res) add0[i] = res[i];
+            row8(i);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                aw[i][k] = fmaf(g[i][k], h[i][k], aw[i][k]);
-                ab[i][k] += g[i][k];
-                g[i][k] *= w[i][k];
-                sg += g[i][k];
-                sgh = fmaf(g[i][k], h[i][k], sgh);
+                aw[i][k] = fmaf(g[k], h[k], aw[i][k]);
+                ab[i][k] += g[k];
+                g[k] *= w[i].get(k);
+                sg += g[k];
+                sgh = fmaf(g[k], h[k], sgh);
             }
-        sg = d.rms ? 0.0f : row_sum<W>(sg, part[turn][0]) / (float)d.N;
-        sgh = row_sum<W>(sgh, part[turn][1]) / (float)d.N;
+            if (C > 1) {
+                dy0[i].keep();
+                x0[i].keep();
+            }
+        }
+        if (kAhead) ask(row + stride < d.M);
+        sg = wave_sum(sg);
+        sgh = wave_sum(sgh);
+        if constexpr (W > 1) {
+            float(*const at)[2] = part[turn][group];
+            if ((t & 63) == 0) {
+                at[t >> 6][0] = sg;
+                at[t >> 6][1] = sgh;
+            }
+            __syncthreads();
+            sg = at[0][0];
+            sgh = at[0][1];
+#pragma unroll
+            for (int q = 1; q < W; ++q) {
+                sg += at[q][0];
+                sgh += at[q][1];
+            }
+        }
+        sg = d.rms ? 0.0f : sg * per_n;
+        sgh *= per_n;
 #pragma unroll
         for (int i = 0; i < C; ++i) {
-            const int64_t j = 8 * (t + 64 * W * i);
-            const int n = valid8(d.N, j);
-            if (n > 0) put_dx8<OF>(g[i], h[i], d, sg, sgh, rstd, row, j, n);
+            if (C > 1) {
+                row8(i);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) g[k] *= w[i].get(k);
+            }
+            float add[8];
+            if (d.res) add0[i].get(add);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) g[k] = fmaf(r, fmaf(-h[k], sgh, g[k] - sg), d.res ? add[k] : 0.0f);
+            Raw<OF> out;
+            out.set(g);
+            out.store(d.dx, at_dx + j[i], row < d.M ? n[i] : 0);
         }
+        at_dx += stride * d.ld_dx;
     }
     if (!a.part) return;
     float* const out = a.part + (int64_t)blockIdx.x * 2 * a.ld_part;
     if constexpr (G == 1) {
 #pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const int64_t j = 8 * (t + 64 * W * i);
-            if (j < d.N) {
-                store8_f(out + j, aw[i], 8);
-                store8_f(out + a.ld_part + j, ab[i], 8);
+        for (int i = 0; i < C; ++i)
+            if (j[i] < d.N) {
+                store8_f(out + j[i], aw[i], 8);
+                store8_f(out + a.ld_part + j[i], ab[i], 8);
             }
-        }
     } else {
         // the groups' sums in LDS, joined in order
 #pragma unroll
@@ -304,11 +553,11 @@ __global__ void __launch_bounds__(kGradBlock) k_norm_grad(const NormGradArgs a) 
             for (int i = 0; i < C; ++i)
                 store8_f(cols + group * kCols + 8 * (t + 64 * W * i), s ? ab[i] : aw[i], 8);
             __syncthreads();
-            for (int j = threadIdx.x; j < kCols && j < d.N; j += kGradBlock) {
-                float v = cols[j];
+            for (int at = threadIdx.x; at < kCols && at < d.N; at += 64 * kRowWaves<C>) {
+                float v = cols[at];
 #pragma unroll
-                for (int q = 1; q < G; ++q) v += cols[q * kCols + j];
-                out[s * a.ld_part + j] = v;
+                for (int q = 1; q < G; ++q) v += cols[q * kCols + at];
+                out[s * a.ld_part + at] = v;
             }
         }
     }
@@ -414,7 +663,8 @@ size_t norm_ws_bytes(int64_t M, int64_t N) {
 template <bool DF, bool XF, bool OF>
 static hipError_t grad_typed(const NormGradArgs& a, hipStream_t st) {
     const NormGradDesc& d = a.d;
-    if (d.N > 16384) {
+    // more chunks to a lane than three, or three of f32, spill
+    if (d.N > (DF + XF + OF < 2 ? 12288 : 8192)) {
         constexpr int64_t kLaunch = (int64_t(1) << 31) / kGradBlock;
         // before dx, which may be written over dy or x
         if (a.part) {
@@ -432,11 +682,12 @@ static hipError_t grad_typed(const NormGradArgs& a, hipStream_t st) {
         return hipSuccess;
     }
     const auto k = d.N <= 512    ? k_norm_grad<DF, XF, OF, 1, 1>
-                   : d.N <= 1024 ? k_norm_grad<DF, XF, OF, 1, 2>
+                   : d.N <= 1024 ? k_norm_grad<DF, XF, OF, 2, 1>
+                   : d.N <= 2048 ? k_norm_grad<DF, XF, OF, 4, 1>
                    : d.N <= 4096 ? k_norm_grad<DF, XF, OF, 8, 1>
-                   : d.N <= 8192 ? k_norm_grad<DF, XF, OF, 8, 2>
-                                 : k_norm_grad<DF, XF, OF, 8, 4>;
-    hipLaunchKernelGGL(k, dim3((unsigned)a.parts), dim3(kGradBlock), 0, st, a);
+                   : d.N <= 8192 ? k_norm_grad<DF, XF, OF, 16, 1>
+                                 : k_norm_grad<DF, XF, OF, 8, DF + XF + OF < 2 ? 3 : 1>;      // or not reached
+    hipLaunchKernelGGL(k, dim3((unsigned)a.parts), dim3(d.N <= 8192 ? 1024 : 512), 0, st, a);
     return hipGetLastError();
 }
 
