@@ -28,7 +28,7 @@ from ._binding import (  # noqa: F401
     zero_state_set_floats, zero_state_pack, zero_state_unpack, zero_device_state_flush,
     ZeroRecordError, ZERO_RECORD_OK, ZERO_RECORD_E_COLLECT, ZERO_RECORD_E_MARKS,
     zero_adam_step_noalloc, ZERO_NOALLOC_SCRATCH_BYTES)
-from .shard_step import DeviceShardStep, OffloadShardStep, ShardStep  # noqa: F401
+from .shard_step import DeviceShardStep, MuonShardStep, OffloadShardStep, ShardStep  # noqa: F401
 from .layer import (  # noqa: F401
     ZERO_ACT_GELU, ZERO_ACT_NONE, ZERO_ACT_RELU, ZERO_ACT_SILU, ZERO_LINEAR_FORWARD, ZERO_LINEAR_GRAD_INPUT,
     ZERO_LINEAR_GRAD_WEIGHT, ZERO_NORM_LAYER, ZERO_NORM_RMS, ZERO_W_IN_OUT, ZERO_W_OUT_IN, FlatLinear, FlatNorm,

@@ -17,11 +17,13 @@ precision is named in "ZeRO Optimizer", "Hybrid Approaches".
 from __future__ import annotations
 
 import ctypes
-from typing import Optional, Sequence
+import math
+from typing import Callable, Optional, Sequence
 
 import torch
 
 from . import _binding as B
+from . import muon
 
 
 class ShardStep:
@@ -437,3 +439,170 @@ class OffloadShardStep:
         self.state.loss_scale, self.state.min_loss_scale = sd["loss_scale"], sd["min_loss_scale"]
         self.state.dynamic = sd["dynamic"]
         self._recast_slot()
+
+
+class MuonShardStep:
+    """The step of a flat buffer that holds matrices by an orthogonalised momentum
+    (``zero_muon.h``): fold the replicas, update the shard's momentum, orthogonalise the
+    whole matrices that meet the shard, update the shard's master copy and slot.
+
+    ``matrices``: (offset, rows, cols) of each in the flat buffer, row-major; the shard is
+    its elements [shard_off, shard_off + shard_S). Matrices of one shape at even distances
+    are orthogonalised in one call. Elements of the shard outside every matrix have no
+    update, only their weight decay.
+
+    A step has three parts, with the program's collectives between them:
+      ``reduce(replicas)``  the averaged gradient and the overflow record ``stats``. Ranks
+                            agree on the record here (overflow: largest, sum of squares: sum),
+                            before anything is written.
+      ``momentum()``        the momentum and this shard's part of ``u`` (bf16, the flat
+                            elements from ``u_off`` on). The parts of matrices that shards
+                            cut are brought into ``u`` here, by an all-gather.
+      ``update()``          the orthogonal forms, the master copy and the slot.
+    ``step`` runs them, with ``agree(stats)`` and ``exchange(u)`` between, and commits. Without
+    an exchange the shard's matrices have to lie in it whole.
+
+    ``scale(rows, cols)`` is what a matrix's orthogonal form is multiplied by; by default 0.2
+    times the root of the larger side, which gives updates the root mean square of Adam's.
+    On overflow nothing is written, on the device; the host keeps the loss scale, as
+    ``ShardStep`` does."""
+
+    def __init__(self, shard_S: int, n_replicas: int, grad_dtype: int, p0: torch.Tensor, matrices, *, lr: float,
+                 shard_off: int = 0, mu: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, steps: int = 5,
+                 coefficients=muon.ZERO_MUON_COEFFICIENTS, eps: float = 1e-7,
+                 scale: Optional[Callable[[int, int], float]] = None, loss_scale: float = 1.0, dynamic: bool = False,
+                 min_loss_scale: float = 1.0, slot: Optional[torch.Tensor] = None):
+        dev = p0.device
+        S, lo = int(shard_S), int(shard_off)
+        assert p0.dtype == torch.float32 and p0.numel() == S and p0.is_contiguous()
+        self.S, self.N, self.grad_dtype = S, int(n_replicas), int(grad_dtype)
+        self.hyper = dict(lr=lr, weight_decay=weight_decay)
+        self.momentum_hyper = dict(mu=mu, nesterov=nesterov)
+        self.orth = dict(steps=steps, coefficients=coefficients, eps=eps)
+        here = sorted((int(o), int(r), int(c)) for o, r, c in matrices if o < lo + S and o + r * c > lo and r * c > 0)
+        for (a, r, c), (b, _, _) in zip(here, here[1:]):
+            if a + r * c > b:
+                raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: matrices at {a} and {b} overlap")
+        if here and here[0][0] < 0:
+            raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a matrix at {here[0][0]}")
+        self.u_off = min([lo] + [o for o, _, _ in here])
+        end = max([lo + S] + [o + r * c for o, r, c in here])
+        self.whole = self.u_off == lo and end == lo + S
+        self.p = p0.clone()
+        self.m = torch.zeros_like(p0)
+        self.g = torch.empty_like(p0)
+        # zeros: what no matrix holds is never updated
+        self.u = torch.zeros(end - self.u_off, dtype=torch.bfloat16, device=dev)
+        self.o = torch.zeros_like(self.u)
+        at = lo - self.u_off
+        self.u_shard, self.o_shard = self.u[at:at + S], self.o[at:at + S]
+        if scale is None:
+            def scale(rows, cols):
+                return 0.2 * math.sqrt(max(rows, cols))
+        self.stacks = []
+        for n, first, every, r, c in self._stacks(here):
+            def view(flat):
+                return flat.as_strided((n, r, c), (every, c, 1), first - self.u_off)
+            self.stacks.append((view(self.u), view(self.o), float(scale(r, c))))
+        need = max([muon.zero_orthogonalize_workspace_bytes(*u.shape) for u, _, _ in self.stacks] + [16])
+        self.orth_ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        self.slot = slot if slot is not None else torch.empty(S, dtype=torch.int16, device=dev)
+        assert self.slot.numel() == S and self.slot.element_size() == 2
+        self.stats = torch.zeros(16, dtype=torch.uint8, device=dev)
+        self.stats_host = torch.zeros(16, dtype=torch.uint8, pin_memory=True)
+        self.ws = torch.empty(B.zero_workspace_bytes(S), dtype=torch.uint8, device=dev)
+        self.state = B.zero_train_state(t=0, n_skipped=0, loss_scale=float(loss_scale),
+                                        min_loss_scale=float(min_loss_scale), dynamic=int(dynamic))
+        B.zero_gather_slot(self.p, S, self.slot)
+
+    @staticmethod
+    def _stacks(here):
+        """(count, first offset, distance, rows, cols) of runs of equal shape and distance."""
+        shapes: dict = {}
+        for o, r, c in here:
+            shapes.setdefault((r, c), []).append(o)
+        out = []
+        for (r, c), offs in shapes.items():
+            k = 0
+            while k < len(offs):
+                n, every = 1, r * c
+                if k + 1 < len(offs):
+                    every = offs[k + 1] - offs[k]
+                    while k + n < len(offs) and offs[k + n] - offs[k + n - 1] == every:
+                        n += 1
+                out.append((n, offs[k], every, r, c))
+                k += n
+        return out
+
+    @property
+    def master(self) -> torch.Tensor:
+        return self.p
+
+    @property
+    def t(self) -> int:
+        return int(self.state.t)
+
+    @property
+    def loss_scale(self) -> float:
+        return float(self.state.loss_scale)
+
+    def reduce(self, replicas: Sequence[torch.Tensor], stream=None) -> None:
+        """Enqueue the first part: the averaged gradient and its record."""
+        if len(replicas) != self.N:
+            raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: {len(replicas)} replicas, not {self.N}")
+        B.zero_reduce_shard(replicas, self.grad_dtype, self.S, self.stats, self.ws, loss_scale=self.state.loss_scale,
+                            grad_out=self.g, stream=stream)
+
+    def momentum(self, stream=None) -> None:
+        """Enqueue the second part: the momentum and this shard's part of u, unless the record overflowed."""
+        muon.zero_muon_momentum(self.g, self.m, u=self.u_shard, stats=self.stats, stream=stream, **self.momentum_hyper)
+
+    def update(self, stream=None) -> None:
+        """Enqueue the third part, once all of u is there."""
+        for u, o, scale in self.stacks:
+            muon.zero_orthogonalize(u, out=o, scale=scale, workspace=self.orth_ws, stream=stream, **self.orth)
+        muon.zero_muon_update(self.p, self.o_shard, slot=self.slot, stats=self.stats, stream=stream, **self.hyper)
+
+    def read_stats(self, stream=None) -> B.zero_stats:
+        st = stream or torch.cuda.current_stream()
+        with torch.cuda.stream(st):
+            self.stats_host.copy_(self.stats, non_blocking=True)
+        st.synchronize()
+        return B.zero_stats.from_buffer_copy(self.stats_host.numpy().tobytes())
+
+    def commit(self, st: B.zero_stats) -> int:
+        """Count the step and keep the loss scale; a skipped one has written nothing."""
+        return B.zero_commit_rule(self.state, st)
+
+    def step(self, replicas: Sequence[torch.Tensor], agree=None, exchange=None, stream=None):
+        """One full step; ``agree`` and ``exchange`` run with ``stream`` current. Returns (stats,
+        ZERO_COMMIT or ZERO_SKIP)."""
+        if exchange is None and not self.whole:
+            raise B.ZeroError(B.ZERO_E_INVAL, "MuonShardStep: shards cut matrices: step needs an exchange")
+        stream = stream or torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            self.reduce(replicas, stream)
+            if agree is not None:
+                agree(self.stats)
+            self.momentum(stream)
+            if exchange is not None:
+                exchange(self.u)
+            self.update(stream)
+            st = self.read_stats(stream)
+        return st, self.commit(st)
+
+    def state_dict(self) -> dict:
+        """The state on the host: master copy, momentum and the commit record."""
+        st = self.state
+        return {"p": self.p.cpu(), "m": self.m.cpu(), "t": int(st.t), "n_skipped": int(st.n_skipped),
+                "loss_scale": float(st.loss_scale), "min_loss_scale": float(st.min_loss_scale),
+                "dynamic": int(st.dynamic)}
+
+    def load_state_dict(self, sd: dict) -> None:
+        """Resume from ``state_dict()``."""
+        for dst, key in ((self.p, "p"), (self.m, "m")):
+            assert sd[key].numel() == self.S and sd[key].dtype == torch.float32
+            dst.copy_(sd[key])
+        self.state = B.zero_train_state(t=sd["t"], n_skipped=sd["n_skipped"], loss_scale=sd["loss_scale"],
+                                        min_loss_scale=sd["min_loss_scale"], dynamic=sd["dynamic"])
+        B.zero_gather_slot(self.p, self.S, self.slot)
