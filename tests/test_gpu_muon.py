@@ -167,7 +167,7 @@ def test_empty(Z):
 # by the products' tiles: 64 wide, 128 in each of their two kinds, 256 whole, split, and whole
 # and split together, of wide and tall matrices
 @pytest.mark.parametrize("size", [(1, 4096, 1000), (2, 1100, 2304), (1, 640, 11008), (30, 256, 512), (40, 700, 500),
-                                  (1, 4096, 4096), (1, 2500, 9000), (1, 9000, 2500), (4, 2304, 4096), (3, 5000, 2304), (4, 4096, 4096)],
+                                  (1, 4096, 4096), (1, 2500, 9000), (1, 9000, 2500), (4, 2304, 4096), (3, 5000, 2304), (4, 4096, 4096), (4, 4096, 2304)],
                          ids=str)
 def test_large(Z, size):
     """Sizes of many tiles, where the fp64 formula runs on the device: the norm of the error is

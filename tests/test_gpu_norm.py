@@ -344,3 +344,24 @@ def test_refuses(Z):
         say("refused for", word)
         with pytest.raises(Z.ZeroError, match=word):
             call()
+
+
+@pytest.mark.parametrize("N", [12, 100, 1000])
+def test_grad_of_a_row_far_from_zero(Z, N):
+    """Equal elements so large that mean times 1/sigma passes fp32: h is 0 in every column, and
+    the columns behind the last add nothing (not 0 times an infinity). The norm of a row of
+    2^118 is exact, and so 1/sigma is eps^-1/2; dx is rstd (dy - mean(dy)) in fp32 with at
+    most 2 N + 8 roundings of 2^-24 of at most max |dy| each, before bf16's."""
+    M = 5
+    dy = torch.randn(M, N, generator=torch.Generator().manual_seed(N)).to(dev()).bfloat16()
+    x = torch.full((M, N), 2.0 ** 118, device=dev())
+    say("far from zero", N)
+    y, stats = Z.zero_norm_forward(x, kind=Z.ZERO_NORM_LAYER, eps=1e-12, stats=True)
+    assert bool((y == 0).all()) and bool((stats[:, 0] == 2.0 ** 118).all())
+    for xt in (x, x.bfloat16()):
+        dw, db = (torch.zeros(N, device=dev()) for _ in range(2))
+        dx = Z.zero_norm_grad(dy, xt, None, stats, kind=Z.ZERO_NORM_LAYER, dtype=torch.float32, dweight=dw, dbias=db)
+        want = 1e6 * (dy.double() - dy.double().mean(1, keepdim=True))
+        assert float((dx.double() - want).abs().max()) <= 1e6 * (2 * N + 8) * 2.0 ** -24 * float(dy.double().abs().max())
+        assert bool((dw == 0).all())
+        assert float((db.double() - dy.double().sum(0)).abs().max()) <= 8 * M * 2.0 ** -24 * float(dy.double().abs().max())

@@ -155,6 +155,7 @@ def test_binding_refuses():
         with pytest.raises(Z.ZeroError, match="neither three numbers nor 5 triples"):
             M._table(M._coefficients(bad), 5)
     assert list(M._table(M._coefficients([(1, 2, 3), (4, 5, 6)]), 2)) == [1, 2, 3, 4, 5, 6]
+    assert list(M._table(M._coefficients(np.arange(1, 7).reshape(2, 3)), 2)) == [1, 2, 3, 4, 5, 6]
     assert list(M._table(R.COEF, 2)) == list(R.COEF) * 2
 
 

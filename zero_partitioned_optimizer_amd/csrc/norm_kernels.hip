@@ -367,8 +367,6 @@ hipError_t launch_norm(const NormDesc& d, hipStream_t st) {
 
 constexpr int kGradBlock = 512, kGradWaves = kGradBlock / 64;
 
-// Workgroups of a gradient by M rows of N columns, each of which leaves a row of partial
-// sums for the weight and one for the bias.
 // k_norm_grad's waves: as many as its registers leave room for.
 template <int C>
 constexpr int kRowWaves = C == 1 ? 16 : 8;
@@ -376,6 +374,8 @@ static int grad_waves(int64_t N) {          // to a row
     return N <= 512 ? 1 : N <= 1024 ? 2 : N <= 2048 ? 4 : N <= 4096 || N > 8192 ? 8 : 16;
 }
 static int64_t grad_rows(int64_t N) { return N <= 8192 ? 16 / grad_waves(N) : 1; }      // at a time
+// Workgroups of a gradient by M rows of N columns, each of which leaves a row of partial
+// sums for the weight and one for the bias.
 static int64_t grad_blocks(int64_t M, int64_t N) {
     const int64_t need = (M + grad_rows(N) - 1) / grad_rows(N);
     return need < 256 ? need : 256;
@@ -413,8 +413,8 @@ __device__ __forceinline__ void put_dx8(const float g[8], const float h[8], cons
 
 // W waves to a row of at most 512 W C columns; a workgroup takes every parts-th group of G
 // rows and keeps the columns' sums in registers. The next rows' loads are under way while
-// the sums of one are made, if C = 1 and at most one matrix is f32. Of C = 3 a row stays as it was loaded between its sums and dx,
-// half the registers where it is bf16.
+// the sums of one are made, if C = 1 and at most one matrix is f32. Of C = 3 a row stays as
+// it was loaded between its sums and dx, half the registers where it is bf16.
 template <bool DF, bool XF, bool OF, int W, int C>
 __global__ void __launch_bounds__(64 * kRowWaves<C>) k_norm_grad(const NormGradArgs a) {
     constexpr int G = kRowWaves<C> / W, kCols = 512 * W * C;
@@ -461,8 +461,8 @@ __global__ void __launch_bounds__(64 * kRowWaves<C>) k_norm_grad(const NormGradA
     for (int i = 0; i < C; ++i) w[i].load(d.w, j[i], n[i], kOnes);
     const float per_n = 1.0f / (float)d.N;
     int turn = 0;
-    // the same turns for all waves: the last rows may be there for some groups only. Columns
-    // that do not exist have dy 0, and so add nothing to the sums whatever h is there.
+    // The same turns for all waves: the last rows may be there for some groups only. Columns
+    // that do not exist have dy and h 0, and so add nothing to the sums.
 #pragma unroll 1
     for (; base < d.M; base += stride, turn ^= 1) {
         const int64_t row = base + group;
@@ -477,7 +477,11 @@ __global__ void __launch_bounds__(64 * kRowWaves<C>) k_norm_grad(const NormGradA
             dy0[i].get(g);
             x0[i].get(h);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) h[k] = (h[k] - m) * r;
+            for (int k = 0; k < 8; ++k) h[k] = (h[k] - (n[i] > 0 ? m : 0.0f)) * r;
+            if (n[i] > 0 && n[i] < 8)
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k >= n[i]) h[k] = 0.0f;
         };
 #pragma unroll
         for (int i = 0; i < C; ++i) {

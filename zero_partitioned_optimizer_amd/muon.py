@@ -156,7 +156,7 @@ def _table(coefficients, steps: int):
 
 def _coefficients(c):
     """As a key of _table."""
-    return None if c is None else tuple(tuple(t) if isinstance(t, (tuple, list)) else t for t in c)
+    return None if c is None else tuple(tuple(t) if hasattr(t, "__len__") else t for t in c)
 
 
 def _stack(fn: str, name: str, t: torch.Tensor, dtype, device: int):
