@@ -4,7 +4,7 @@
 // Bound by HBM: each array is read or written once, f32 16 bytes to a lane, four elements to
 // a thread (eight, or two or four groups of four, were 3 to 15% slower). Loads do not stay in
 // the caches; stores do where all outputs fit the Infinity Cache, for whoever reads them next
-// (GPT-2 small's shard of 15.6M: momentum from f32 to bf16 35 us, update 31.5 us), and
+// (GPT-2 small's shard of 15.6M: momentum from f32 to bf16 34.5 us, update 31.3 us), and
 // not beyond (a Llama-7B shaped layer's 202M elements 451 us, 6.3 TB/s, and 375 us, 6.5 TB/s;
 // 511 and 431 with cached stores, 492 and 417 with cached loads too).
 #include <hip/hip_runtime.h>
