@@ -232,3 +232,7 @@ def test_refuses(Z):
     step = Z.MuonShardStep(100, 1, Z.ZERO_F32, p0, [(0, 5, 10)], lr=0.1)
     with pytest.raises(Z.ZeroError, match="replicas"):
         step.step([p0, p0])
+    for bad in (p0[:99], p0.bfloat16(), p0.cpu(), torch.zeros(200, device=dev())[::2]):
+        with pytest.raises(Z.ZeroError, match="a replica of"):
+            step.step([bad])
+    assert step.t == 0

@@ -195,3 +195,18 @@ def test_the_bounds_see_mistakes():
     wrong = want.copy()
     wrong[3, 5] = -wrong[3, 5]
     assert (np.abs(wrong - want) > each).any()
+
+
+def test_matrix_step_stacks_and_refusals():
+    """Runs of one shape at even distances, and the layouts that are refused before any GPU work."""
+    S = Z.MuonShardStep._stacks
+    assert S([(0, 2, 3), (6, 2, 3), (12, 2, 3), (20, 3, 2), (30, 2, 3)]) == [(3, 0, 6, 2, 3), (1, 30, 6, 2, 3),
+                                                                             (1, 20, 6, 3, 2)]
+    assert S([(4, 2, 3), (14, 2, 3)]) == [(2, 4, 10, 2, 3)] and S([]) == []
+    p0 = torch.zeros(100)
+    for matrices, text in (([(0, 5, 10), (49, 5, 10)], "overlap"), ([(60, 1, 1), (59, 2, 1)], "overlap"),
+                           ([(-1, 5, 10)], "matrix at -1")):
+        with pytest.raises(Z.ZeroError, match=text):
+            Z.MuonShardStep(100, 1, Z.ZERO_F32, p0, matrices, lr=0.1)
+    with pytest.raises(Z.ZeroError, match="p0"):
+        Z.MuonShardStep(100, 1, Z.ZERO_F32, p0, [(0, 5, 10)], lr=0.1)

@@ -485,6 +485,7 @@ class MuonShardStep:
                 raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: matrices at {a} and {b} overlap")
         if here and here[0][0] < 0:
             raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a matrix at {here[0][0]}")
+        muon._on_device("MuonShardStep", "p0", p0)
         self.u_off = min([lo] + [o for o, _, _ in here])
         end = max([lo + S] + [o + r * c for o, r, c in here])
         self.whole = self.u_off == lo and end == lo + S
@@ -550,6 +551,11 @@ class MuonShardStep:
         """Enqueue the first part: the averaged gradient and its record."""
         if len(replicas) != self.N:
             raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: {len(replicas)} replicas, not {self.N}")
+        size = 4 if self.grad_dtype == B.ZERO_F32 else 2
+        for r in replicas:
+            if r.device != self.p.device or not r.is_contiguous() or r.numel() < self.S or r.element_size() != size:
+                raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a replica of {r.numel()} elements, {r.dtype} on "
+                                  f"{r.device}, not {self.S} contiguous ones of {size} bytes on {self.p.device}")
         B.zero_reduce_shard(replicas, self.grad_dtype, self.S, self.stats, self.ws, loss_scale=self.state.loss_scale,
                             grad_out=self.g, stream=stream)
 
