@@ -77,11 +77,13 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * x + k * stride_x, its rows ld_x elements apart; o likewise. coefficients: host array
  * of `steps` triples a, b, c, or NULL for (3.4445, -4.7750, 2.0315) in every step.
  *
- * o is bf16. The products run on the matrix cores with fp16 operands and fp32 sums; X is
- * carried with 18 bits and the diagonals of A and b A + c A A in fp32. With the default
- * coefficients the result is about 1e-3 of its norm from the formula's (2e-3 was not
- * passed, 4e-3 where a side is below 32), plus o's own rounding, whatever the fall of the
- * singular values. X's elements must stay below 16 and those of A and b A + c A A off their
+ * o is bf16. The products run on the matrix cores, each as three of fp16 operands with fp32
+ * sums: X, A and b A + c A A are pairs of fp16 numbers, 22 bits and a sign, the diagonals of the
+ * last two fp32. A step multiplies by a what roundings leave in directions that x does not
+ * hold, whatever number format they were made in. Before o is rounded the result is therefore,
+ * with the default coefficients, at most 2^-20 times the product of the steps' a's of its norm
+ * from the formula's (5e-4 for five steps; 2e-4 was not passed, by matrices of rank 1, and
+ * 2e-5 where no singular value is 0), 1 to 4 times what fp32 operations leave. X's elements must stay below 16 and those of A and b A + c A A off their
  * diagonals below 64, as they do for coefficients that keep the singular values below 3;
  * beyond, results are NaN. A matrix of zeros gives zeros. A matrix that holds an infinity
  * or a NaN gives NaN in all its elements, and does not reach the others. The sum of squares

@@ -1,0 +1,56 @@
+"""The allowance of tests/muon_error_ref.py (CPU only): it holds for a model of pairs of fp16
+numbers and for fp32, and does not hold for fewer bits."""
+import numpy as np
+import pytest
+import torch
+
+import muon_error_ref as E
+import muon_ref as R
+
+
+def in_32_bits(x, steps):
+    f = np.float32
+    X = np.asarray(x, f) / f(np.sqrt((np.asarray(x, np.float64) ** 2).sum()) + 1e-7)
+    tall = X.shape[0] > X.shape[1]
+    X = X.T.copy() if tall else X
+    a, b, c = (f(v) for v in R.COEF)
+    for _ in range(steps):
+        A = X @ X.T
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X.T if tall else X
+
+
+def rounded(x):
+    return torch.from_numpy(np.ascontiguousarray(x, np.float32)).to(torch.bfloat16).double().numpy()
+
+
+@pytest.mark.parametrize("kind,rows,cols,steps", E.CASES)
+def test_models_are_within_what_arithmetic_allows(kind, rows, cols, steps):
+    x = E.matrix(kind, rows, cols, np.random.default_rng(rows * 1000 + cols))
+    x = x.astype(np.float32).astype(np.float64)
+    want, allowed = E.growth(x, steps=steps)
+    pairs, singles = (np.linalg.norm(v - want) for v in (E.model(x, steps=steps), in_32_bits(x, steps)))
+    assert pairs <= allowed and singles <= allowed
+    assert pairs <= 4 * singles + 2.0 ** -22 * np.linalg.norm(want)         # as the header says
+    assert pairs <= 2.0 ** -20 * R.COEF[0] ** steps * np.linalg.norm(want)
+    assert E.beyond_rounding(rounded(E.model(x, steps=steps)), want) <= allowed
+
+
+@pytest.mark.parametrize("kind,rows,cols,steps", [c for c in E.CASES if c[1] >= 64 and c[3] == 5])
+def test_the_allowance_sees_fewer_bits(kind, rows, cols, steps):
+    """fp16 operands and 18 bits of X leave more than is allowed, through o's rounding too where the
+    matrix is of more than a few directions; so does a mistake in the formula."""
+    x = E.matrix(kind, rows, cols, np.random.default_rng(rows * 1000 + cols))
+    want, allowed = E.growth(x, steps=steps)
+    if kind != "rank1":
+        assert np.linalg.norm(R.model(x) - want) > allowed
+    if kind not in ("rank1", "rank6"):
+        assert E.beyond_rounding(rounded(R.model(x)), want) > allowed
+    wrong = R.orthogonalize(x, steps=steps, coefficients=(3.4445, -4.7750, 2.0815))
+    assert E.beyond_rounding(rounded(wrong), want) > allowed
+
+
+def test_a_table_of_larger_gains():
+    x = E.matrix("rank6", 200, 300, np.random.default_rng(4))
+    want, allowed = E.growth(x, coefficients=E.TABLE)
+    assert np.linalg.norm(E.model(x, coefficients=E.TABLE) - want) <= allowed

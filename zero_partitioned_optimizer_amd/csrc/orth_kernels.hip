@@ -4,26 +4,24 @@
 // X <- a X + X (b A + c A A) instead, so that nothing is transposed in memory.
 //
 // A step is three products on the matrix cores: the Gram product A, whose two triangles
-// are equal, the square's, likewise, and the update's. Their operands are fp16, their sums
-// fp32. What is rounded to 16 bits, and what is not:
-//   X        kept as an fp16 number hi, X rounded, and lo, the next 8 bits of its fp32 mantissa:
-//            18 bits in 3 bytes; hi is the operand. The update adds a X from both.
-//            A step multiplies directions that X does not hold by a, 485 times in five
-//            steps: rounding noise of X in both its missing rows and columns grows by that (X
-//            in fp16 alone leaves a rank-8 matrix 4% off, in bf16 33%), while the noise of an
-//            operand lies in rows or columns that X holds.
-//   A        off its diagonal. The diagonal, near 1 once X is nearly orthogonal and then
-//            most of A, stays in fp32, in a vector.
-//   b A + c A A   likewise. Its diagonal multiplies hi and lo in the last three steps, hi alone
-//            before: with lo it is closer where it is most of the product, but puts a little
-//            of hi's noise where X holds nothing, which later steps grow.
-// What that leaves, against the formula in 64 bits and before o is rounded (which is 1.7e-3),
-// on a CPU model of these roundings: 0.5 to 1e-3 of the result's norm for normal numbers,
-// rank 1, rank 4 and falling spectra at 32 x 32 to 512 x 2048 (up to 1.6e-3 there, 2.5e-3
-// at 8 x 8); with the diagonals in fp16 1.0 to 2.4e-3; with lo in every step 0.4 to 1.0e-3 on
-// normal numbers but 4e-3 on rank 1 at 64 x 256, in none 1.1 to 1.6e-3 on normal numbers.
+// are equal, the square's, likewise, and the update's, with fp32 sums. A step multiplies
+// directions that X does not hold by a, 485 times in five steps, and any rounding puts some
+// noise there: with operands and X in fp16 alone a rank-8 matrix comes out 4% off, in bf16
+// 33%, and with fp16 operands and 18 bits of X one of 64 equal singular values 0.4%, where
+// fp32 is 8e-6 off. So all of X, A and b A + c A A are pairs of fp16 numbers, hi the value
+// rounded and lo what that leaves, rounded: 22 bits and a sign, 32 in all. A product of two pairs
+// is three of fp16 operands into the same fp32 sums,
+//   hi hi + hi lo + lo hi,
+// and leaves out lo lo, 2^-22 of it at most. Of A and b A + c A A the diagonal, near 1 once X is
+// nearly orthogonal and then most of them, is kept beside in fp32 and meets X in fp32.
+// What that leaves, against the formula in 64 bits and before o is rounded (which is 1.7e-3 of
+// the norm), on a CPU model of these roundings: 1e-6 for normal numbers, 1e-5 for rank 32 to
+// 66, 2e-4 for rank 1, each up to 2.4 times what operations in fp32 leave. Noise that
+// doubles with each a is why the product of the a's is bounded.
 // fp16 holds A and b A + c A A times 1024 and X times 4096, of which a 4096 x 11008 one starts
-// with elements of 1.5e-4; with the default coefficients no element of them passes 3.
+// with elements of 1.5e-4; with the default coefficients no element of them passes 3. Below
+// 6e-5 fp16's numbers are 6e-8 apart, so lo is known to 1.5e-11 of X's norm and 6e-11 of A's at
+// the least.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -40,31 +38,31 @@ typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr int kBR = 64;                     // reduction elements per staged tile
+constexpr int kTerms = 3;                   // of a product of pairs: hi hi, hi lo, lo hi
 constexpr int kSide = 128;                  // all sides are padded to this, with zeros
 constexpr float kScale = 1024.0f, kScaleX = 4096.0f;
 constexpr int kSquareParts = 256;           // partial sums of squares of a matrix, at most
 
 enum OrthOp { kGram, kSquare, kUpdate, kUpdateTall };        // of a matrix that is taller than wide
 
-// C[p, q] = sum_r A(p, r) B(q, r) for each matrix of a group.
+// C[p, q] = sum_r A(p, r) B(q, r) for each matrix of a group, of pairs hi and lo.
 struct OrthArgs {
-    const _Float16* a;
+    const _Float16* a;                      // hi
     const _Float16* b;
+    int64_t low_a, low_b;                   // from an element's hi to its lo
     int64_t lda, ldb, step_a, step_b;       // row lengths, and from one matrix to the next
     int64_t P, Q;                           // multiples of kSide
-    int32_t turns;                          // reduction tiles of kBR
+    int32_t turns;                          // kTerms for each reduction tile of kBR
     int32_t np, nq, tiles;                  // output tiles: down, across, of a matrix
     int32_t first, all;                     // the launch's first one, of all matrices', and how many
-    const _Float16* in;                     // square: A, update: X hi; of C's shape
-    int64_t ld_in, step_in;
+    const _Float16* in;                     // square: A, update: X, hi; of C's shape
+    int64_t low_in, ld_in, step_in;
     const float* diag_in;                   // square: of A, update: of b A + c A A
-    _Float16* out;                          // update: X hi of the next step, or nullptr after the last
-    int64_t ld_out, step_out;
+    _Float16* out;                          // update: X of the next step, or nullptr after the last
+    int64_t low_out, ld_out, step_out;
     float* diag_out;
     int64_t step_diag;
-    uint8_t* lo;                             // update: X lo, in place, laid out as `in`
     float ca, cb, cc;
-    bool low;                               // update: whether the diagonal meets lo too
     uint16_t* o;                            // the last update's output and its size
     int64_t ld_o, step_o, rows, cols;
     float scale;
@@ -121,17 +119,18 @@ __device__ __forceinline__ void meet_waves() {
 }
 
 // PARTS runs of ROWS outer indices from memory to LDS, a thread's chunks at byte offsets
-// from `base` that every tile of the reduction shares; THREADS consecutive threads load a
-// run. A run that lies outside the operand reads its last one instead, which reaches no
-// output.
-template <int ROWS, bool T, int THREADS, int PARTS>
+// from at(turn) that every turn shares; THREADS consecutive threads load a run. A run that
+// lies outside the operand reads its last one instead, which reaches no output. Turns take
+// a reduction tile's three terms one after another, operand A as hi, hi, lo and operand B (LOW
+// 1) as hi, lo, hi: what a turn reads again is still in the caches.
+template <int ROWS, bool T, int THREADS, int PARTS, int LOW>
 struct Loader {
     static constexpr int kLoads = ROWS * kBR / 8 / THREADS;
     static_assert(kLoads % 2 == 0, "pairs of loads");
     uint32_t at[PARTS][kLoads];
     const char* base;
-    int64_t step;
-    __device__ __forceinline__ void init(const _Float16* src, int64_t ld, int64_t o0, int64_t O) {
+    int64_t step, low;
+    __device__ __forceinline__ void init(const _Float16* src, int64_t to_low, int64_t ld, int64_t o0, int64_t O) {
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) {
             const int64_t run = o0 + ROWS * h < O ? ROWS * h : O - ROWS - o0;
@@ -149,8 +148,13 @@ struct Loader {
         }
         base = reinterpret_cast<const char*>(src + (T ? o0 : o0 * ld));
         step = (T ? kBR * ld : kBR) * 2;
+        low = to_low * 2;
     }
-    // Run h of the tile at `from` to LDS byte address `tile`; `wave` (of those that load the
+    __device__ __forceinline__ const char* turn(int k) const {
+        const uint32_t tile = (uint32_t)k / kTerms, term = (uint32_t)k - kTerms * tile;
+        return base + tile * step + (term == LOW ? low : 0);
+    }
+    // Run h of what lies at `from` to LDS byte address `tile`; `wave` (of those that load the
     // run) is the same in all lanes. With `records` 0 the buffer's range check stops the
     // loads (which still count).
     __device__ __forceinline__ void issue(int h, const char* from, uint32_t tile, int wave, int records) const {
@@ -163,6 +167,10 @@ struct Loader {
     }
 };
 constexpr int kAllRecords = 0x7FFFFFFF;
+template <int ROWS, bool T, int THREADS, int PARTS>
+using LoaderA = Loader<ROWS, T, THREADS, PARTS, 2>;
+template <int ROWS, bool T, int THREADS, int PARTS>
+using LoaderB = Loader<ROWS, T, THREADS, PARTS, 1>;
 
 // The matrix instruction's operands from a tile of ROWS outer indices: for block i, lane l
 // holds outer index o0 + 16 i + (l & 15) and reduction elements 32 s + 8 (l >> 4) .. + 7. o0 is a
@@ -227,45 +235,30 @@ __device__ __forceinline__ int place(const OrthArgs& g, int t, int* tp, int* tq)
 // epilogues
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void put_h8(_Float16* p, const float v[8]) {
-    h8 t;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) t[k] = (_Float16)v[k];
-    *reinterpret_cast<h8*>(p) = t;
-}
-
-// X (times kScaleX) as hi and lo: with half of hi's last place added to its bits, hi is what
-// fp16 holds of them (rounded to nearest, then; ties away from zero) and lo the next 8. Below
-// fp16's normal numbers, 1.5e-8 of X itself, it is 0; beyond its largest it is NaN.
-constexpr uint32_t kHalfPlace = 1u << 12;
-typedef uint32_t v2u __attribute__((ext_vector_type(2)));
-__device__ __forceinline__ void split_x8(const float v[8], h8* hi, v2u* lo) {
-    uint32_t t[8], h[4];
-    float most = 0.0f;
+// Eight values as pairs, lo `low` elements behind hi. A value beyond fp16's largest has an
+// infinity in both, of either sign, so that what it reaches is NaN.
+struct Pair8 {
+    h8 hi, lo;
+    __device__ __forceinline__ void load(const _Float16* p, int64_t low) {
+        hi = *reinterpret_cast<const h8*>(p);
+        lo = *reinterpret_cast<const h8*>(p + low);
+    }
+    __device__ __forceinline__ float get(int k) const { return (float)hi[k] + (float)lo[k]; }
+};
+__device__ __forceinline__ void put_pairs(_Float16* p, int64_t low, const float v[8]) {
+    h8 hi, lo;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-        const float x = fabsf(v[k]) < 0x1p-14f ? 0.0f : v[k];
-        most = fmaxf(most, fabsf(x));
-        t[k] = __float_as_uint(x) + kHalfPlace;
+        hi[k] = (_Float16)v[k];
+        lo[k] = (_Float16)(v[k] - (float)hi[k]);
     }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        h[k] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_pkrtz(__uint_as_float(t[2 * k]), __uint_as_float(t[2 * k + 1])));
-        if (!(most < 65504.0f)) h[k] = 0x7E007E00u;
-    }
-    *hi = __builtin_bit_cast(h8, v4u{h[0], h[1], h[2], h[3]});
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-        (*lo)[k] = __builtin_amdgcn_perm(__builtin_amdgcn_perm(t[4 * k + 3] >> 5, t[4 * k + 2] >> 5, 0x0C0C0400u),
-                                         __builtin_amdgcn_perm(t[4 * k + 1] >> 5, t[4 * k] >> 5, 0x0C0C0400u), 0x05040100u);
-}
-__device__ __forceinline__ float joined(float hi, const v2u& lo, int k) {
-    return __uint_as_float((__float_as_uint(hi) | (lo[k >> 2] >> 8 * (k & 3) & 255u) << 5) - kHalfPlace);
+    *reinterpret_cast<h8*>(p) = hi;
+    *reinterpret_cast<h8*>(p + low) = lo;
 }
 
-// What a product makes of its sums, for a lane's eight columns q .. q + 7 of matrix m: what
-// the columns need is loaded once (the constructor), what a row needs ahead of its use (In,
-// load), so that many rows' loads are under way.
+// What a product makes of its sums, for a lane's eight columns q + s .. q + s + 7 of matrix m (s:
+// a run's distance from the first one): what the columns need is loaded once a run (columns),
+// what a row needs ahead of its use (In, load), so that many rows' loads are under way.
 template <int OP>
 struct OrthEpilogue;
 
@@ -274,24 +267,26 @@ template <>
 struct OrthEpilogue<kGram> {
     static constexpr float kOff = kScale / (kScaleX * kScaleX);
     struct In {};
+    struct Columns {};
     const OrthArgs& g;
     _Float16* out;
     float* diag;
     const int64_t q;
     __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t col)
         : g(a), out(a.out + m * a.step_out + col), diag(a.diag_out + m * a.step_diag), q(col) {}
-    __device__ __forceinline__ void load(In&, int64_t) const {}
+    __device__ __forceinline__ void columns(Columns&, int) const {}
+    __device__ __forceinline__ void load(In&, int64_t, int) const {}
     // v: in, the sums; out, what the matrix holds, here and, of a symmetric one, at the mirrored place
-    __device__ __forceinline__ void put(const In&, int64_t p, float v[8]) const {
+    __device__ __forceinline__ void put(const In&, const Columns&, int64_t p, int s, float v[8]) const {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             v[k] *= kOff;
-            if (p == q + k) {
+            if (p == q + s + k) {
                 diag[p] = v[k] * (1.0f / kScale);
                 v[k] = 0.0f;
             }
         }
-        put_h8(out + p * g.ld_out, v);
+        put_pairs(out + p * g.ld_out + s, g.low_out, v);
     }
 };
 
@@ -300,8 +295,11 @@ template <>
 struct OrthEpilogue<kSquare> {
     static constexpr float kOnce = 1.0f / kScale;
     struct In {
-        h8 f;
+        Pair8 f;
         float d;
+    };
+    struct Columns {
+        float d[8];
     };
     const OrthArgs& g;
     const _Float16* in;
@@ -309,27 +307,25 @@ struct OrthEpilogue<kSquare> {
     _Float16* out;
     float* diag;
     const int64_t q;
-    float dq[8];
     __device__ __forceinline__ OrthEpilogue(const OrthArgs& a, int64_t m, int64_t col)
         : g(a), in(a.in + m * a.step_in + col), from(a.diag_in + m * a.step_diag), out(a.out + m * a.step_out + col),
-          diag(a.diag_out + m * a.step_diag), q(col) {
-        load8_f(dq, from + q, 8);
-    }
-    __device__ __forceinline__ void load(In& r, int64_t p) const {
-        r.f = *reinterpret_cast<const h8*>(in + p * g.ld_in);
+          diag(a.diag_out + m * a.step_diag), q(col) {}
+    __device__ __forceinline__ void columns(Columns& c, int s) const { load8_f(c.d, from + q + s, 8); }
+    __device__ __forceinline__ void load(In& r, int64_t p, int s) const {
+        r.f.load(in + p * g.ld_in + s, g.low_in);
         r.d = from[p];
     }
-    __device__ __forceinline__ void put(const In& r, int64_t p, float v[8]) const {
+    __device__ __forceinline__ void put(const In& r, const Columns& c, int64_t p, int s, float v[8]) const {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float f = (float)r.f[k], ff = v[k] * kOnce;
-            v[k] = fmaf(g.cc, fmaf(r.d + dq[k], f, ff), g.cb * f);
-            if (p == q + k) {
+            const float f = r.f.get(k), ff = v[k] * kOnce;
+            v[k] = fmaf(g.cc, fmaf(r.d + c.d[k], f, ff), g.cb * f);
+            if (p == q + s + k) {
                 diag[p] = fmaf(g.cc, fmaf(r.d, r.d, ff * kOnce), g.cb * r.d);
                 v[k] = 0.0f;
             }
         }
-        put_h8(out + p * g.ld_out, v);
+        put_pairs(out + p * g.ld_out + s, g.low_out, v);
     }
 };
 
@@ -338,43 +334,37 @@ template <bool TALL>
 struct UpdateEpilogue {
     static constexpr float kOnce = 1.0f / kScale;
     struct In {
-        h8 hi;
-        v2u lo;
+        Pair8 x;
         float d;
+    };
+    struct Columns {
+        float d[8];
     };
     const OrthArgs& g;
     const int64_t at;
     const float* from;
     uint16_t* o;
-    const int n;                            // of the columns in the last step's output
-    float dq[8];
-    __device__ __forceinline__ UpdateEpilogue(const OrthArgs& a, int64_t m, int64_t q)
-        : g(a), at(m * a.step_in + q), from(a.diag_in + m * a.step_diag), o(a.o + m * a.step_o + q),
-          n(a.cols - q >= 8 ? 8 : a.cols > q ? (int)(a.cols - q) : 0) {
-        if constexpr (TALL) load8_f(dq, from + q, 8);
+    const int64_t q;
+    __device__ __forceinline__ UpdateEpilogue(const OrthArgs& a, int64_t m, int64_t col)
+        : g(a), at(m * a.step_in + col), from(a.diag_in + m * a.step_diag), o(a.o + m * a.step_o + col), q(col) {}
+    __device__ __forceinline__ void columns(Columns& c, int s) const {
+        if constexpr (TALL) load8_f(c.d, from + q + s, 8);
     }
-    __device__ __forceinline__ void load(In& r, int64_t p) const {
-        r.hi = *reinterpret_cast<const h8*>(g.in + at + p * g.ld_in);
-        r.lo = *reinterpret_cast<const v2u*>(g.lo + at + p * g.ld_in);
+    __device__ __forceinline__ void load(In& r, int64_t p, int s) const {
+        r.x.load(g.in + at + p * g.ld_in + s, g.low_in);
         if constexpr (!TALL) r.d = from[p];
     }
-    __device__ __forceinline__ void put(const In& r, int64_t p, float v[8]) const {
+    __device__ __forceinline__ void put(const In& r, const Columns& c, int64_t p, int s, float v[8]) const {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            // a x + d x, or a x + d hi
-            const float d = TALL ? dq[k] : r.d, h = (float)r.hi[k], x = joined(h, r.lo, k);
-            v[k] = fmaf(g.low ? g.ca + d : g.ca, x, fmaf(g.low ? 0.0f : d, h, v[k] * kOnce));
+            v[k] = fmaf(g.ca + (TALL ? c.d[k] : r.d), r.x.get(k), v[k] * kOnce);
         }
         if (g.out) {
-            h8 h;
-            v2u l;
-            split_x8(v, &h, &l);
-            *reinterpret_cast<h8*>(g.out + at + p * g.ld_in) = h;
-            *reinterpret_cast<v2u*>(g.lo + at + p * g.ld_in) = l;
-        } else if (p < g.rows && n > 0) {
+            put_pairs(g.out + at + p * g.ld_in + s, g.low_out, v);
+        } else if (p < g.rows && q + s < g.cols) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) v[k] *= g.scale * (1.0f / kScaleX);
-            store8_bf(o + p * g.ld_o, v, n);
+            store8_bf(o + p * g.ld_o + s, v, g.cols - q - s >= 8 ? 8 : (int)(g.cols - q - s));
         }
     }
 };
@@ -391,8 +381,8 @@ constexpr bool symmetric(int op) { return op < kUpdate; }
 // A wave's blocks, four times FQ at a time, through its part of LDS (64 rows of 16 FQ floats),
 // so that a lane has eight consecutive columns, the same in all its rows of a run. Blocks are
 // computed as (q, p): a lane holds four consecutive columns of a row, a 16-byte unit, unit u
-// of row o at u ^ (o & mask). What a lane's rows need is asked for a run ahead, and (ask) of the
-// first run together: before the reduction by k_orth_mid, behind it by the others, which
+// of row o at u ^ (o & mask). What a lane's rows need is asked for kAhead rows ahead, and (ask) of
+// the first ones together: before the reduction by k_orth_mid, behind it by the others, which
 // gain nothing from it or lose (12 updates of 768 x 2304 55 to 59 us). Below the diagonal of a
 // symmetric product the results go back to LDS, and from there to their mirrored places,
 // eight consecutive rows to a lane. row_of(i): first row of block i, an even one's before the
@@ -405,27 +395,33 @@ struct Finish {
     const Row row_of;
     const Col col_of;
     const int lane, c, o0;
-    const OrthEpilogue<OP> epi[2];
-    typename OrthEpilogue<OP>::In in[kRows];
+    const OrthEpilogue<OP> epi;
+    // a run's rows, or half of them where all, beside two runs' sums, would not fit the registers
+    static constexpr int kAhead = OP == kSquare && RUNS == 2 ? kRows / 2 : kRows;
+    typename OrthEpilogue<OP>::In in[kAhead];
 
     __device__ __forceinline__ Finish(const OrthArgs& a, int64_t matrix, Row rows, Col cols)
         : g(a), m(matrix), row_of(rows), col_of(cols), lane(threadIdx.x & 63), c(lane % kGroups), o0(lane / kGroups),
-          epi{{a, m, inside(0)}, {a, m, inside(RUNS - 1)}} {}
+          epi(a, m, cols(0) + 8 * c) {}
     __device__ __forceinline__ int64_t row(int o) const { return row_of(o >> 4) + (o & 15); }
     __device__ __forceinline__ int64_t column(int run) const { return col_of(run) + 8 * c; }
-    __device__ __forceinline__ int64_t inside(int run) const { return column(run) < g.Q ? column(run) : 0; }
-    __device__ __forceinline__ void load(int run, int u) {
-        const int64_t p = row(o0 + kStep * u);
-        if (column(run) < g.Q && p < g.P) epi[run].load(in[u], p);
+    __device__ __forceinline__ int shift(int run) const { return (int)(col_of(run) - col_of(0)); }
+    // what row `at` of all runs' needs
+    __device__ __forceinline__ void load(int at) {
+        const int run = at / kRows;
+        const int64_t p = row(o0 + kStep * (at % kRows));
+        if (at < RUNS * kRows && column(run) < g.Q && p < g.P) epi.load(in[at % kAhead], p, shift(run));
     }
     __device__ __forceinline__ void ask() {
 #pragma unroll
-        for (int u = 0; u < kRows; ++u) load(0, u);
+        for (int u = 0; u < kAhead; ++u) load(u);
     }
     __device__ __forceinline__ void operator()(const v4f (&acc)[4][FQ * RUNS], float* mine, bool mirror) {
         const int r = lane & 7;
 #pragma unroll
         for (int run = 0; run < RUNS; ++run) {
+            typename OrthEpilogue<OP>::Columns col;
+            if (column(run) < g.Q) epi.columns(col, shift(run));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -439,12 +435,12 @@ struct Finish {
                 v4f* const lo = reinterpret_cast<v4f*>(mine + kCols * o + 4 * ((2 * c) ^ (o & kMask)));
                 v4f* const hi = reinterpret_cast<v4f*>(mine + kCols * o + 4 * ((2 * c + 1) ^ (o & kMask)));
                 float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
-                if (column(run) < g.Q && row(o) < g.P) epi[run].put(in[u], row(o), v);
+                if (column(run) < g.Q && row(o) < g.P) epi.put(in[u % kAhead], col, row(o), shift(run), v);
                 if (symmetric(OP) && mirror) {
                     *lo = v4f{v[0], v[1], v[2], v[3]};
                     *hi = v4f{v[4], v[5], v[6], v[7]};
                 }
-                if (run + 1 < RUNS) load(run + 1, u);
+                load(run * kRows + u + kAhead);
             }
             if (symmetric(OP) && mirror && row(8 * r) < g.P) {
 #pragma unroll 2
@@ -456,7 +452,7 @@ struct Finish {
                         v[k] = mine[kCols * o + 4 * ((j >> 2) ^ (o & kMask)) + (j & 3)];
                     }
                     const int64_t q = col_of(run) + j;
-                    if (q < g.Q) put_h8(g.out + m * g.step_out + q * g.ld_out + row(8 * r), v);
+                    if (q < g.Q) put_pairs(g.out + m * g.step_out + q * g.ld_out + row(8 * r), g.low_out, v);
                 }
             }
         }
@@ -481,9 +477,9 @@ __device__ __forceinline__ void clear(v4f (&acc)[FP][FQ]) {
 }
 
 // 64 x 64 outputs by eight waves, for outputs of few tiles: two groups of four waves take
-// every other reduction tile, each with a ring of four in LDS, and their sums are joined
-// there. A wave has 32 x 32. A product of 768 x 768 takes 6 to 7 us, of which its six turns are
-// 1.1 and what surrounds them the rest.
+// every other turn, each with a ring of four in LDS, and their sums are joined there. A wave
+// has 32 x 32. A product of 768 x 768 takes 11 to 13 us, of which its 36 turns are about 7 and what
+// surrounds them the rest.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
     constexpr bool SYM = symmetric(OP);
@@ -498,22 +494,18 @@ __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
     const Fragments<H, TA> ga(wp);
     const Fragments<H, TB> gb(wq);
     const uint32_t base = lds_address(lds) + 2 * kSlots * kSlot * half;
-    Loader<H, TA, 256, 1> la;
-    Loader<H, TB, 256, 1> lb;
-    constexpr int kLoads = 2 * Loader<H, TA, 256, 1>::kLoads;
-    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
-    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
-    la.base += half * la.step;
-    lb.base += half * lb.step;
+    LoaderA<H, TA, 256, 1> la;
+    LoaderB<H, TB, 256, 1> lb;
+    constexpr int kLoads = 2 * decltype(la)::kLoads;
+    la.init(g.a + m * g.step_a, g.low_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.low_b, g.ldb, q0, g.Q);
     const int n = g.turns / 2;              // sides are padded to 128: an even number
-    // loads of tiles behind the last are stopped by their buffer's range
+    // loads of turns behind the last are stopped by their buffer's range
     const auto load = [&](int k) {
         const int records = k < n ? kAllRecords : 0;
         const uint32_t to = base + 2 * kSlot * (k % kSlots);
-        la.issue(0, la.base, to, wave & 3, records);
-        lb.issue(0, lb.base, to + 2 * kTile, wave & 3, records);
-        la.base += 2 * la.step;
-        lb.base += 2 * lb.step;
+        la.issue(0, la.turn(2 * k + half), to, wave & 3, records);
+        lb.issue(0, lb.turn(2 * k + half), to + 2 * kTile, wave & 3, records);
     };
 #pragma unroll
     for (int k = 0; k < kSlots - 1; ++k) load(k);
@@ -540,7 +532,9 @@ __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
     loads_landed<0>();
     const OrthEpilogue<OP> epi(g, m, q0 + 8 * (threadIdx.x & 7));
     typename OrthEpilogue<OP>::In in;
-    epi.load(in, p0 + (threadIdx.x >> 3));
+    typename OrthEpilogue<OP>::Columns col;
+    epi.columns(col, 0);
+    epi.load(in, p0 + (threadIdx.x >> 3), 0);
     meet_waves();
     // [64][64] floats, unit u of row o at u ^ (o & 15)
     float* const sums = reinterpret_cast<float*>(lds);
@@ -562,7 +556,7 @@ __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
     v4f* const lo = reinterpret_cast<v4f*>(sums + 64 * o + 4 * ((2 * c) ^ (o & 15)));
     v4f* const hi = reinterpret_cast<v4f*>(sums + 64 * o + 4 * ((2 * c + 1) ^ (o & 15)));
     float v[8] = {(*lo)[0], (*lo)[1], (*lo)[2], (*lo)[3], (*hi)[0], (*hi)[1], (*hi)[2], (*hi)[3]};
-    epi.put(in, p0 + o, v);
+    epi.put(in, col, p0 + o, 0, v);
     if (SYM && tp != tq) {
         *lo = v4f{v[0], v[1], v[2], v[3]};
         *hi = v4f{v[4], v[5], v[6], v[7]};
@@ -572,14 +566,14 @@ __global__ void __launch_bounds__(512) k_orth_few(const OrthArgs g) {
             const int row = 8 * c + k;
             v[k] = sums[64 * row + 4 * ((o >> 2) ^ (row & 15)) + (o & 3)];
         }
-        put_h8(g.out + m * g.step_out + (q0 + o) * g.ld_out + p0 + 8 * c, v);
+        put_pairs(g.out + m * g.step_out + (q0 + o) * g.ld_out + p0 + 8 * c, g.low_out, v);
     }
 }
 
-// 128 x 128 outputs by four waves, 64 x 64 each; two tiles of the reduction in LDS, the next
-// one loading while one is multiplied. Two workgroups fit a compute unit, and one's epilogue
-// runs beside the other's products: the update of twelve of 768 x 2304 54 to 62 us by the card,
-// 32.6 GFLOP and 113 MB, with the matrix cores busy a quarter of the time.
+// 128 x 128 outputs by four waves, 64 x 64 each; two turns' tiles in LDS, the next one
+// loading while one is multiplied. Two workgroups fit a compute unit, and one's epilogue
+// runs beside the other's products: the update of twelve of 768 x 2304 124 to 138 us, 97.8 GFLOP
+// in three terms, 0.7 to 0.8 PFLOP/s.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
     constexpr bool SYM = symmetric(OP);
@@ -593,20 +587,20 @@ __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
     const Fragments<H, TA> ga(wp);
     const Fragments<H, TB> gb(wq);
     const uint32_t base = lds_address(lds);
-    Loader<H, TA, 256, 1> la;
-    Loader<H, TB, 256, 1> lb;
-    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
-    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
-    la.issue(0, la.base, base, wave, kAllRecords);
-    lb.issue(0, lb.base, base + 2 * kTile, wave, kAllRecords);
+    LoaderA<H, TA, 256, 1> la;
+    LoaderB<H, TB, 256, 1> lb;
+    la.init(g.a + m * g.step_a, g.low_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.low_b, g.ldb, q0, g.Q);
+    la.issue(0, la.turn(0), base, wave, kAllRecords);
+    lb.issue(0, lb.turn(0), base + 2 * kTile, wave, kAllRecords);
 #pragma unroll 1
     for (int k = 0; k < g.turns; ++k) {
         loads_landed<0>();
         meet_waves();
         const uint32_t tile = base + 4 * kTile * (k & 1), next = base + 4 * kTile * ((k + 1) & 1);
         if (k + 1 < g.turns) {
-            la.issue(0, la.base += la.step, next, wave, kAllRecords);
-            lb.issue(0, lb.base += lb.step, next + 2 * kTile, wave, kAllRecords);
+            la.issue(0, la.turn(k + 1), next, wave, kAllRecords);
+            lb.issue(0, lb.turn(k + 1), next + 2 * kTile, wave, kAllRecords);
         }
 #pragma unroll
         for (int s = 0; s < kBR / 32; ++s) {
@@ -628,13 +622,13 @@ __global__ void __launch_bounds__(256, 2) k_orth(const OrthArgs g) {
 }
 
 // 128 x 128 outputs by eight waves, 64 x 32 each, one workgroup to a compute unit: a ring of
-// four reduction tiles, in turns that barriers divide into two parts. A wave reads the
+// four turns' tiles, in turns that barriers divide into two parts. A wave reads the
 // turn's operands and asks for the tile three ahead; then it multiplies; waves 4-7 are one
 // barrier behind waves 0-3, which share their SIMDs, so that one wave of each pair
 // multiplies while the other reads. A tile's place is asked for again one turn after it was
 // read, two barriers or more after its last reads began; each turn ends when the next turn's
 // tile is here, one barrier before anyone reads it. The 252 tiles of twelve of 768 x 2304 take
-// 27 to 30 us for the Gram product and 16 to 18 for the square.
+// 67 to 73 us for the Gram product and 31 to 34 for the square.
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
     constexpr bool SYM = symmetric(OP);
@@ -648,19 +642,17 @@ __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
     const Fragments<H, TA> ga(wp);
     const Fragments<H, TB> gb(wq);
     const uint32_t base = lds_address(lds);
-    Loader<H, TA, 512, 1> la;
-    Loader<H, TB, 512, 1> lb;
-    constexpr int kLoads = 2 * Loader<H, TA, 512, 1>::kLoads;
-    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
-    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
+    LoaderA<H, TA, 512, 1> la;
+    LoaderB<H, TB, 512, 1> lb;
+    constexpr int kLoads = 2 * decltype(la)::kLoads;
+    la.init(g.a + m * g.step_a, g.low_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.low_b, g.ldb, q0, g.Q);
     const int n = g.turns;
     const auto load = [&](int k) {
         const int records = k < n ? kAllRecords : 0;
         const uint32_t to = base + 2 * kSlot * (k % kSlots);
-        la.issue(0, la.base, to, wave, records);
-        lb.issue(0, lb.base, to + 2 * kTile, wave, records);
-        la.base += la.step;
-        lb.base += lb.step;
+        la.issue(0, la.turn(k), to, wave, records);
+        lb.issue(0, lb.turn(k), to + 2 * kTile, wave, records);
     };
     auto end = finish<OP, 2, 1>(g, m, [&](int i) { return p0 + wp + 16 * i; }, [&](int) { return q0 + wq; });
     end.ask();
@@ -703,8 +695,9 @@ __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
 
 // 256 x 256 outputs by eight waves, one workgroup to a compute unit. Reduction tiles lie in
 // LDS as halves of 128 outer indices, two tiles of four halves. A wave's outputs are 32 x 64
-// of each quarter (half of A, half of B), so that it stores whole lines. A tile is two turns
-// of 32 matrix instructions, and a turn has two parts that barriers divide: the wave reads
+// of each quarter (half of A, half of B), so that it stores whole lines. A tile (a term of 64
+// reduction elements: a turn of OrthArgs) is two turns of 32 matrix instructions here, and such a
+// turn has two parts that barriers divide: the wave reads
 // what its turn needs and no turn before it read, and asks for halves of the tiles to come;
 // then it multiplies. Waves 4-7 are one barrier behind waves 0-3, so that one wave of each
 // pair multiplies while the other reads.
@@ -718,12 +711,12 @@ __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
 // reads was asked for in turn f - 3, or before, or in the prologue; turn f - 1 waits until at
 // most the four halves of the two latest turns are under way, and its barrier comes before
 // anyone's turn f.
-// (Four turns of 16 instructions, eight barriers a tile in place of four: the Gram product
-// of 4096 x 11008 242 us in place of 200. Half of the first turn's reads a turn ahead, 12 KB in
-// every turn in place of 16 and 8: 208 us there, and the update's 340 in place of 348. The
-// 32 x 32 matrix instruction, with four turns: 5-8% slower.) The update of 11008 x 4096 takes
-// 330 to 354 us, 1.04 to 1.12 PFLOP/s, the matrix cores busy 53% of the time; its square's 136
-// tiles leave 120 compute units without any, 97 to 104 us.
+// (With one term a product: four turns of 16 instructions, eight barriers a tile in place of
+// four, made the Gram product of 4096 x 11008 take 242 us in place of 200; half of the first
+// turn's reads a turn ahead, 12 KB in every turn in place of 16 and 8, 208 us there, and the
+// update's 340 in place of 348; the 32 x 32 matrix instruction, with four turns, 5-8% more.) The
+// 512 whole tiles of the update of 11008 x 4096 take 575 to 600 us, 1.37 to 1.43 PFLOP/s in three
+// terms; the other 176 are split, 229 to 244 and 36 to 42 for the join.
 //
 // The workgroup takes reduction tiles first .. last of output tile `t`: WHOLE, or a part,
 // whose sums go to memory for k_orth_join, a wave's as they lie in its registers.
@@ -767,25 +760,22 @@ __device__ __forceinline__ void wide_tile(const OrthArgs& g, int t, int first, i
         __builtin_amdgcn_s_setprio(0);
         __builtin_amdgcn_sched_barrier(0);
     };
-    Loader<H, TA, 512, 2> la;
-    Loader<H, TB, 512, 2> lb;
-    constexpr int kLoads = Loader<H, TA, 512, 2>::kLoads;
-    la.init(g.a + m * g.step_a, g.lda, p0, g.P);
-    lb.init(g.b + m * g.step_b, g.ldb, q0, g.Q);
-    la.base += first * la.step;
-    lb.base += first * lb.step;
+    LoaderA<H, TA, 512, 2> la;
+    LoaderB<H, TB, 512, 2> lb;
+    constexpr int kLoads = decltype(la)::kLoads;
+    la.init(g.a + m * g.step_a, g.low_a, g.lda, p0, g.P);
+    lb.init(g.b + m * g.step_b, g.low_b, g.ldb, q0, g.Q);
     const int n = last - first;
     // loads of tiles behind the last are stopped by their buffer's range
     const auto there = [&](int k) { return k < n ? kAllRecords : 0; };
-    la.issue(0, la.base, half(0, 0), wave, kAllRecords);
-    la.issue(1, la.base, half(0, 1), wave, kAllRecords);
-    lb.issue(0, lb.base, half(0, 2), wave, kAllRecords);
-    lb.issue(1, lb.base, half(0, 3), wave, kAllRecords);
-    la.issue(0, la.base + la.step, half(1, 0), wave, there(1));
-    la.issue(1, la.base + la.step, half(1, 1), wave, there(1));
-    lb.issue(0, lb.base + lb.step, half(1, 2), wave, there(1));
-    la.base += 2 * la.step;                 // of tile k + 2
-    lb.base += 2 * lb.step;
+    const char *a0 = la.turn(first), *b0 = lb.turn(first), *a1 = la.turn(first + 1), *b1 = lb.turn(first + 1);
+    la.issue(0, a0, half(0, 0), wave, kAllRecords);
+    la.issue(1, a0, half(0, 1), wave, kAllRecords);
+    lb.issue(0, b0, half(0, 2), wave, kAllRecords);
+    lb.issue(1, b0, half(0, 3), wave, kAllRecords);
+    la.issue(0, a1, half(1, 0), wave, there(1));
+    la.issue(1, a1, half(1, 1), wave, there(1));
+    lb.issue(0, b1, half(1, 2), wave, there(1));
     loads_landed<4 * kLoads>();
     meet_waves();
     if (wave >= 4) meet_waves();
@@ -795,17 +785,17 @@ __device__ __forceinline__ void wide_tile(const OrthArgs& g, int t, int first, i
         read_a(0, half(k, 0));
         read_b(half(k, 2));
         read_a(1, half(k, 1));
-        lb.issue(1, lb.base - lb.step, half(k + 1, 3), wave, one);
+        lb.issue(1, b1, half(k + 1, 3), wave, one);
         loads_landed<4 * kLoads>();
         meet_waves();
         multiply(0);
         meet_waves();
         read_b(half(k, 3));
-        la.issue(0, la.base, half(k, 0), wave, two);
-        la.issue(1, la.base, half(k, 1), wave, two);
-        lb.issue(0, lb.base, half(k, 2), wave, two);
-        la.base += la.step;
-        lb.base += lb.step;
+        a1 = la.turn(first + k + 2);
+        b1 = lb.turn(first + k + 2);
+        la.issue(0, a1, half(k, 0), wave, two);
+        la.issue(1, a1, half(k, 1), wave, two);
+        lb.issue(0, b1, half(k, 2), wave, two);
         loads_landed<4 * kLoads>();
         meet_waves();
         multiply(1);
@@ -837,9 +827,10 @@ __global__ void __launch_bounds__(512) k_orth_wide(const OrthArgs g) {
 // reduction as those that share operand rows with them: workgroup w < a s takes slice w / a of
 // s of tile w % a; the r tiles that are left over are cut likewise, into t slices, for a
 // second part of each workgroup's work. k_orth_join puts the parts together, in order.
-// (Runs of consecutive reduction tiles, whatever tile they are of, share no operand rows in
-// the caches: the Gram product of 4096 x 11008 took 240 us, 2.2 a tile's turns; as it is it
-// takes 169 to 180 and its join 33 to 37, by the 128 MB of sums between them.)
+// (Runs of consecutive turns, whatever tile they are of, share no operand rows in the caches:
+// with one term a product, the Gram product of 4096 x 11008 took 240 us in place of 180.) As it
+// is the Gram product of 11008 x 4096 takes 477 to 512 us and its join 44 to 46, by the 128 MB of
+// sums between them; the square 180 to 192 and 42 to 44.
 constexpr int kSplit = 256;
 constexpr int64_t kPartFloats = 256 * 256;
 struct Slices {
@@ -908,7 +899,7 @@ struct StartArgs {
     int64_t ld_x, step_x, rows, cols;
     int64_t Rp, Cp;
     _Float16* hi;
-    uint8_t* lo;
+    int64_t low;
     double* parts;                  // [matrix][kSquareParts]
     int32_t n_parts;
     double eps;
@@ -964,7 +955,7 @@ __global__ void __launch_bounds__(kSquareBlock) k_orth_squares(const StartArgs g
     if (threadIdx.x == 0) g.parts[m * kSquareParts + blockIdx.x] = sum;
 }
 
-// X hi and lo with their padding, 11008 x 4096 in 41 us (5.6 TB/s). A norm that is not finite makes all of them NaN.
+// X with its padding, 11008 x 4096 from bf16 in 44 to 50 us (5.4 to 6.1 TB/s). A norm that is not finite makes all of them NaN.
 template <bool XF>
 __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
     const int64_t m = blockIdx.y, chunks = g.Cp / 8, all = g.Rp * chunks;
@@ -980,12 +971,7 @@ __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
         load_x8<XF>(v, g, m, row, 8 * c);
 #pragma unroll
         for (int k = 0; k < 8; ++k) v[k] = fine ? (float)((double)v[k] * by) : NAN;
-        h8 h;
-        v2u l;
-        split_x8(v, &h, &l);
-        const int64_t at = m * g.Rp * g.Cp + row * g.Cp + 8 * c;
-        *reinterpret_cast<h8*>(g.hi + at) = h;
-        *reinterpret_cast<v2u*>(g.lo + at) = l;
+        put_pairs(g.hi + m * g.Rp * g.Cp + row * g.Cp + 8 * c, g.low, v);
     }
 }
 
@@ -994,6 +980,7 @@ __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
 // ---------------------------------------------------------------------------
 
 static int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
+static int64_t turns_of(int64_t R) { return kTerms * R / kBR; }
 
 static int64_t over(int64_t n, int64_t by) { return (n + by - 1) / by; }
 static int64_t tiles_of(int64_t P, int64_t Q, int64_t side, bool sym) {
@@ -1007,7 +994,7 @@ struct OrthPlan {
     OrthKind kind;
     int64_t split;                  // kWide: of all tiles, the last ones that are split
 };
-static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym) {
+static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym, bool may_split) {
     const int64_t few = n * tiles_of(P, Q, 64, sym), mid = n * tiles_of(P, Q, 128, sym), wide = n * tiles_of(P, Q, 256, sym);
     OrthPlan best{kTwo, 0};
     double least = 1e300;
@@ -1017,7 +1004,7 @@ static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym
             best = OrthPlan{k, split};
         }
     };
-    // us for a reduction tile (turn) and for a tile's start and end, in a round of the chip:
+    // us for a turn and for a tile's start and end, in a round of the chip:
     // measured at 768 x 768 to 4096 x 11008, one matrix to twelve
     const int64_t rest = mid % 512;
     offer(kTwo, 0, mid / 512 * (0.9 * turns + 9) + (rest == 0 ? 0 : rest <= 256 ? 0.65 * turns + 8.5 : 0.9 * turns + 9));
@@ -1026,7 +1013,7 @@ static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym
     const int64_t left = wide % kSplit;
     const double ends = sym ? 12 : 18, rounds = wide / 256 * (1.4 * turns + ends);
     offer(kWide, 0, rounds + (left == 0 ? 0 : (left <= 160 ? 1.15 : 1.4) * turns + ends));
-    if (left > 0) {
+    if (left > 0 && may_split) {
         const Slices c = slices_of((int32_t)left);
         const double each = (double)turns / c.s + (c.r > 0 ? (double)turns / c.t : 0);
         if (turns >= 2 * c.s && turns >= c.t)       // two reduction tiles to a slice, one to the others
@@ -1035,13 +1022,14 @@ static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym
     return best;
 }
 
-// What a group of matrices has in the workspace, in this order: X hi twice and lo, A and
-// b A + c A A, their diagonals, the partial sums of squares, those of split tiles.
+// What a group of matrices has in the workspace, in this order: X twice, A and b A + c A A, hi
+// and then lo of each, the diagonals, the partial sums of squares, those of split tiles.
 struct OrthShape {
     int64_t Rp, Cp, m;              // padded sides, the smaller one
     int64_t x, a;                   // elements
     size_t each;                    // bytes of a matrix
     int64_t group;                  // matrices at a time
+    bool may_split;
     size_t part;                    // bytes of split tiles' partial sums
 };
 static OrthShape shape_of(int64_t batch, int64_t rows, int64_t cols) {
@@ -1051,16 +1039,17 @@ static OrthShape shape_of(int64_t batch, int64_t rows, int64_t cols) {
     s.m = s.Rp < s.Cp ? s.Rp : s.Cp;
     s.x = s.Rp * s.Cp;
     s.a = s.m * s.m;
-    s.each = (size_t)(5 * s.x + 4 * s.a + 8 * s.m) + kSquareParts * sizeof(double);
+    s.each = (size_t)(8 * s.x + 8 * s.a + 8 * s.m) + kSquareParts * sizeof(double);
     const int64_t most = (int64_t)((size_t(4) << 30) / s.each);
     s.group = most < 1 ? 1 : most > 16384 ? 16384 : most;     // a grid's y
     if (s.group > batch) s.group = batch;
-    // the last group may have fewer matrices, and split what the others need not
-    const int64_t last = batch - (batch - 1) / s.group * s.group, gram = (rows > cols ? s.Rp : s.Cp) / kBR, square = s.m / kBR;
-    bool split = false;
-    for (const int64_t n : {s.group, last})
-        split = split || plan_of(n, s.m, s.m, gram, true).split || plan_of(n, s.m, s.m, square, true).split ||
-                plan_of(n, s.Rp, s.Cp, square, false).split;
+    // Groups of a longer stack are 4 GiB of matrices, whose tiles go round the chip many times: what
+    // a split would save of the last round is little, and its partial sums are 128 MB.
+    s.may_split = s.group == batch || s.group == 1;
+    const int64_t gram = turns_of(rows > cols ? s.Rp : s.Cp), square = turns_of(s.m), n = s.group;
+    const bool split = plan_of(n, s.m, s.m, gram, true, s.may_split).split ||
+                       plan_of(n, s.m, s.m, square, true, s.may_split).split ||
+                       plan_of(n, s.Rp, s.Cp, square, false, s.may_split).split;
     s.part = split ? 2 * kSplit * kPartFloats * sizeof(float) : 0;
     return s;
 }
@@ -1100,17 +1089,16 @@ static hipError_t run(const OrthPlan& plan, OrthArgs g, int64_t n, hipStream_t s
     return hipGetLastError();
 }
 template <int OP, bool TA, bool TB>
-static hipError_t product(const OrthArgs& g, int64_t n, hipStream_t st) {
-    return run<OP, TA, TB>(plan_of(n, g.P, g.Q, g.turns, symmetric(OP)), g, n, st);
+static hipError_t product(const OrthArgs& g, int64_t n, bool may_split, hipStream_t st) {
+    return run<OP, TA, TB>(plan_of(n, g.P, g.Q, g.turns, symmetric(OP), may_split), g, n, st);
 }
 
 static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t first, int64_t n, hipStream_t st) {
     const int64_t x_all = s.group * s.x, a_all = s.group * s.a;
-    _Float16* hi[2] = {static_cast<_Float16*>(d.ws), static_cast<_Float16*>(d.ws) + x_all};
-    uint8_t* const lo = reinterpret_cast<uint8_t*>(hi[1] + x_all);
-    _Float16* const A = reinterpret_cast<_Float16*>(lo + x_all);
-    _Float16* const B = A + a_all;
-    float* const da = reinterpret_cast<float*>(B + a_all);
+    _Float16* const xs[2] = {static_cast<_Float16*>(d.ws), static_cast<_Float16*>(d.ws) + 2 * x_all};
+    _Float16* const A = xs[1] + 2 * x_all;
+    _Float16* const B = A + 2 * a_all;
+    float* const da = reinterpret_cast<float*>(B + 2 * a_all);
     float* const db = da + s.group * s.m;
     double* const parts = reinterpret_cast<double*>(db + s.group * s.m);
     float* const part = reinterpret_cast<float*>(parts + s.group * kSquareParts);
@@ -1126,8 +1114,8 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
     b.cols = d.cols;
     b.Rp = s.Rp;
     b.Cp = s.Cp;
-    b.hi = hi[0];
-    b.lo = lo;
+    b.hi = xs[0];
+    b.low = x_all;
     b.parts = parts;
     b.eps = d.eps;
     // a chunk to a thread while all workgroups run at once, else four (768 x 768 4.2 us in place
@@ -1144,7 +1132,7 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
     if ((e = hipGetLastError()) != hipSuccess) return e;
 
     for (int k = 0; k < d.steps; ++k) {
-        const _Float16* const X = hi[k & 1];
+        const _Float16* const X = xs[k & 1];
         OrthArgs g{};
         g.ca = (float)d.coefficients[3 * k];
         g.cb = (float)d.coefficients[3 * k + 1];
@@ -1154,46 +1142,50 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
         // A
         OrthArgs p = g;
         p.a = p.b = X;
+        p.low_a = p.low_b = x_all;
         p.lda = p.ldb = s.Cp;
         p.step_a = p.step_b = s.x;
         p.P = p.Q = s.m;
-        p.turns = (int32_t)((tall ? s.Rp : s.Cp) / kBR);
+        p.turns = (int32_t)turns_of(tall ? s.Rp : s.Cp);
         p.out = A;
+        p.low_out = a_all;
         p.ld_out = s.m;
         p.step_out = s.a;
         p.diag_out = da;
-        e = tall ? product<kGram, true, true>(p, n, st) : product<kGram, false, false>(p, n, st);
+        e = tall ? product<kGram, true, true>(p, n, s.may_split, st) : product<kGram, false, false>(p, n, s.may_split, st);
         if (e != hipSuccess) return e;
         // b A + c A A
         p = g;
         p.a = p.b = p.in = A;
+        p.low_a = p.low_b = p.low_in = p.low_out = a_all;
         p.lda = p.ldb = p.ld_in = p.ld_out = s.m;
         p.step_a = p.step_b = p.step_in = p.step_out = s.a;
         p.P = p.Q = s.m;
-        p.turns = (int32_t)(s.m / kBR);
+        p.turns = (int32_t)turns_of(s.m);
         p.diag_in = da;
         p.out = B;
         p.diag_out = db;
-        if ((e = product<kSquare, false, false>(p, n, st)) != hipSuccess) return e;
+        if ((e = product<kSquare, false, false>(p, n, s.may_split, st)) != hipSuccess) return e;
         // X; b A + c A A is symmetric, and so an operand with its outer index in rows on either side
         p = g;
         p.a = tall ? X : B;
         p.b = tall ? B : X;
+        p.low_a = tall ? x_all : a_all;
+        p.low_b = tall ? a_all : x_all;
         p.lda = tall ? s.Cp : s.m;
         p.ldb = tall ? s.m : s.Cp;
         p.step_a = tall ? s.x : s.a;
         p.step_b = tall ? s.a : s.x;
         p.P = s.Rp;
         p.Q = s.Cp;
-        p.turns = (int32_t)(s.m / kBR);
+        p.turns = (int32_t)turns_of(s.m);
         p.in = X;
+        p.low_in = p.low_out = x_all;
         p.ld_in = p.ld_out = s.Cp;
         p.step_in = p.step_out = s.x;
-        p.lo = lo;
         p.diag_in = db;
-        p.low = d.steps - 1 - k <= 2;
         if (k + 1 < d.steps) {
-            p.out = hi[(k + 1) & 1];
+            p.out = xs[(k + 1) & 1];
         } else {
             p.o = d.o + first * d.stride_o;
             p.ld_o = d.ld_o;
@@ -1202,7 +1194,7 @@ static hipError_t orthogonalize(const OrthDesc& d, const OrthShape& s, int64_t f
             p.cols = d.cols;
             p.scale = d.scale;
         }
-        e = tall ? product<kUpdateTall, false, false>(p, n, st) : product<kUpdate, false, true>(p, n, st);
+        e = tall ? product<kUpdateTall, false, false>(p, n, s.may_split, st) : product<kUpdate, false, true>(p, n, s.may_split, st);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
