@@ -83,7 +83,10 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * hold, whatever number format they were made in. Before o is rounded the result is therefore,
  * with the default coefficients, at most 2^-20 times the product of the steps' a's of its norm
  * from the formula's (5e-4 for five steps; 2e-4 was not passed, by matrices of rank 1, and
- * 2e-5 where no singular value is 0), 1 to 4 times what fp32 operations leave. X's elements must stay below 16 and those of A and b A + c A A off their
+ * 2e-5 where no singular value is 0), 1 to 4 times what fp32 operations leave. Steps whose a's,
+ * those below 1 in magnitude left out, multiply to more than 2^13 are refused (with the default
+ * coefficients more than seven): a matrix of low rank would come out of them, in 32 bits, wrong
+ * in the second digit. X's elements must stay below 16 and those of A and b A + c A A off their
  * diagonals below 64, as they do for coefficients that keep the singular values below 3;
  * beyond, results are NaN. A matrix of zeros gives zeros. A matrix that holds an infinity
  * or a NaN gives NaN in all its elements, and does not reach the others. The sum of squares
@@ -92,8 +95,8 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * matrix at least. The same call gives the same bits; how sums are split, and so a
  * result's last bits, depends on the sizes and on how many matrices there are.
  * Errors: ZERO_E_INVAL (NULL, an unknown type, steps outside [1, 64], eps not in
- * [1e-30, 1e30], scale or a coefficient not finite or beyond 1e4 in magnitude, overlap of the extents of x,
- * o and the workspace), ZERO_E_ALIGN (a pointer not aligned to its element, a workspace
+ * [1e-30, 1e30], scale or a coefficient not finite or beyond 1e4 in magnitude, a's that multiply
+ * to more than 2^13, overlap of the extents of x, o and the workspace), ZERO_E_ALIGN (a pointer not aligned to its element, a workspace
  * not to 16 bytes), ZERO_E_RANGE (batch outside [0, 2^31 - 1], the smaller side above 2^15
  * or the larger above 2^20, an ld below cols or above 2^40, a batch stride below a
  * matrix's extent or above 2^50, a workspace below zero_orthogonalize_workspace_bytes),

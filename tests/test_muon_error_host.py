@@ -54,3 +54,28 @@ def test_a_table_of_larger_gains():
     x = E.matrix("rank6", 200, 300, np.random.default_rng(4))
     want, allowed = E.growth(x, coefficients=E.TABLE)
     assert np.linalg.norm(E.model(x, coefficients=E.TABLE) - want) <= allowed
+
+
+def test_steps_that_would_grow_roundings_are_refused():
+    """The product of the a's above 1 is bounded, where there is nothing to do as well: seven steps
+    of the default coefficients, twelve of a = 2, any number of a at most 1."""
+    import ctypes
+
+    import zero_partitioned_optimizer_amd as Z
+    from zero_partitioned_optimizer_amd import _binding as B
+    from zero_partitioned_optimizer_amd import muon as M
+
+    def call(steps, triples=None, batch=0):
+        flat = None if triples is None else [v for t in triples for v in t]
+        a = Z.zero_orthogonalize_args(batch=batch, rows=4, cols=4, steps=steps, eps=1e-7, scale=1.0, x_dtype=B.ZERO_F32,
+                                      ld_x=4, ld_o=4,
+                                      coefficients=None if flat is None else (ctypes.c_double * len(flat))(*flat))
+        return M._lib().zero_orthogonalize(a, None)
+
+    for steps, triples in ((7, None), (13, [(2.0, -1.5, 0.5)] * 13), (5, E.TABLE), (64, [(1.0, -0.5, 0.0)] * 64),
+                           (64, [(0.25, 0.0, 0.0)] * 63 + [(8192.0, 0.0, 0.0)])):
+        assert call(steps, triples) == B.ZERO_OK
+    for steps, triples in ((8, None), (64, None), (14, [(2.0, -1.5, 0.5)] * 14), (14, [(-2.0, 1.5, -0.5)] * 14),
+                           (5, [E.TABLE[0]] * 5)):
+        for batch in (0, 1):
+            assert call(steps, triples, batch) == B.ZERO_E_INVAL and "multiply to" in Z.zero_last_error()

@@ -176,7 +176,8 @@ def zero_orthogonalize(x, *, out=None, steps: int = 5, coefficients=ZERO_MUON_CO
     """scale times the nearly semi-orthogonal matrix of x [R, C], or of each matrix of a
     stack [B, R, C] (bfloat16 or float32, rows and matrices at any stride): X = x / (|x| +
     eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T. ``coefficients``:
-    (a, b, c), or one such triple for each step. Returns ``out`` (bfloat16, x's shape; new
+    (a, b, c), or one such triple for each step; the steps' |a|, where above 1, may multiply to
+    8192 (seven steps of the default ones). Returns ``out`` (bfloat16, x's shape; new
     if None)."""
     fn = "zero_orthogonalize"
     dev = _on_device(fn, "x", x)
