@@ -82,13 +82,15 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * last two fp32. A step multiplies by a what roundings leave in directions that x does not
  * hold, whatever number format they were made in. Before o is rounded the result is therefore,
  * with the default coefficients, at most 2^-20 times the product of the steps' a's of its norm
- * from the formula's (5e-4 for five steps; 2e-4 was not passed, by matrices of rank 1, and
- * 2e-5 where no singular value is 0), 1 to 4 times what fp32 operations leave. Steps whose a's,
+ * from the formula's (5e-4 for five steps; a model of the roundings gives 2e-4 at rank
+ * 1, 1e-5 at rank 32 and 1e-6 for normal numbers), 1 to 4 times what fp32 operations leave. Steps whose a's,
  * those below 1 in magnitude left out, multiply to more than 2^13 are refused (with the default
  * coefficients more than seven): a matrix of low rank would come out of them, in 32 bits, wrong
  * in the second digit. X's elements must stay below 16 and those of A and b A + c A A off their
  * diagonals below 64, as they do for coefficients that keep the singular values below 3;
- * beyond, results are NaN. A matrix of zeros gives zeros. A matrix that holds an infinity
+ * beyond, every element of o that the formula makes of such an element is NaN: all of its matrix,
+ * but for the rows (of a matrix taller than wide: columns) that an element of the last step's
+ * b A + c A A does not belong to. A matrix of zeros gives zeros. A matrix that holds an infinity
  * or a NaN gives NaN in all its elements, and does not reach the others. The sum of squares
  * is fp64: no scale of x overflows it.
  * Matrices are processed in groups whose intermediate results take 4 GiB at most, one

@@ -62,3 +62,38 @@ def test_near_the_formula_by_every_kind_of_tile(Z, size):
     want = (X.transpose(1, 2) if r > c else X).cpu().numpy()
     off = E.beyond_rounding(o.double().cpu().numpy(), want)
     assert off <= 2 * error, (off, 2 * error, float(X.norm()))
+
+
+@pytest.mark.parametrize("tall", [False, True])
+def test_what_passes_the_range_is_nan(Z, tall):
+    """Elements of X from 16 and of A and b A + c A A from 64 on, in a middle step: NaN all over, in
+    that matrix alone. An element (0, 1) of the last step's b A + c A A: rows (or columns) 0 and 1,
+    and the others are the formula's, which does not use it for them."""
+    rng = np.random.default_rng(9)
+
+    def run_both(x, **kw):
+        other = rng.standard_normal(x.shape).astype(np.float32)
+        both = np.stack([x, other, x])
+        o = run(Z, np.ascontiguousarray(both.transpose(0, 2, 1)) if tall else both, **kw)
+        return o.transpose(0, 2, 1) if tall else o, other
+
+    # rows 0 and 1 half alike, the others orthogonal to all: A is 0.1 at (0, 1) and 0.2 on the diagonal
+    q = np.linalg.qr(rng.standard_normal((300, 5)))[0].T
+    q[1] = 0.5 * q[0] + np.sqrt(0.75) * q[1]
+    x = q.astype(np.float32)
+    kw = dict(steps=1, coefficients=(1.0, 1000.0, 0.0))
+    say("beyond the range", tall)
+    o, _ = run_both(x, **kw)
+    assert np.isnan(o[0, :2]).all() and np.isnan(o[2, :2]).all()
+    want = E.R.orthogonalize(x, **kw)[2:]
+    # 201 x, its roundings in 32 bits a hundredth of bf16's half step
+    assert np.abs(o[[0, 2], 2:] - want).max() <= 2.0 ** -8 * np.abs(want).max() * 1.01
+    # X of one large element: 0.9 * 20 in the second step
+    x = np.full((5, 300), 0.01, np.float32)
+    x[3, 7] = 1.0
+    o, _ = run_both(x, steps=2, coefficients=[(20.0, 0.0, 0.0), (1.0, -0.5, 0.0)])
+    assert np.isnan(o[[0, 2]]).all() and np.isfinite(o[1]).all()
+    # A of rank 1, 8100 / 64 off its diagonal in the second step, X's own elements 90 / 140
+    x = np.ones((64, 300), np.float32)
+    o, _ = run_both(x, steps=2, coefficients=[(90.0, 0.0, 0.0), (1.0, -0.5, 0.0)])
+    assert np.isnan(o[[0, 2]]).all()
