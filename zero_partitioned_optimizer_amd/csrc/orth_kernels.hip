@@ -378,6 +378,13 @@ struct OrthEpilogue<kUpdateTall> : UpdateEpilogue<true> {
 };
 constexpr bool symmetric(int op) { return op < kUpdate; }
 
+// What lanes of a wave have written to LDS, other lanes of it may read: LDS operations of a wave
+// are done in their order, and the compiler keeps them in it.
+__device__ __forceinline__ void meet_lanes() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // A wave's blocks, four times FQ at a time, through its part of LDS (64 rows of 16 FQ floats),
 // so that a lane has eight consecutive columns, the same in all its rows of a run. Blocks are
 // computed as (q, p): a lane holds four consecutive columns of a row, a 16-byte unit, unit u
@@ -429,6 +436,7 @@ struct Finish {
                     const int o = 16 * i + (lane & 15), u = 4 * j + (lane >> 4);
                     *reinterpret_cast<v4f*>(mine + kCols * o + 4 * (u ^ (o & kMask))) = acc[i][FQ * run + j];
                 }
+            meet_lanes();
 #pragma unroll
             for (int u = 0; u < kRows; ++u) {
                 const int o = o0 + kStep * u;
@@ -442,6 +450,7 @@ struct Finish {
                 }
                 load(run * kRows + u + kAhead);
             }
+            if (symmetric(OP) && mirror) meet_lanes();
             if (symmetric(OP) && mirror && row(8 * r) < g.P) {
 #pragma unroll 2
                 for (int j = lane >> 3; j < kCols; j += 8) {
@@ -455,6 +464,7 @@ struct Finish {
                     if (q < g.Q) put_pairs(g.out + m * g.step_out + q * g.ld_out + row(8 * r), g.low_out, v);
                 }
             }
+            if (run + 1 < RUNS) meet_lanes();
         }
     }
 };
