@@ -119,3 +119,10 @@ TABLE = [(8.28721201814563, -23.595886519098837, 17.300387312530933),
          (3.9486908534822946, -2.908902115962949, 0.5518191394370137),
          (3.3184196573706015, -2.488488024314874, 0.51004894012372),
          (2.300652019954817, -1.6689039845747493, 0.4188073119525673)]
+
+# (batch, rows, columns) whose products are cut in every way there is: tests/c/orth_plans.cpp
+# prints how, tests/test_muon_plan.py holds that none is missing
+PLAN_SIZES = [(1, 65, 70), (1, 67, 64), (1, 70, 12552), (1, 1835, 9244), (1, 2924, 2844), (1, 12659, 65), (2, 8470, 969),
+              (3, 67, 8558), (3, 8840, 64), (6, 2449, 2309), (8, 1961, 2224), (8, 2008, 1956), (12, 513, 580),
+              (12, 558, 521), (12, 774, 883), (12, 786, 785), (12, 1029, 1277), (12, 1047, 1041), (12, 1614, 2193),
+              (1, 11008, 4096), (1, 4096, 11008)]

@@ -97,3 +97,35 @@ def test_what_passes_the_range_is_nan(Z, tall):
     x = np.ones((64, 300), np.float32)
     o, _ = run_both(x, steps=2, coefficients=[(90.0, 0.0, 0.0), (1.0, -0.5, 0.0)])
     assert np.isnan(o[[0, 2]]).all()
+
+
+@pytest.mark.parametrize("size", E.PLAN_SIZES, ids=str)
+def test_near_the_formula_however_the_products_are_cut(Z, size):
+    """Every kind of tile, whole, split in one part and in two, of wide and tall matrices, against the
+    formula in 64 bits on the device, matrix by matrix; the allowance with s = 1.3 as above."""
+    B, r, c = size
+    g = torch.Generator(device=dev()).manual_seed(r * c)
+    x = torch.randn(B, r, 12, generator=g, device=dev()) @ torch.randn(B, 12, c, generator=g, device=dev())
+    x += 0.3 * torch.randn(B, r, c, generator=g, device=dev())
+    say("orthogonalize", size)
+    o = Z.zero_orthogonalize(x)
+    assert torch.equal(o, Z.zero_orthogonalize(x))
+    X = x.double()
+    X = X / X.square().sum((1, 2), keepdim=True).sqrt()
+    X = X.transpose(1, 2).contiguous() if r > c else X
+    ca, cb, cc = E.R.COEF
+    at = np.linspace(0, 1.3, 200)
+    gain = np.abs(ca + 3 * cb * at ** 2 + 5 * cc * at ** 4).max()
+    fresh = 2.0 ** -23 * (abs(ca) + abs(cb) * 1.3 ** 2 + abs(cc) * 1.3 ** 4)
+    error = torch.full((B,), 2.0 ** -23, dtype=torch.float64, device=dev())
+    for _ in range(5):
+        error = error * gain + fresh * X.square().sum((1, 2)).sqrt()
+        A = torch.bmm(X, X.transpose(1, 2).contiguous())
+        X = ca * X + torch.bmm(cb * A + cc * torch.bmm(A, A), X)
+    o = o.double()
+    o = o.transpose(1, 2) if r > c else o
+    half = torch.ldexp(torch.ones_like(X), torch.frexp(torch.maximum(o.abs(), X.abs())).exponent - 9)
+    off = ((o - X).abs() - half).clamp(min=0).square().sum((1, 2)).sqrt()
+    assert bool((off <= 2 * error).all()), (off / error).tolist()
+    # and nowhere by more than 25 standard deviations of that
+    assert float(((o - X).abs() - half).max()) <= 25 * float((2 * error).max()) / (r * c) ** 0.5

@@ -30,6 +30,7 @@
 
 #include "layer_device.h"
 #include "muon_internal.h"
+#include "orth_plan.h"
 
 namespace zk {
 
@@ -37,11 +38,7 @@ typedef _Float16 h8 __attribute__((ext_vector_type(8)));
 typedef short s4 __attribute__((ext_vector_type(4)));
 typedef int v4i __attribute__((ext_vector_type(4)));
 
-constexpr int kBR = 64;                     // reduction elements per staged tile
-constexpr int kTerms = 3;                   // of a product of pairs: hi hi, hi lo, lo hi
-constexpr int kSide = 128;                  // all sides are padded to this, with zeros
 constexpr float kScale = 1024.0f, kScaleX = 4096.0f;
-constexpr int kSquareParts = 256;           // partial sums of squares of a matrix, at most
 
 enum OrthOp { kGram, kSquare, kUpdate, kUpdateTall };        // of a matrix that is taller than wide
 
@@ -725,8 +722,7 @@ __global__ void __launch_bounds__(512) k_orth_mid(const OrthArgs g) {
 // four, made the Gram product of 4096 x 11008 take 242 us in place of 200; half of the first
 // turn's reads a turn ahead, 12 KB in every turn in place of 16 and 8, 208 us there, and the
 // update's 340 in place of 348; the 32 x 32 matrix instruction, with four turns, 5-8% more.) The
-// 512 whole tiles of the update of 11008 x 4096 take 575 to 600 us, 1.37 to 1.43 PFLOP/s in three
-// terms; the other 176 are split, 229 to 244 and 36 to 42 for the join.
+// 688 tiles of the update of 11008 x 4096 take 813 us, 1.36 PFLOP/s in three terms.
 //
 // The workgroup takes reduction tiles first .. last of output tile `t`: WHOLE, or a part,
 // whose sums go to memory for k_orth_join, a wave's as they lie in its registers.
@@ -833,7 +829,7 @@ __global__ void __launch_bounds__(512) k_orth_wide(const OrthArgs g) {
     wide_tile<OP, TA, TB, true>(g, g.first + in_turn(g.all), 0, g.turns, lds, nullptr);
 }
 
-// Fewer tiles than kSplit, shared by kSplit workgroups, all of them at the same place of the
+// Fewer tiles than kSplit, shared by kSplit workgroups (Slices), all of them at the same place of the
 // reduction as those that share operand rows with them: workgroup w < a s takes slice w / a of
 // s of tile w % a; the r tiles that are left over are cut likewise, into t slices, for a
 // second part of each workgroup's work. k_orth_join puts the parts together, in order.
@@ -841,20 +837,6 @@ __global__ void __launch_bounds__(512) k_orth_wide(const OrthArgs g) {
 // with one term a product, the Gram product of 4096 x 11008 took 240 us in place of 180.) As it
 // is the Gram product of 11008 x 4096 takes 477 to 512 us and its join 44 to 46, by the 128 MB of
 // sums between them; the square 180 to 192 and 42 to 44.
-constexpr int kSplit = 256;
-constexpr int64_t kPartFloats = 256 * 256;
-struct Slices {
-    int32_t s, a, r, t;
-};
-__host__ __device__ __forceinline__ Slices slices_of(int32_t tiles) {
-    Slices c;
-    c.s = (kSplit + tiles - 1) / tiles;
-    c.a = kSplit / c.s;
-    c.r = tiles - c.a;
-    c.t = c.r > 0 ? kSplit / c.r : 0;
-    return c;
-}
-
 template <int OP, bool TA, bool TB>
 __global__ void __launch_bounds__(512) k_orth_split(const OrthArgs g) {
     __shared__ __attribute__((aligned(16))) _Float16 lds[2 * 4 * kSide * kBR];
@@ -988,81 +970,6 @@ __global__ void __launch_bounds__(256) k_orth_start(const StartArgs g) {
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-
-static int64_t padded(int64_t n) { return (n + kSide - 1) / kSide * kSide; }
-static int64_t turns_of(int64_t R) { return kTerms * R / kBR; }
-
-static int64_t over(int64_t n, int64_t by) { return (n + by - 1) / by; }
-static int64_t tiles_of(int64_t P, int64_t Q, int64_t side, bool sym) {
-    const int64_t p = over(P, side), q = over(Q, side);
-    return sym ? p * (p + 1) / 2 : p * q;
-}
-
-// How a product of n matrices runs, by an estimate of its time in microseconds.
-enum OrthKind { kFew, kMid, kTwo, kWide };
-struct OrthPlan {
-    OrthKind kind;
-    int64_t split;                  // kWide: of all tiles, the last ones that are split
-};
-static OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym, bool may_split) {
-    const int64_t few = n * tiles_of(P, Q, 64, sym), mid = n * tiles_of(P, Q, 128, sym), wide = n * tiles_of(P, Q, 256, sym);
-    OrthPlan best{kTwo, 0};
-    double least = 1e300;
-    const auto offer = [&](OrthKind k, int64_t split, double time) {
-        if (time < least) {
-            least = time;
-            best = OrthPlan{k, split};
-        }
-    };
-    // us for a turn and for a tile's start and end, in a round of the chip:
-    // measured at 768 x 768 to 4096 x 11008, one matrix to twelve
-    const int64_t rest = mid % 512;
-    offer(kTwo, 0, mid / 512 * (0.9 * turns + 9) + (rest == 0 ? 0 : rest <= 256 ? 0.65 * turns + 8.5 : 0.9 * turns + 9));
-    offer(kFew, 0, over(few, 256) * (0.185 * turns + 3.4));
-    if (mid <= 256) offer(kMid, 0, 0.49 * turns + 8.5);
-    const int64_t left = wide % kSplit;
-    const double ends = sym ? 12 : 18, rounds = wide / 256 * (1.4 * turns + ends);
-    offer(kWide, 0, rounds + (left == 0 ? 0 : (left <= 160 ? 1.15 : 1.4) * turns + ends));
-    if (left > 0 && may_split) {
-        const Slices c = slices_of((int32_t)left);
-        const double each = (double)turns / c.s + (c.r > 0 ? (double)turns / c.t : 0);
-        if (turns >= 2 * c.s && turns >= c.t)       // two reduction tiles to a slice, one to the others
-            offer(kWide, left, rounds + 1.4 * each + 15 + 0.088 * (c.a * c.s + c.r * c.t));
-    }
-    return best;
-}
-
-// What a group of matrices has in the workspace, in this order: X twice, A and b A + c A A, hi
-// and then lo of each, the diagonals, the partial sums of squares, those of split tiles.
-struct OrthShape {
-    int64_t Rp, Cp, m;              // padded sides, the smaller one
-    int64_t x, a;                   // elements
-    size_t each;                    // bytes of a matrix
-    int64_t group;                  // matrices at a time
-    bool may_split;
-    size_t part;                    // bytes of split tiles' partial sums
-};
-static OrthShape shape_of(int64_t batch, int64_t rows, int64_t cols) {
-    OrthShape s{};
-    s.Rp = padded(rows);
-    s.Cp = padded(cols);
-    s.m = s.Rp < s.Cp ? s.Rp : s.Cp;
-    s.x = s.Rp * s.Cp;
-    s.a = s.m * s.m;
-    s.each = (size_t)(8 * s.x + 8 * s.a + 8 * s.m) + kSquareParts * sizeof(double);
-    const int64_t most = (int64_t)((size_t(4) << 30) / s.each);
-    s.group = most < 1 ? 1 : most > 16384 ? 16384 : most;     // a grid's y
-    if (s.group > batch) s.group = batch;
-    // Groups of a longer stack are 4 GiB of matrices, whose tiles go round the chip many times: what
-    // a split would save of the last round is little, and its partial sums are 128 MB.
-    s.may_split = s.group == batch || s.group == 1;
-    const int64_t gram = turns_of(rows > cols ? s.Rp : s.Cp), square = turns_of(s.m), n = s.group;
-    const bool split = plan_of(n, s.m, s.m, gram, true, s.may_split).split ||
-                       plan_of(n, s.m, s.m, square, true, s.may_split).split ||
-                       plan_of(n, s.Rp, s.Cp, square, false, s.may_split).split;
-    s.part = split ? 2 * kSplit * kPartFloats * sizeof(float) : 0;
-    return s;
-}
 
 size_t orth_ws_bytes(int64_t batch, int64_t rows, int64_t cols) {
     if (batch < 1 || rows < 1 || cols < 1) return 0;
