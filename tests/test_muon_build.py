@@ -73,14 +73,3 @@ def test_headers_are_plain_c(tmp_path):
                    "int (*g)(const zero_orthogonalize_args*, void*) = zero_orthogonalize;\n")
     subprocess.run(["gcc", "-std=c11", "-Wall", "-Werror", "-pedantic", "-I", os.path.join(ROOT, "include"), "-c", str(src),
                     "-o", str(tmp_path / "h.o")], check=True)
-
-
-def test_lanes_that_exchange_rows_through_lds_meet():
-    """Between a wave's writes to its part of LDS and other lanes' reads of them stands a fence, and
-    one before the next run's writes."""
-    from zero_partitioned_optimizer_amd import build as B
-    text = open(os.path.join(B.CSRC, "orth_kernels.hip")).read()
-    assert re.search(r'void meet_lanes\(\) \{\s*__builtin_amdgcn_fence\(__ATOMIC_ACQ_REL, "wavefront", "local"\);\s*'
-                     r'__builtin_amdgcn_wave_barrier\(\);', text)
-    finish = text[text.index("struct Finish {"):text.index("// products\n")]
-    assert finish.count("meet_lanes();") == 3

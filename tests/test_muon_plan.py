@@ -1,6 +1,7 @@
 """How the products of an orthogonalisation are cut into tiles (CPU only): the sizes that the GPU
 tests run reach every kind of tile and every way to split them, for each product."""
 import os
+import re
 import shutil
 import subprocess
 
@@ -67,3 +68,13 @@ def test_workspace_holds_what_the_plan_needs(plans):
         each = 8 * R * C + 8 * m * m + 8 * m + 8 * 256
         part = 2 * 256 * 256 * 256 * 4 if any("split" in w for w in ways) else 0
         assert Z.zero_orthogonalize_workspace_bytes(b, r, c) == b * each + part
+
+
+def test_lanes_that_exchange_rows_through_lds_meet():
+    """Between a wave's writes to its part of LDS and other lanes' reads of them stands a fence, and
+    one before the next run's writes."""
+    text = open(os.path.join(B.CSRC, "orth_kernels.hip")).read()
+    assert re.search(r'void meet_lanes\(\) \{\s*__builtin_amdgcn_fence\(__ATOMIC_ACQ_REL, "wavefront", "local"\);\s*'
+                     r'__builtin_amdgcn_wave_barrier\(\);', text)
+    finish = text[text.index("struct Finish {"):text.index("// products\n")]
+    assert finish.count("meet_lanes();") == 3
