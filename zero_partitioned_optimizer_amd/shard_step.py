@@ -551,11 +551,12 @@ class MuonShardStep:
         """Enqueue the first part: the averaged gradient and its record."""
         if len(replicas) != self.N:
             raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: {len(replicas)} replicas, not {self.N}")
-        size = 4 if self.grad_dtype == B.ZERO_F32 else 2
+        # bf16 also as its bit patterns, as in a slot
+        types = (torch.float32,) if self.grad_dtype == B.ZERO_F32 else (torch.bfloat16, torch.int16)
         for r in replicas:
-            if r.device != self.p.device or not r.is_contiguous() or r.numel() < self.S or r.element_size() != size:
+            if r.device != self.p.device or not r.is_contiguous() or r.numel() < self.S or r.dtype not in types:
                 raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a replica of {r.numel()} elements, {r.dtype} on "
-                                  f"{r.device}, not {self.S} contiguous ones of {size} bytes on {self.p.device}")
+                                  f"{r.device}, not {self.S} contiguous ones of {types[0]} on {self.p.device}")
         B.zero_reduce_shard(replicas, self.grad_dtype, self.S, self.stats, self.ws, loss_scale=self.state.loss_scale,
                             grad_out=self.g, stream=stream)
 
