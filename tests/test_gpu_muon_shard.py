@@ -31,3 +31,41 @@ def test_replicas_of_another_type_are_refused(Z):
     bits[0].step([t.bfloat16()])
     bits[1].step([t.bfloat16().view(torch.int16)])
     assert torch.equal(bits[0].master, bits[1].master) and bits[0].t == 1
+
+
+BAD = [dict(lr=-0.1), dict(lr=float("nan")), dict(weight_decay=float("inf")), dict(mu=1.0), dict(steps=0), dict(steps=8),
+       dict(eps=0.0), dict(coefficients=(1.0, float("nan"), 0.0)), dict(coefficients=[(1.0, 2.0, 3.0)] * 4),
+       dict(scale=lambda r, c: 1e9)]
+
+
+@pytest.mark.parametrize("bad", BAD, ids=str)
+def test_bad_hyperparameters_are_refused_before_anything_is_written(Z, bad):
+    """By the constructor; and where they are set later, by a step that leaves its state as it was."""
+    with pytest.raises(Z.ZeroError):
+        new(Z, **bad)
+    if "scale" in bad:
+        return
+    step = new(Z)
+    g = torch.ones(64, device=dev())
+    step.step([g])
+    was = step.state_dict()
+    for group in (step.hyper, step.momentum_hyper, step.orth):
+        group.update({k: v for k, v in bad.items() if k in group})
+    with pytest.raises(Z.ZeroError):
+        step.step([g])
+    torch.cuda.synchronize()
+    now = step.state_dict()
+    assert torch.equal(was["m"], now["m"]) and torch.equal(was["p"], now["p"]) and now["t"] == 1
+    assert torch.equal(step.slot.view(BF), step.master.to(BF))
+
+
+def test_a_slot_that_is_not_the_shards_is_refused(Z):
+    for slot in (torch.zeros(64, dtype=torch.int16), torch.zeros(128, dtype=torch.int16, device=dev())[::2],
+                 torch.zeros(63, dtype=torch.int16, device=dev()), torch.zeros(64, dtype=torch.float16, device=dev()),
+                 torch.zeros(8, 8, dtype=BF, device=dev())):
+        with pytest.raises(Z.ZeroError, match="slot is"):
+            new(Z, slot=slot)
+    mine = torch.zeros(64, dtype=BF, device=dev())
+    step = new(Z, slot=mine)
+    step.step([torch.ones(64, device=dev())])
+    assert step.slot is mine and torch.equal(mine, step.master.to(BF))

@@ -1,0 +1,18 @@
+"""MuonShardStep's refusals that need no GPU."""
+import pytest
+import torch
+
+import zero_partitioned_optimizer_amd as Z
+
+
+@pytest.mark.parametrize("bad,word", [
+    (dict(lr=-0.1), "lr="), (dict(weight_decay=float("nan")), "weight_decay="), (dict(mu=1.0), "mu="),
+    (dict(steps=0), "steps=0"), (dict(steps=65), "steps=65"), (dict(steps=9), "multiply to"), (dict(eps=0.0), "eps="),
+    (dict(coefficients=(1.0, 2.0)), "neither three numbers"), (dict(coefficients=(float("inf"), 0.0, 0.0)), "coefficient"),
+    (dict(scale=lambda r, c: 1e5), "scale="), (dict(matrices=[(0, 1 << 16, 1 << 16)]), "smaller side"),
+    (dict(matrices=[(0, 1, (1 << 20) + 1)]), "larger")], ids=str)
+def test_bad_values_are_refused_by_the_constructor(bad, word):
+    """Not by the last part of a step, which would leave it half done."""
+    kw = {"lr": 0.1, "matrices": [(0, 5, 10)], **bad}
+    with pytest.raises(Z.ZeroError, match=word):
+        Z.MuonShardStep(100, 1, Z.ZERO_F32, torch.zeros(100), kw.pop("matrices"), **kw)

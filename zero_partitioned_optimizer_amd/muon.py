@@ -159,6 +159,19 @@ def _coefficients(c):
     return None if c is None else tuple(tuple(t) if hasattr(t, "__len__") else t for t in c)
 
 
+def _check_step(shapes, *, mu, nesterov, lr, weight_decay, steps, coefficients, eps) -> None:
+    """Raises what the operators of a step would for these values and (rows, cols, scale) of
+    its matrices: the calls themselves, with nothing to do."""
+    bf16, f32 = B.ZERO_BF16, B.ZERO_F32
+    _enqueue("zero_muon_momentum", _MOMENTUM.pack(0, 0, 0, 0, f32, bf16, 1 if nesterov else 0, 0, mu, 0), 0)
+    _enqueue("zero_muon_update", _UPDATE.pack(0, 0, 0, 0, lr, weight_decay, 0), 0)
+    table = _table(_coefficients(coefficients), int(steps)) if 1 <= steps <= 64 else None
+    for rows, cols, scale in shapes:
+        _enqueue("zero_orthogonalize",
+                 _ORTH.pack(0, rows, cols, 0, cols, 0, 0, cols, 0, bf16, steps,
+                            ctypes.addressof(table) if table is not None else 0, eps, scale, 0, 0), 0)
+
+
 def _stack(fn: str, name: str, t: torch.Tensor, dtype, device: int):
     """(address, ld, batch stride) of a matrix or a stack of matrices."""
     if t.dim() == 2:

@@ -465,7 +465,8 @@ class MuonShardStep:
     ``scale(rows, cols)`` is what a matrix's orthogonal form is multiplied by; by default 0.2
     times the root of the larger side, which gives updates the root mean square of Adam's.
     On overflow nothing is written, on the device; the host keeps the loss scale, as
-    ``ShardStep`` does."""
+    ``ShardStep`` does. Hyperparameters (``hyper``, ``momentum_hyper``, ``orth``) may be changed between
+    steps. What ``exchange`` raises leaves a step half done: the momentum has taken its gradient."""
 
     def __init__(self, shard_S: int, n_replicas: int, grad_dtype: int, p0: torch.Tensor, matrices, *, lr: float,
                  shard_off: int = 0, mu: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, steps: int = 5,
@@ -485,7 +486,16 @@ class MuonShardStep:
                 raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: matrices at {a} and {b} overlap")
         if here and here[0][0] < 0:
             raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a matrix at {here[0][0]}")
+        if scale is None:
+            def scale(rows, cols):
+                return 0.2 * math.sqrt(max(rows, cols))
+        self.shapes = [(r, c, float(scale(r, c))) for r, c in sorted({(r, c) for _, r, c in here})]
+        self._check()
         muon._on_device("MuonShardStep", "p0", p0)
+        if slot is not None and (slot.device != dev or slot.dim() != 1 or not slot.is_contiguous() or slot.numel() != S
+                                 or slot.dtype not in (torch.bfloat16, torch.int16)):
+            raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: slot is {slot.dtype} of shape {tuple(slot.shape)} on "
+                              f"{slot.device}, not {S} contiguous bfloat16 or int16 on {dev}")
         self.u_off = min([lo] + [o for o, _, _ in here])
         end = max([lo + S] + [o + r * c for o, r, c in here])
         self.whole = self.u_off == lo and end == lo + S
@@ -497,24 +507,25 @@ class MuonShardStep:
         self.o = torch.zeros_like(self.u)
         at = lo - self.u_off
         self.u_shard, self.o_shard = self.u[at:at + S], self.o[at:at + S]
-        if scale is None:
-            def scale(rows, cols):
-                return 0.2 * math.sqrt(max(rows, cols))
+        scales = {(r, c): s for r, c, s in self.shapes}
         self.stacks = []
         for n, first, every, r, c in self._stacks(here):
             def view(flat):
                 return flat.as_strided((n, r, c), (every, c, 1), first - self.u_off)
-            self.stacks.append((view(self.u), view(self.o), float(scale(r, c))))
+            self.stacks.append((view(self.u), view(self.o), scales[r, c]))
         need = max([muon.zero_orthogonalize_workspace_bytes(*u.shape) for u, _, _ in self.stacks] + [16])
         self.orth_ws = torch.empty(need, dtype=torch.uint8, device=dev)
         self.slot = slot if slot is not None else torch.empty(S, dtype=torch.int16, device=dev)
-        assert self.slot.numel() == S and self.slot.element_size() == 2
         self.stats = torch.zeros(16, dtype=torch.uint8, device=dev)
         self.stats_host = torch.zeros(16, dtype=torch.uint8, pin_memory=True)
         self.ws = torch.empty(B.zero_workspace_bytes(S), dtype=torch.uint8, device=dev)
         self.state = B.zero_train_state(t=0, n_skipped=0, loss_scale=float(loss_scale),
                                         min_loss_scale=float(min_loss_scale), dynamic=int(dynamic))
         B.zero_gather_slot(self.p, S, self.slot)
+
+    def _check(self) -> None:
+        """Refuse what a later part of a step would, before an earlier one writes anything."""
+        muon._check_step(self.shapes, **self.momentum_hyper, **self.hyper, **self.orth)
 
     @staticmethod
     def _stacks(here):
@@ -561,7 +572,9 @@ class MuonShardStep:
                             grad_out=self.g, stream=stream)
 
     def momentum(self, stream=None) -> None:
-        """Enqueue the second part: the momentum and this shard's part of u, unless the record overflowed."""
+        """Enqueue the second part: the momentum and this shard's part of u, unless the record overflowed.
+        Hyperparameters that ``update`` would refuse are refused here, with the momentum as it was."""
+        self._check()
         muon.zero_muon_momentum(self.g, self.m, u=self.u_shard, stats=self.stats, stream=stream, **self.momentum_hyper)
 
     def update(self, stream=None) -> None:
