@@ -69,3 +69,42 @@ def test_a_slot_that_is_not_the_shards_is_refused(Z):
     step = new(Z, slot=mine)
     step.step([torch.ones(64, device=dev())])
     assert step.slot is mine and torch.equal(mine, step.master.to(BF))
+
+
+@pytest.mark.parametrize("given", [True, False])
+def test_what_no_matrix_holds_is_left_alone(Z, given):
+    """A norm and a bias between the matrices and an embedding behind them, with weight decay:
+    master copy and slot keep their bits, also where another optimizer has changed them in
+    between; the matrices are updated as in a shard of their own."""
+    S = 2000
+    mats = [(0, 10, 40), (400, 10, 40), (900, 20, 25), (1408, 12, 16)]
+    slot = torch.zeros(S, dtype=torch.int16, device=dev()) if given else None
+    step = new(Z, S, matrices=mats, weight_decay=0.1, slot=slot)
+    inside = torch.zeros(S, dtype=torch.bool, device=dev())
+    for o, r, c in mats:
+        inside[o:o + r * c] = True
+    inside[1400:1408] = True                    # padding between the last two
+    assert step.runs == [(0, 800), (900, 1600)]
+    rest = ~inside
+    p0 = step.master.clone()
+    say("a shard of matrices and others")
+    g = torch.Generator(device=dev()).manual_seed(1)
+    want = p0.clone()
+    for k in range(2):
+        held = step.slot.clone()
+        step.step([torch.randn(S, generator=g, device=dev())])
+        assert torch.equal(step.master[rest], p0[rest]) and torch.equal(step.slot[rest], held[rest])
+        want = torch.from_numpy(R.update(want.cpu().numpy(), step.o_shard.float().cpu().numpy(), 0.1, 0.1)).to(dev())
+        assert torch.equal(step.master[inside], want[inside])
+        assert torch.equal(step.slot.view(BF)[inside], want.to(BF)[inside])
+        # another optimizer's step
+        step.slot[rest] = 77 + k
+    # resumed: a slot that others write too keeps what is theirs
+    other = torch.full((S,), 5, dtype=torch.int16, device=dev()) if given else None
+    again = new(Z, S, matrices=mats, weight_decay=0.1, slot=other)
+    if given:
+        other[rest] = 9
+    again.load_state_dict(step.state_dict())
+    assert torch.equal(again.slot.view(BF)[inside], want.to(BF)[inside])
+    assert bool((again.slot[rest] == 9).all()) if given else torch.equal(again.slot.view(BF), again.master.to(BF))
+    assert torch.equal(again.master, step.master) and torch.equal(again.m, step.m)

@@ -448,8 +448,13 @@ class MuonShardStep:
 
     ``matrices``: (offset, rows, cols) of each in the flat buffer, row-major; the shard is
     its elements [shard_off, shard_off + shard_S). Matrices of one shape at even distances
-    are orthogonalised in one call. Elements of the shard outside every matrix have no
-    update, only their weight decay.
+    are orthogonalised in one call. Elements of the shard outside every matrix, norms, biases
+    and embeddings, are another optimizer's: their master copy and slot are left as they are (the
+    constructor casts all of p0 into the slot, ``load_state_dict`` all of it into a slot of its own). Only
+    gaps of fewer than ``padding`` elements behind a matrix, up to the next one or the end of
+    the shard, are taken for the layout's alignment padding, whose zeros the update passes over in one
+    go with the matrices. Where smaller tensors than that lie between matrices, or a tensor begins
+    so close to the shard's end behind the last matrix, pass ``padding=0``.
 
     A step has three parts, with the program's collectives between them:
       ``reduce(replicas)``  the averaged gradient and the overflow record ``stats``. Ranks
@@ -472,7 +477,7 @@ class MuonShardStep:
                  shard_off: int = 0, mu: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0, steps: int = 5,
                  coefficients=muon.ZERO_MUON_COEFFICIENTS, eps: float = 1e-7,
                  scale: Optional[Callable[[int, int], float]] = None, loss_scale: float = 1.0, dynamic: bool = False,
-                 min_loss_scale: float = 1.0, slot: Optional[torch.Tensor] = None):
+                 min_loss_scale: float = 1.0, slot: Optional[torch.Tensor] = None, padding: int = 16):
         dev = p0.device
         S, lo = int(shard_S), int(shard_off)
         assert p0.dtype == torch.float32 and p0.numel() == S and p0.is_contiguous()
@@ -499,6 +504,8 @@ class MuonShardStep:
         self.u_off = min([lo] + [o for o, _, _ in here])
         end = max([lo + S] + [o + r * c for o, r, c in here])
         self.whole = self.u_off == lo and end == lo + S
+        spans = sorted((int(o), int(r) * int(c)) for o, r, c in matrices if r * c > 0)
+        self.runs = self._runs(spans, lo, S, int(padding))
         self.p = p0.clone()
         self.m = torch.zeros_like(p0)
         self.g = torch.empty_like(p0)
@@ -507,6 +514,8 @@ class MuonShardStep:
         self.o = torch.zeros_like(self.u)
         at = lo - self.u_off
         self.u_shard, self.o_shard = self.u[at:at + S], self.o[at:at + S]
+        self.own_slot = slot is None
+        self.runs_p = [(self.p[a:b], self.o_shard[a:b]) for a, b in self.runs]
         scales = {(r, c): s for r, c, s in self.shapes}
         self.stacks = []
         for n, first, every, r, c in self._stacks(here):
@@ -546,6 +555,24 @@ class MuonShardStep:
                 k += n
         return out
 
+    @staticmethod
+    def _runs(spans, lo, S, padding):
+        """[begin, end) of the shard's elements that an update writes: (offset, length) in order of all
+        matrices of the flat buffer, with the padding behind them, cut to the shard at lo."""
+        out: list = []
+        for k, (o, n) in enumerate(spans):
+            # behind the last, the shard's end, where it is the shard of the last one's end
+            after = spans[k + 1][0] if k + 1 < len(spans) else lo + S if o + n > lo else o + n
+            end = after if o + n < after < o + n + padding else o + n
+            a, b = max(o, lo) - lo, min(end, lo + S) - lo
+            if a >= b:
+                continue
+            if out and out[-1][1] == a:
+                out[-1][1] = b
+            else:
+                out.append([a, b])
+        return [tuple(r) for r in out]
+
     @property
     def master(self) -> torch.Tensor:
         return self.p
@@ -581,7 +608,8 @@ class MuonShardStep:
         """Enqueue the third part, once all of u is there."""
         for u, o, scale in self.stacks:
             muon.zero_orthogonalize(u, out=o, scale=scale, workspace=self.orth_ws, stream=stream, **self.orth)
-        muon.zero_muon_update(self.p, self.o_shard, slot=self.slot, stats=self.stats, stream=stream, **self.hyper)
+        for (p, o), (a, b) in zip(self.runs_p, self.runs):
+            muon.zero_muon_update(p, o, slot=self.slot[a:b], stats=self.stats, stream=stream, **self.hyper)
 
     def read_stats(self, stream=None) -> B.zero_stats:
         st = stream or torch.cuda.current_stream()
@@ -625,4 +653,9 @@ class MuonShardStep:
             dst.copy_(sd[key])
         self.state = B.zero_train_state(t=sd["t"], n_skipped=sd["n_skipped"], loss_scale=sd["loss_scale"],
                                         min_loss_scale=sd["min_loss_scale"], dynamic=sd["dynamic"])
-        B.zero_gather_slot(self.p, self.S, self.slot)
+        if self.own_slot:
+            B.zero_gather_slot(self.p, self.S, self.slot)
+            return
+        slot = self.slot.view(torch.bfloat16)
+        for a, b in self.runs:
+            slot[a:b].copy_(self.p[a:b])
