@@ -108,3 +108,22 @@ def test_what_no_matrix_holds_is_left_alone(Z, given):
     assert torch.equal(again.slot.view(BF)[inside], want.to(BF)[inside])
     assert bool((again.slot[rest] == 9).all()) if given else torch.equal(again.slot.view(BF), again.master.to(BF))
     assert torch.equal(again.master, step.master) and torch.equal(again.m, step.m)
+
+
+def test_strides_of_a_stack(Z):
+    """Rows and matrices further apart than they need be; and what the documentation excludes,
+    matrices between another's rows, refused for x as for out."""
+    g = torch.Generator(device=dev()).manual_seed(2)
+    both = torch.randn(6, 40, 90, generator=g, device=dev())
+    x = both[::2, 4:30, 8:60]
+    want = Z.zero_orthogonalize(x.contiguous())
+    assert torch.equal(Z.zero_orthogonalize(x), want)
+    out = torch.zeros(6, 40, 90, dtype=BF, device=dev())
+    assert torch.equal(Z.zero_orthogonalize(x, out=out[1::2, :26, :52]), want)
+    assert bool((out[::2] == 0).all())
+    heads = torch.randn(26, 3 * 52, generator=g, device=dev()).view(26, 3, 52).transpose(0, 1)
+    for kw in (dict(x=heads), dict(x=x, out=torch.zeros(26, 3, 52, dtype=BF, device=dev()).transpose(0, 1))):
+        with pytest.raises(Z.ZeroError, match="batch stride"):
+            Z.zero_orthogonalize(**kw)
+    with pytest.raises(Z.ZeroError, match="column stride"):
+        Z.zero_orthogonalize(x.transpose(1, 2))

@@ -187,7 +187,8 @@ def _stack(fn: str, name: str, t: torch.Tensor, dtype, device: int):
 def zero_orthogonalize(x, *, out=None, steps: int = 5, coefficients=ZERO_MUON_COEFFICIENTS, eps: float = 1e-7,
                        scale: float = 1.0, workspace=None, stream=None):
     """scale times the nearly semi-orthogonal matrix of x [R, C], or of each matrix of a
-    stack [B, R, C] (bfloat16 or float32, rows and matrices at any stride): X = x / (|x| +
+    stack [B, R, C] (bfloat16 or float32; a row contiguous, rows at least C elements apart, and
+    matrices at least as far as one reaches, so that none lies within another): X = x / (|x| +
     eps), then ``steps`` times X = a X + (b A + c A A) X with A = X X^T. ``coefficients``:
     (a, b, c), or one such triple for each step; the steps' |a|, where above 1, may multiply to
     8192 (seven steps of the default ones). Returns ``out`` (bfloat16, x's shape; new
