@@ -230,9 +230,10 @@ int zero_dropout_grad(const zero_dropout_args* args, void* stream);
  * ZERO_NORM_RMS takes mean as 0 and leaves out sum(g) / N. s is rounded to its own type
  * before it is normed: the backward pass reads what the forward pass normed, and a call
  * with a residual gives what an addition and a call without one give. Sums and
- * statistics are fp32, the variance from the differences to the mean. A row of one
- * value with eps 0 has rstd = inf and, by the formula, NaN; an infinity or NaN in a row
- * makes that row's y NaN.
+ * statistics are fp32, the variance from the differences to the mean, and y from the mean
+ * before it is rounded to its place in stats (the gradient's h has that one: it is off by
+ * 2^-25 mean / sigma). A row of one value gives y = b, and with eps 0 rstd = inf and, by the
+ * formula, NaN; an infinity or NaN in a row makes that row's y NaN.
  */
 typedef enum { ZERO_NORM_LAYER = 0, ZERO_NORM_RMS = 1 } zero_norm_kind;
 

@@ -2,12 +2,16 @@
 //   forward   s = residual + x; y = (s - mean) rstd w + b
 //   gradient  h = (x - mean) rstd, g = dy w: dx = residual_grad + rstd (g - mean(g) - h mean(g h)),
 //             dw = [dw +] sum of dy h over the rows, db = [db +] sum of dy
+// The mean is taken in two parts, m from the sum of the differences to one of the row's elements
+// and delta from that of the differences to m: a row of one value has differences of exactly 0
+// however its mean would round, and where the mean is large beside sigma delta is what m lacks.
+// The variance is the mean of the squared differences to m, less delta^2.
 // Bound by HBM where rows are long: each matrix is read or written once. A row stays in
 // registers between its sums and its outputs, eight columns to a lane and 16 bytes to a load.
 // 8192 x 4096, bf16 rows added to an f32 stream, RMS: 77 us, 5.2 TB/s; back through it with the
 // stream's gradient in bf16 61 us, 5.5 TB/s, 4.8 of them the second launch. Rows of 768 in bf16
-// are bound by their instructions as much: 8192 of them forward 11.3 us, 4.5 TB/s, back 16.0 and
-// 3.2 (12.1 and 4 the two launches). Divisions, masks of columns that do not exist and 64-bit
+// are bound by their instructions as much: 8192 of them forward 11.6 to 12 us, 4.2 to 4.3 TB/s (0.3
+// of it the mean in two parts), back 16.0 and 3.2 (12.1 and 4 the two launches). Divisions, masks of columns that do not exist and 64-bit
 // products of addresses out of the loops were 3 of 19 us there, and of 45 at 2304 columns 7.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -166,6 +170,58 @@ __device__ __forceinline__ float row_sum(float v, float* part) {
     return v;
 }
 
+// Two sums at a time; `part` likewise, of pairs.
+template <int W>
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*part)[2]) {
+    a = wave_sum(a);
+    b = wave_sum(b);
+    if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            part[threadIdx.x >> 6][0] = a;
+            part[threadIdx.x >> 6][1] = b;
+        }
+        __syncthreads();
+        a = part[0][0];
+        b = part[0][1];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            a += part[w][0];
+            b += part[w][1];
+        }
+    }
+}
+// The mean of a row from the sums that its waves have of the differences to an element of theirs:
+// wave w has columns 512 (w + W i) .. + 511, i < C, that are below N.
+template <int W, int C>
+__device__ __forceinline__ float row_mean(float sum, float one, int N, float (*part)[2]) {
+    sum = wave_sum(sum);
+    if constexpr (W > 1) {
+        if ((threadIdx.x & 63) == 0) {
+            part[threadIdx.x >> 6][0] = sum;
+            part[threadIdx.x >> 6][1] = one;
+        }
+        __syncthreads();
+        sum = part[0][0];
+        one = part[0][1];
+#pragma unroll
+        for (int w = 1; w < W; ++w) {
+            int n = 0;
+#pragma unroll
+            for (int i = 0; i < C; ++i) {
+                const int left = N - 512 * (w + W * i);
+                n += left > 512 ? 512 : left > 0 ? left : 0;
+            }
+            sum += fmaf((float)n, part[w][1] - one, part[w][0]);
+        }
+    }
+    return one + sum / (float)N;
+}
+// rstd, from the mean of the squares of a row's differences to m and delta, their own mean.
+__device__ __forceinline__ float row_rstd(float square, float delta, float eps) {
+    const float var = fmaf(-delta, delta, square);
+    return 1.0f / sqrtf((var < 0.0f ? 0.0f : var) + eps);       // a NaN stays one
+}
+
 constexpr int kNormBlock = 256;
 
 // s of eight columns, rounded to its own type and stored, where there is a residual; x
@@ -184,7 +240,7 @@ __device__ __forceinline__ void sum8(float v[8], const NormDesc& d, int64_t row,
     store8<SF>(d.sum, row * d.ld_sum + j, v, n);
 }
 template <bool YF>
-__device__ __forceinline__ void norm8(const float v[8], const NormDesc& d, float mean, float rstd, int64_t row,
+__device__ __forceinline__ void norm8(const float v[8], const NormDesc& d, float m, float rstd, float shift, int64_t row,
                                       int64_t j, int n) {
     float w[8], b[8], y[8];
     weights8(w, d.w, j, n);
@@ -192,7 +248,7 @@ __device__ __forceinline__ void norm8(const float v[8], const NormDesc& d, float
     for (int k = 0; k < 8; ++k) b[k] = 0.0f;
     if (d.b) load8_bf(b, d.b + j, n);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = (v[k] - mean) * rstd * w[k] + b[k];
+    for (int k = 0; k < 8; ++k) y[k] = fmaf(v[k] - m, rstd, shift) * w[k] + b[k];
     store8<YF>(d.y, row * d.ld_y + j, y, n);
 }
 
@@ -202,7 +258,7 @@ __device__ __forceinline__ void norm8(const float v[8], const NormDesc& d, float
 template <bool XF, bool SF, bool YF, int W, int C>
 __global__ void __launch_bounds__(W > 4 ? 512 : kNormBlock) k_norm(const NormDesc d, int64_t stride) {
     constexpr int G = W == 1 ? 4 : 1;
-    __shared__ float part[2][2][W];
+    __shared__ float part[2][2][W][2];
     const int t = W == 1 ? threadIdx.x & 63 : threadIdx.x;
     int64_t row = (int64_t)blockIdx.x * G + (W == 1 ? threadIdx.x >> 6 : 0);
     if (row >= d.M) return;
@@ -231,7 +287,7 @@ __global__ void __launch_bounds__(W > 4 ? 512 : kNormBlock) k_norm(const NormDes
     int turn = 0;
 #pragma unroll 1
     for (;; turn ^= 1) {
-        float v[C][8], sum = 0.0f, sq = 0.0f, mean = 0.0f;
+        float v[C][8], sq = 0.0f, delta = 0.0f, m = 0.0f;
         Raw<SF> s[C];
 #pragma unroll
         for (int i = 0; i < C; ++i) {
@@ -250,34 +306,48 @@ __global__ void __launch_bounds__(W > 4 ? 512 : kNormBlock) k_norm(const NormDes
         if (d.res)
 #pragma unroll
             for (int i = 0; i < C; ++i) s[i].store(d.sum, row * d.ld_sum + j[i], n[i]);
-        if (!d.rms) {
+        // the differences of a chunk to `by`; of no column: zeros, and 0 to the sums
+        const auto less = [&](float to[8], int i, float by) {
+            const float b = n[i] > 0 ? by : 0.0f;
 #pragma unroll
-            for (int i = 0; i < C; ++i)
-#pragma unroll
-                for (int k = 0; k < 8; ++k) sum += v[i][k];
-            mean = row_sum<W>(sum, part[turn][0]) / (float)d.N;
-        }
-#pragma unroll
-        for (int i = 0; i < C; ++i) {
-            const float m = n[i] > 0 ? mean : 0.0f;         // of no column: zeros, and 0 to the sum
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] -= m;
+            for (int k = 0; k < 8; ++k) to[k] = v[i][k] - b;
             if (n[i] > 0 && n[i] < 8)
 #pragma unroll
                 for (int k = 1; k < 8; ++k)
-                    if (k >= n[i]) v[i][k] = 0.0f;
+                    if (k >= n[i]) to[k] = 0.0f;
+        };
+        if (!d.rms) {
+            const float one = lane_of(v[0][0], 0);
+            float sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) sq = fmaf(v[i][k], v[i][k], sq);
+            for (int i = 0; i < C; ++i) {
+                float e[8];
+                less(e, i, one);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += e[k];
+            }
+            m = row_mean<W, C>(sum, one, (int)d.N, part[turn][0]);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<W>(sq, part[turn][1]) / (float)d.N + d.eps);
+#pragma unroll
+        for (int i = 0; i < C; ++i) {
+            less(v[i], i, m);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sq = fmaf(v[i][k], v[i][k], sq);
+                delta += v[i][k];
+            }
+        }
+        row_sums<W>(sq, delta, part[turn][1]);
+        delta = d.rms ? 0.0f : delta / (float)d.N;
+        const float rstd = row_rstd(sq / (float)d.N, delta, d.eps), shift = d.rms ? 0.0f : -delta * rstd;
         if (d.stats && t == 0) {
-            d.stats[2 * row] = mean;
+            d.stats[2 * row] = m + delta;
             d.stats[2 * row + 1] = rstd;
         }
 #pragma unroll
         for (int i = 0; i < C; ++i) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[i][k] = v[i][k] * rstd * w[i].get(k) + b[i].get(k);
+            for (int k = 0; k < 8; ++k) v[i][k] = fmaf(v[i][k], rstd, shift) * w[i].get(k) + b[i].get(k);
             Raw<YF> y;
             y.set(v[i]);
             y.store(d.y, row * d.ld_y + j[i], n[i]);
@@ -290,37 +360,49 @@ __global__ void __launch_bounds__(W > 4 ? 512 : kNormBlock) k_norm(const NormDes
 // Rows of any length, read again for each sum (from the caches, up to some length).
 template <bool XF, bool SF, bool YF>
 __global__ void __launch_bounds__(kNormBlock) k_norm_long(const NormDesc d, int64_t first) {
-    __shared__ float part[2][4];
+    __shared__ float part[4];
+    __shared__ float parts[4][2];
     const int64_t row = first + blockIdx.x;
-    float v[8], sum = 0.0f, sq = 0.0f, mean = 0.0f;
+    float v[8], one[8], sum = 0.0f, sq = 0.0f, delta = 0.0f, m = 0.0f;
+    load8<XF>(one, d.x, row * d.ld_x, 1);
+    if (d.res) {
+        load8<SF>(v, d.res, row * d.ld_res, 1);
+        one[0] += v[0];
+        if constexpr (!SF) one[0] = bf_f(bf_one(one[0]));
+    }
+    __syncthreads();                    // sum may be written over x or the residual
     const auto again = [&](int64_t j, int n) {
         if (d.res) load8<SF>(v, d.sum, row * d.ld_sum + j, n);
         else load8<XF>(v, d.x, row * d.ld_x + j, n);
     };
     for (int64_t j = 8 * threadIdx.x; j < d.N; j += 8 * kNormBlock) {
-        sum8<XF, SF>(v, d, row, j, valid8(d.N, j));
+        const int n = valid8(d.N, j);
+        sum8<XF, SF>(v, d, row, j, n);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) sum += v[k];
+        for (int k = 0; k < 8; ++k) sum += k < n ? v[k] - one[0] : 0.0f;
     }
-    if (!d.rms) mean = row_sum<4>(sum, part[0]) / (float)d.N;
+    if (!d.rms) m = one[0] + row_sum<4>(sum, part) / (float)d.N;
     for (int64_t j = 8 * threadIdx.x; j < d.N; j += 8 * kNormBlock) {
         const int n = valid8(d.N, j);
         again(j, n);
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float e = k < n ? v[k] - mean : 0.0f;
+            const float e = k < n ? v[k] - m : 0.0f;
             sq = fmaf(e, e, sq);
+            delta += e;
         }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<4>(sq, part[1]) / (float)d.N + d.eps);
+    row_sums<4>(sq, delta, parts);
+    delta = d.rms ? 0.0f : delta / (float)d.N;
+    const float rstd = row_rstd(sq / (float)d.N, delta, d.eps), shift = d.rms ? 0.0f : -delta * rstd;
     if (d.stats && threadIdx.x == 0) {
-        d.stats[2 * row] = mean;
+        d.stats[2 * row] = m + delta;
         d.stats[2 * row + 1] = rstd;
     }
     for (int64_t j = 8 * threadIdx.x; j < d.N; j += 8 * kNormBlock) {
         const int n = valid8(d.N, j);
         again(j, n);
-        norm8<YF>(v, d, mean, rstd, row, j, n);
+        norm8<YF>(v, d, m, rstd, shift, row, j, n);
     }
 }
 
