@@ -233,7 +233,9 @@ int zero_dropout_grad(const zero_dropout_args* args, void* stream);
  * statistics are fp32, the variance from the differences to the mean, and y from the mean
  * before it is rounded to its place in stats (the gradient's h has that one: it is off by
  * 2^-25 mean / sigma). A row of one value gives y = b, and with eps 0 rstd = inf and, by the
- * formula, NaN; an infinity or NaN in a row makes that row's y NaN.
+ * formula, NaN. A NaN in a row makes that row's y NaN, an infinity too, except that in an
+ * RMS norm, whose rstd is then 0, it does so in its own place and leaves b in the others; so
+ * does (without the NaN) a row whose squares pass fp32.
  */
 typedef enum { ZERO_NORM_LAYER = 0, ZERO_NORM_RMS = 1 } zero_norm_kind;
 
@@ -264,7 +266,7 @@ typedef struct {
 
 /*
  * Errors of both calls: ZERO_E_INVAL (NULL args or matrix, an unknown kind or type, eps
- * negative or not finite, a residual without sum or a sum without residual, overlap),
+ * outside [0, 1e30] or NaN, a residual without sum or a sum without residual, overlap),
  * ZERO_E_ALIGN (a pointer not aligned to its element, a workspace not to 16 bytes),
  * ZERO_E_RANGE (M outside [0, 2^31 - 1], N outside [0, 2^24], an ld below its columns or
  * above 2^40, a workspace below zero_norm_workspace_bytes), ZERO_E_HIP.

@@ -78,3 +78,28 @@ def test_long_rows_in_place(Z, over):
     a, b = x.clone(), r.clone()
     got = Z.zero_norm_forward(a, residual=b, sum=a if over == "x" else b, stats=True)
     assert all(torch.equal(p, q) for p, q in zip(got, want))
+
+
+@pytest.mark.parametrize("N", [40, 3001, 20011])
+def test_infinities_by_the_formula(Z, N):
+    """Layer: the mean is infinite and all differences, and y, NaN. RMS: 1 / sigma is 0, the
+    infinity's own place 0 times infinity, the others the bias."""
+    g = torch.Generator(device=dev()).manual_seed(N)
+    x = torch.randn(4, N, generator=g, device=dev())
+    b = torch.randn(N, generator=g, device=dev()).to(BF)
+    x[1, N // 3], x[2, 5], x[3, 2] = float("inf"), float("-inf"), float("nan")
+    for xt in (x, x.to(BF)):
+        y = Z.zero_norm_forward(xt, None, b, dtype=F32)
+        assert bool(y[1:].isnan().all()) and bool(y[0].isfinite().all())
+        y, stats = Z.zero_norm_forward(xt, None, b, kind=Z.ZERO_NORM_RMS, stats=True, dtype=F32)
+        for row, at in ((1, N // 3), (2, 5)):
+            others = torch.arange(N, device=dev()) != at
+            assert bool(y[row, at].isnan()) and torch.equal(y[row][others], b.float()[others])
+            assert float(stats[row, 1]) == 0.0 and float(stats[row, 0]) == 0.0
+        assert bool(y[3].isnan().all()) and bool(y[0].isfinite().all())
+    # squares beyond fp32
+    y = Z.zero_norm_forward(torch.full((2, N), 1e30, device=dev()), None, b, kind=Z.ZERO_NORM_RMS, dtype=F32)
+    assert torch.equal(y, b.float()[None].expand_as(y))
+    for eps in (-1e-9, 2e30, float("inf"), float("nan")):
+        with pytest.raises(Z.ZeroError, match="eps"):
+            Z.zero_norm_forward(x, eps=eps)
