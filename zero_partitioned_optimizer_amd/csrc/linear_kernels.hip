@@ -12,6 +12,7 @@
 #include <type_traits>
 
 #include "layer_device.h"
+#include "tile_device.h"
 
 namespace zk {
 
@@ -34,18 +35,6 @@ struct ProductArgs {
     float* sums;                    // [sum_rows, ld_sums]
     int64_t join_blocks;            // k_join: workgroups on the product, before those on the sums
 };
-
-// Staged tiles hold eight-element chunks (16 bytes), permuted within a row so that
-// the lanes that read together meet different banks.
-//   outer rows:   [rows][kBR], chunk c of row o at c ^ (o & 7): the 8 lanes of a
-//                 16-byte read hold 8 rows at one c.
-//   reduced rows: [kBR][cols], chunk c of row r at c ^ perm(r): a transposing read
-//                 takes 4 rows x 32 bytes per 16 lanes, and two such groups 8 rows apart
-//                 (of 64 columns, even and odd rows have different banks as it is).
-template <int COLS>
-__device__ __forceinline__ int perm_reduced(int r) {
-    return COLS >= 128 ? (r & 3) << 1 | (r >> 3 & 1) << 3 : (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1;
-}
 
 // Eight elements (n of them valid, the rest 0) from any element-aligned address.
 __device__ __forceinline__ v4u chunk_load(const uint16_t* p, int n) {
@@ -160,43 +149,8 @@ __device__ __forceinline__ void stage_tail(uint16_t* lds, const uint16_t* src, i
         put_chunk<ROWS, T>(lds, id, tile_chunk<ROWS, T>(id, src, ld, o0, O, r0, r1));
 }
 
-typedef __attribute__((address_space(3))) const uint16_t lds_u16;
-typedef __attribute__((address_space(3))) const v8bf lds_v8bf;
-typedef __attribute__((address_space(3))) v4bf lds_v4bf;
-__device__ __forceinline__ uint32_t lds_address(const uint16_t* p) {
-    return (uint32_t)reinterpret_cast<uintptr_t>((lds_u16*)p);
-}
-
-// The matrix instruction's operands from a staged tile: for block i, lane l holds
-// outer index o0 + 16 i + (l & 15) and reduction elements 32 s + 8 (l >> 4) .. + 7.
-// o0 is a multiple of the outer indices that the wave's blocks cover, a power of
-// two, so one byte offset per lane serves all blocks: a constant is added to it,
-// or, where a block's chunks lie under the permutation, exchanged into it.
 template <int ROWS, bool T>
-struct Fragments {
-    uint32_t at;
-    __device__ __forceinline__ explicit Fragments(int o0) {
-        const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-        if constexpr (T) {
-            const int r = 8 * g + (i >> 2), chunk = (o0 >> 3) + ((i & 3) >> 1);
-            at = 2 * (r * ROWS + 8 * (chunk ^ perm_reduced<ROWS>(r)) + 4 * (i & 1));
-        } else {
-            const int o = o0 + i;
-            at = 2 * (o * kBR + 8 * (g ^ (o & 7)));
-        }
-    }
-    __device__ __forceinline__ v8bf get(uint32_t tile, int i, int s) const {
-        if constexpr (T) {
-            // rows 32 further on have the same permutation
-            const uint32_t p = tile + (at ^ (32u * i)) + 2 * 32 * ROWS * s;
-            const v4bf lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)p);
-            const v4bf hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((lds_v4bf*)(p + 2 * 4 * ROWS));
-            return __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7);
-        } else {
-            return *(lds_v8bf*)(tile + (at ^ (64u * s)) + 2 * 16 * kBR * i);
-        }
-    }
-};
+using Fragments = TileFragments<ROWS, T, kBR, v8bf>;
 
 // The epilogue of eight consecutive columns q .. of row p; n of them exist. What it
 // reads beside the sums is asked for in one part (EpilogueIn::load), used in another,
@@ -280,8 +234,6 @@ __device__ __forceinline__ void epilogue8(const ProductDesc& d, uint64_t off, in
     else store8_bf(static_cast<uint16_t*>(d.out) + p * d.ld_out + q, v, n);
 }
 
-typedef int v4i __attribute__((ext_vector_type(4)));
-
 // N loads of 16 bytes a lane from the buffer's bytes `at` to LDS, lane l of the wave to
 // byte 16 l behind `to` (the same in all lanes), each load STEP bytes further on. Written
 // in assembly because the compiler, which sees in its own builtin a store to LDS of
@@ -326,24 +278,12 @@ __device__ __forceinline__ void lds_loads(v4i rsrc, const uint32_t* at, uint32_t
         if constexpr (N > 4) lds_loads<N - 4, STEP>(rsrc, at + 4, to + 4 * STEP);
     }
 }
-// Until at most N of this wave's loads are under way.
-template <int N>
-__device__ __forceinline__ void loads_landed() {
-    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-// All waves have come here and their LDS reads and writes are done.
-__device__ __forceinline__ void meet_waves() {
-    asm volatile("" : : : "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0), where the compiler counts it too
-    asm volatile("s_barrier" : : : "memory");
-}
 
 // One operand's tiles from memory straight into LDS: 16 bytes a lane, lane l of a
 // wave to byte 16 l behind the wave's LDS address, so the chunk permutation is
 // applied to the address that a lane reads. Rows and chunks outside the operand
 // read its last ones instead: they only reach outputs that do not exist. Used
 // where rows start on 16 bytes and a whole tile of the reduction is left.
-constexpr int kAllRecords = 0x7FFFFFFF;     // more than a tile's rows reach
 template <int ROWS, bool T, int THREADS, int PARTS>
 struct Direct {
     static constexpr int kLoads = ROWS * kBR / 8 / THREADS;
@@ -372,8 +312,7 @@ struct Direct {
         step = (T ? kBR * ld : kBR) * 2;
     }
     // Part h of the tile at `from` (base, or steps away from it) to LDS byte address
-    // `tile`; `wave` is the same in all lanes. With `records` 0 the buffer's range check
-    // stops the loads (which still count as loads).
+    // `tile`; `wave` is the same in all lanes. `records`: kAllRecords, or 0 for no load.
     __device__ __forceinline__ void issue(int h, const char* from, uint32_t tile, int wave, int records) const {
         lds_loads<kLoads, 16 * THREADS>(descriptor(from, records), at[h], tile + 16 * 64 * wave);
     }
@@ -384,11 +323,6 @@ struct Direct {
 #pragma unroll
         for (int h = 0; h < PARTS; ++h) each[h] = at[h][0];
         lds_loads<PARTS, 16 * THREADS>(descriptor(from, records), each, tile + 16 * 64 * wave);
-    }
-    static __device__ __forceinline__ v4i descriptor(const char* from, int records) {
-        const uintptr_t b = reinterpret_cast<uintptr_t>(from);
-        return v4i{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
-                   __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), records, 0x00020000};
     }
 };
 

@@ -31,12 +31,11 @@
 #include "layer_device.h"
 #include "muon_internal.h"
 #include "orth_plan.h"
+#include "tile_device.h"
 
 namespace zk {
 
 typedef _Float16 h8 __attribute__((ext_vector_type(8)));
-typedef short s4 __attribute__((ext_vector_type(4)));
-typedef int v4i __attribute__((ext_vector_type(4)));
 
 constexpr float kScale = 1024.0f, kScaleX = 4096.0f;
 
@@ -70,23 +69,6 @@ struct OrthArgs {
 // tiles in LDS
 // ---------------------------------------------------------------------------
 
-// A staged tile has 64 or 128 outer indices and kBR reduction elements in chunks of eight
-// (16 bytes), permuted so that lanes that read together meet different banks: with the outer
-// index in rows chunk c of row o lies at c ^ (o & 7); with the reduction in rows (T), chunk c
-// of row r at c ^ perm(r), as a transposing read takes 4 rows x 32 bytes per 16 lanes, two
-// such groups 8 rows apart (of 64 columns, even and odd rows have different banks as it is).
-template <int COLS>
-__device__ __forceinline__ int perm_rows(int r) {
-    return COLS >= 128 ? (r & 3) << 1 | (r >> 3 & 1) << 3 : (r >> 1 & 1) << 2 | (r >> 3 & 1) << 1;
-}
-
-typedef __attribute__((address_space(3))) const _Float16 lds_f16;
-typedef __attribute__((address_space(3))) const h8 lds_h8;
-typedef __attribute__((address_space(3))) s4 lds_s4;
-__device__ __forceinline__ uint32_t lds_address(const _Float16* p) {
-    return (uint32_t)reinterpret_cast<uintptr_t>((lds_f16*)p);
-}
-
 // Two loads of 16 bytes a lane from the buffer's bytes at0, at1 to LDS, lane l of the wave
 // to byte 16 l behind `to` and `to` + STEP. In assembly because the compiler, which sees in
 // its own builtin a store to LDS of unknown extent, waits for it before the next LDS read of
@@ -103,20 +85,9 @@ __device__ __forceinline__ void lds_loads(v4i rsrc, uint32_t at0, uint32_t at1, 
                  : "s"(to), "s"(rsrc), "n"(STEP), "v"(at0), "v"(at1)
                  : "memory", "m0", "scc");
 }
-// Until at most N of this wave's loads are under way.
-template <int N>
-__device__ __forceinline__ void loads_landed() {
-    asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
-// All waves have come here and their LDS reads and writes are done.
-__device__ __forceinline__ void meet_waves() {
-    asm volatile("" : : : "memory");
-    __builtin_amdgcn_s_waitcnt(0xC07F);         // lgkmcnt(0), where the compiler counts it too
-    asm volatile("s_barrier" : : : "memory");
-}
 
 // PARTS runs of ROWS outer indices from memory to LDS, a thread's chunks at byte offsets
-// from at(turn) that every turn shares; THREADS consecutive threads load a run. A run that
+// from turn(k) that every turn shares; THREADS consecutive threads load a run. A run that
 // lies outside the operand reads its last one instead, which reaches no output. Turns take
 // a reduction tile's three terms one after another, operand A as hi, hi, lo and operand B (LOW
 // 1) as hi, lo, hi: what a turn reads again is still in the caches.
@@ -135,7 +106,7 @@ struct Loader {
             for (int i = 0; i < kLoads; ++i) {
                 const int id = threadIdx.x % THREADS + i * THREADS;
                 if constexpr (T) {
-                    const int r = id / (ROWS / 8), c = 8 * ((id % (ROWS / 8)) ^ perm_rows<ROWS>(r));
+                    const int r = id / (ROWS / 8), c = 8 * ((id % (ROWS / 8)) ^ perm_reduced<ROWS>(r));
                     at[h][i] = (uint32_t)((r * ld + run + c) * 2);
                 } else {
                     const int o = id / (kBR / 8), c = 8 * ((id % (kBR / 8)) ^ (o & 7));
@@ -152,51 +123,21 @@ struct Loader {
         return base + tile * step + (term == LOW ? low : 0);
     }
     // Run h of what lies at `from` to LDS byte address `tile`; `wave` (of those that load the
-    // run) is the same in all lanes. With `records` 0 the buffer's range check stops the
-    // loads (which still count).
+    // run) is the same in all lanes. `records`: kAllRecords, or 0 for no load.
     __device__ __forceinline__ void issue(int h, const char* from, uint32_t tile, int wave, int records) const {
-        const uintptr_t b = reinterpret_cast<uintptr_t>(from);
-        const v4i rsrc = {__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
-                          __builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32)), records, 0x00020000};
+        const v4i rsrc = descriptor(from, records);
 #pragma unroll
         for (int i = 0; i < kLoads; i += 2)
             lds_loads<16 * THREADS>(rsrc, at[h][i], at[h][i + 1], tile + 16 * 64 * wave + 16 * THREADS * i);
     }
 };
-constexpr int kAllRecords = 0x7FFFFFFF;
 template <int ROWS, bool T, int THREADS, int PARTS>
 using LoaderA = Loader<ROWS, T, THREADS, PARTS, 2>;
 template <int ROWS, bool T, int THREADS, int PARTS>
 using LoaderB = Loader<ROWS, T, THREADS, PARTS, 1>;
 
-// The matrix instruction's operands from a tile of ROWS outer indices: for block i, lane l
-// holds outer index o0 + 16 i + (l & 15) and reduction elements 32 s + 8 (l >> 4) .. + 7. o0 is a
-// multiple of what the wave's blocks cover.
 template <int ROWS, bool T>
-struct Fragments {
-    uint32_t at;
-    __device__ __forceinline__ explicit Fragments(int o0) {
-        const int lane = threadIdx.x & 63, i = lane & 15, g = lane >> 4;
-        if constexpr (T) {
-            const int r = 8 * g + (i >> 2), chunk = (o0 >> 3) + ((i & 3) >> 1);
-            at = 2 * (r * ROWS + 8 * (chunk ^ perm_rows<ROWS>(r)) + 4 * (i & 1));
-        } else {
-            const int o = o0 + i;
-            at = 2 * (o * kBR + 8 * (g ^ (o & 7)));
-        }
-    }
-    __device__ __forceinline__ h8 get(uint32_t tile, int i, int s) const {
-        if constexpr (T) {
-            // rows 32 further on have the same permutation
-            const uint32_t p = tile + (at ^ (32u * i)) + 2 * 32 * ROWS * s;
-            const s4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)p);
-            const s4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(p + 2 * 4 * ROWS));
-            return __builtin_bit_cast(h8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-        } else {
-            return *(lds_h8*)(tile + (at ^ (64u * s)) + 2 * 16 * kBR * i);
-        }
-    }
-};
+using Fragments = TileFragments<ROWS, T, kBR, h8>;
 
 // Workgroup `id` of `all` goes to XCD id % 8, each with an L2 of its own: each XCD gets a run
 // of consecutive tiles.
