@@ -87,8 +87,7 @@ int zero_muon_update(const zero_muon_update_args* args, void* stream);
  * those below 1 in magnitude left out, multiply to more than 2^13 are refused (with the default
  * coefficients more than seven): a matrix of low rank would come out of them, in 32 bits, wrong
  * in the second digit. X's elements must stay below 16 and those of A and b A + c A A off their
- * diagonals below 64, as they do for coefficients that keep the singular values below 3;
- * beyond, every element of o that the formula makes of such an element is NaN: all of its matrix,
+ * diagonals below 64 (with the default coefficients none passes 3); beyond, every element of o that the formula makes of such an element is NaN: all of its matrix,
  * but for the rows (of a matrix taller than wide: columns) that an element of the last step's
  * b A + c A A does not belong to. A matrix of zeros gives zeros. A matrix that holds an infinity
  * or a NaN gives NaN in all its elements, and does not reach the others. The sum of squares
