@@ -27,10 +27,10 @@ def test_replicas_of_another_type_are_refused(Z):
             step.step([bad])
         assert step.t == 0 and bool((step.m == 0).all())
     # bf16 and its bit patterns are the same
-    bits = [new(Z, grad=Z.ZERO_BF16) for _ in range(2)]
-    bits[0].step([t.bfloat16()])
-    bits[1].step([t.bfloat16().view(torch.int16)])
-    assert torch.equal(bits[0].master, bits[1].master) and bits[0].t == 1
+    bits = [new(Z, grad=Z.ZERO_BF16) for _ in range(3)]
+    for step, as_type in zip(bits, (BF, torch.int16, torch.uint16)):
+        step.step([t.bfloat16().view(as_type)])
+        assert torch.equal(step.master, bits[0].master) and step.t == 1
 
 
 BAD = [dict(lr=-0.1), dict(lr=float("nan")), dict(weight_decay=float("inf")), dict(mu=1.0), dict(steps=0), dict(steps=8),

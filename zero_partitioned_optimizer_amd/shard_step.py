@@ -589,8 +589,8 @@ class MuonShardStep:
         """Enqueue the first part: the averaged gradient and its record."""
         if len(replicas) != self.N:
             raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: {len(replicas)} replicas, not {self.N}")
-        # bf16 also as its bit patterns, as in a slot
-        types = (torch.float32,) if self.grad_dtype == B.ZERO_F32 else (torch.bfloat16, torch.int16)
+        # bf16 also as its bit patterns
+        types = (torch.float32,) if self.grad_dtype == B.ZERO_F32 else (torch.bfloat16, torch.int16, torch.uint16)
         for r in replicas:
             if r.device != self.p.device or not r.is_contiguous() or r.numel() < self.S or r.dtype not in types:
                 raise B.ZeroError(B.ZERO_E_INVAL, f"MuonShardStep: a replica of {r.numel()} elements, {r.dtype} on "
