@@ -54,12 +54,14 @@ inline OrthPlan plan_of(int64_t n, int64_t P, int64_t Q, int64_t turns, bool sym
         }
     };
     // us for a turn and for a tile's start and end, in a round of the chip, as measured with 1 to 2,752
-    // tiles of 64 to 5,632 columns and 6 to 516 turns; of 45 such products the estimate took the
-    // fastest kind for 44 and one 1% slower for the last. A wide tile's turn takes 1.45 in a round of
+    // tiles of 64 to 5,632 columns and 6 to 516 turns; of 54 such products the estimate took the
+    // fastest kind for 48 and ones 1 to 6% slower for the others. A wide tile's turn takes 1.45 in a round of
     // 256 and 1.1 with half of the compute units idle (128 tiles 1.06 to 1.18, 180 1.21, 216 1.32).
     const int64_t rest = mid % 512;
     offer(kTwo, 0, mid / 512 * (0.9 * turns + 9) + (rest == 0 ? 0 : rest <= 256 ? 0.65 * turns + 8.5 : 0.9 * turns + 9));
     offer(kFew, 0, over(few, 256) * (0.185 * turns + 3.4));
+    // a compute unit to each: at 171 to 252 tiles 15 to 31% faster than two a unit, at 273 to 960 from
+    // 2% faster to 24% slower
     if (mid <= 256) offer(kMid, 0, 0.49 * turns + 8.5);
     const int64_t left = wide % kSplit;
     const double ends = sym ? 12 : 18, rounds = wide / 256 * (1.45 * turns + ends);
