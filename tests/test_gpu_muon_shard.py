@@ -127,3 +127,14 @@ def test_strides_of_a_stack(Z):
             Z.zero_orthogonalize(**kw)
     with pytest.raises(Z.ZeroError, match="column stride"):
         Z.zero_orthogonalize(x.transpose(1, 2))
+
+
+def test_a_shard_without_matrices(Z):
+    """Its matrices lie in other shards: it folds, counts and agrees as they do, and writes nothing."""
+    step = new(Z, 96, matrices=[(0, 8, 8), (4000, 8, 8)], shard_off=200, weight_decay=0.1)
+    was, slot = step.master.clone(), step.slot.clone()
+    st, verdict = step.step([torch.ones(96, device=dev())])
+    assert verdict == Z.ZERO_COMMIT and step.t == 1 and st.sumsq == 96.0
+    assert step.runs == [] and torch.equal(step.master, was) and torch.equal(step.slot, slot)
+    st, verdict = step.step([torch.full((96,), float("inf"), device=dev())])
+    assert verdict == Z.ZERO_SKIP and step.t == 1

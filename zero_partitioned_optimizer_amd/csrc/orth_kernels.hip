@@ -16,8 +16,8 @@
 // nearly orthogonal and then most of them, is kept beside in fp32 and meets X in fp32.
 // What that leaves, against the formula in 64 bits and before o is rounded (which is 1.7e-3 of
 // the norm), on a CPU model of these roundings: 1e-6 for normal numbers, 1e-5 for rank 32 to
-// 66, 2e-4 for rank 1, each up to 2.4 times what operations in fp32 leave. Noise that
-// doubles with each a is why the product of the a's is bounded.
+// 66, 2e-4 for rank 1, each up to 2.4 times what operations in fp32 leave. As it grows with
+// each a, the product of the a's is bounded.
 // fp16 holds A and b A + c A A times 1024 and X times 4096, of which a 4096 x 11008 one starts
 // with elements of 1.5e-4; with the default coefficients no element of them passes 3. Below
 // 6e-5 fp16's numbers are 6e-8 apart, so lo is known to 1.5e-11 of X's norm and 6e-11 of A's at
@@ -25,8 +25,6 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
-
-#include <initializer_list>
 
 #include "layer_device.h"
 #include "muon_internal.h"
